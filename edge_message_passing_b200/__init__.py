@@ -26,6 +26,8 @@ SYMBOLS = (
     "emp_set_wait_limit", "emp_wait_selftest", "emp_tf32_split_selftest", "emp_tf32_mma_rate", "mp_model_radial_tables", "mp_radial_hidden",
     "mp_weight_grad_workspace_bytes", "mp_energy_weight_grad", "nl_refresh",
     "mp_sharded_workspace_bytes", "mp_energy_forces_sharded",
+    "mp_rms_norm", "mp_rms_norm_grad_workspace_bytes", "mp_rms_norm_grad",
+    "mp_dense_workspace_bytes", "mp_dense", "mp_dense_grad_workspace_bytes", "mp_dense_grad",
 )
 
 # int (*)(float* buf, size_t n, cudaStream_t stream, void* ctx): the sum over ranks, in place
@@ -53,6 +55,31 @@ class SpecC(ctypes.Structure):
                 ("readout_hidden", ctypes.c_int32), ("gated", ctypes.c_int32),
                 ("pair_radial", ctypes.c_int32), ("cohort_edges", ctypes.c_int32),
                 ("cutoff", ctypes.c_float), ("env_p", ctypes.c_int32), ("avg_degree", ctypes.c_float)]
+
+
+def _fields(text: str):
+    kinds = {"i64": ctypes.c_int64, "i32": ctypes.c_int32, "f32": ctypes.c_float, "ptr": ctypes.c_void_p}
+    return [(name, kinds[kind]) for kind, *names in (line.split() for line in text.split(";")) for name in names]
+
+
+class RmsNormC(ctypes.Structure):
+    _fields_ = _fields("i64 rows; i32 cols dtype y_dtype degrees; f32 eps; ptr x; i64 ldx; ptr residual; i64 ldr; "
+                       "ptr weight y; i64 ldy; ptr scale s; i64 lds")
+
+
+class RmsNormGradC(ctypes.Structure):
+    _fields_ = _fields("i64 rows; i32 cols dtype degrees; f32 eps; ptr g; i64 ldg; ptr s; i64 lds; ptr g_s; i64 ldgs; "
+                       "ptr weight g_x; i64 ldgx; ptr g_weight")
+
+
+class DenseC(ctypes.Structure):
+    _fields_ = _fields("i64 rows; i32 fan_in fan_out dtype y_dtype activation; ptr x; i64 ldx; ptr x_scale weight; "
+                       "i64 ldw; ptr w_scale bias residual; i64 ldr; ptr y; i64 ldy; ptr z; i64 ldz")
+
+
+class DenseGradC(ctypes.Structure):
+    _fields_ = _fields("i64 rows; i32 fan_in fan_out dtype activation; ptr g; i64 ldg; ptr z; i64 ldz; ptr x; i64 ldx; "
+                       "ptr weight; i64 ldw; ptr g_x; i64 ldgx; ptr g_weight g_bias")
 
 
 _lib_handle = None
@@ -130,6 +157,14 @@ def lib() -> ctypes.CDLL:
         L.mp_radial_hidden.argtypes = [vp, i32, i32, i64, vp, vp, vp, vp, vp, vp, sz, vp]
         L.emp_tf32_mma_rate.restype = ctypes.c_int
         L.emp_tf32_mma_rate.argtypes = [i32, vp, ctypes.POINTER(ctypes.c_double)]
+        for name, args in (("mp_rms_norm", RmsNormC), ("mp_rms_norm_grad", RmsNormGradC), ("mp_dense", DenseC),
+                           ("mp_dense_grad", DenseGradC)):
+            ws = [] if name == "mp_rms_norm" else [vp, sz]
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name).argtypes = [ctypes.POINTER(args), *ws, vp]
+            if ws:
+                getattr(L, name + "_workspace_bytes").restype = sz
+                getattr(L, name + "_workspace_bytes").argtypes = [ctypes.POINTER(args)]
         _lib_handle = L
     return _lib_handle
 
@@ -580,3 +615,205 @@ def mp_radial_chain(chain: Chain, x, g_kc=None, g_y0=None, out=None):
     _check(lib().mp_radial_chain(chain.handle, E, _ptr(x), _ptr(kc), _ptr(y0), _ptr(g_kc), _ptr(g_y0), _ptr(gx),
                                  _stream()), "mp_radial_chain")
     return kc, y0, gx
+
+
+# ------------------------------------------------------------------ row-wise operators
+_ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
+
+
+def _dtype_code(t, what: str, e4m3: bool = False) -> int:
+    torch = _torch()
+    codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    if e4m3:
+        codes[torch.float8_e4m3fn] = 3
+    if t not in codes:
+        raise EmpError(f"{what}: type {t} is not supported")
+    return codes[t]
+
+
+def _on(device, dtype, **tensors):
+    """Every tensor given is on `device` and of `dtype`."""
+    for name, t in tensors.items():
+        if t is not None and (t.device != device or t.dtype != dtype):
+            raise EmpError(f"{name} must be a {dtype} tensor on {device}, not {t.dtype} on {t.device}")
+
+
+def _as_rows(t, rows: int, cols: int):
+    """t seen as [rows, cols] with contiguous elements in a row (copied if its strides do not allow it),
+    and its row pitch."""
+    t = t.reshape(rows, cols)
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        t = t.contiguous()
+    return t, (t.stride(0) if rows > 1 else cols)
+
+
+def _vector(t, n: int, name: str):
+    if t is None:
+        return None
+    if tuple(t.shape) != (n,):
+        raise EmpError(f"{name} must have the shape ({n},), not {tuple(t.shape)}")
+    return t.contiguous()
+
+
+def _like(t, shape, name: str):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise EmpError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _call(name: str, args, device):
+    """Call an entry point on the tensors' device and that device's current stream; its workspace is
+    its own (allocated on that stream), so calls on two streams or in two captured graphs share nothing."""
+    torch = _torch()
+    fn = getattr(lib(), name)
+    with torch.cuda.device(device):
+        stream = torch.cuda.current_stream().cuda_stream
+        if name == "mp_rms_norm":
+            _check(fn(ctypes.byref(args), stream), name)
+            return
+        nbytes = getattr(lib(), name + "_workspace_bytes")(ctypes.byref(args))
+        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+        _check(fn(ctypes.byref(args), _ptr(ws), nbytes, stream), name)
+
+
+def _norm_rows(x, weight, what: str):
+    """(rows, cols, degrees): rows are x's last dimension, or, with a weight [4, C], an atom's 16 C features
+    (x [..., 16, C] or [..., 16 C])."""
+    if not x.is_cuda or x.dim() < 1:
+        raise EmpError(f"{what} must be a CUDA tensor of rows")
+    cols, degrees = x.shape[-1], 0
+    if weight is not None and weight.dim() == 2:
+        C = weight.shape[1]
+        if weight.shape[0] != 4 or not (cols == 16 * C or (x.dim() >= 2 and tuple(x.shape[-2:]) == (16, C))):
+            raise EmpError(f"weight [4, C] needs {what} [..., 16, C] or [..., 16 C], not {tuple(x.shape)}")
+        cols, degrees = 16 * C, 1
+    elif weight is not None and tuple(weight.shape) != (cols,):
+        raise EmpError(f"weight must have the shape ({cols},) or (4, C), not {tuple(weight.shape)}")
+    if cols == 0:
+        raise EmpError(f"{what} has rows without elements")
+    return x.numel() // cols, cols, degrees
+
+
+def mp_rms_norm(x, weight=None, residual=None, eps: float = 1e-6, quantize: bool = False):
+    """Root-mean-square norm of rows with the residual's addition (see include/emp.h):
+    s = x + residual, y = s / sqrt(mean(s^2) + eps) * weight.
+
+    x, residual: float32, bfloat16 or float16 of one shape; weight: None, [D] for rows of D (the last
+    dimension), or [4, C] for node features [N, 16, C] (or rows of 16 C), one weight per degree and channel.
+    Returns (y, s), or with quantize (y in float8_e4m3fn, its scale per row (float32), s); s is x itself
+    without a residual.  No autograd: mp_rms_norm_grad is the gradient."""
+    torch = _torch()
+    rows, cols, degrees = _norm_rows(x, weight, "x")
+    code = _dtype_code(x.dtype, "x")
+    _on(x.device, x.dtype, weight=weight, residual=residual)
+    _like(residual, x.shape, "residual")
+    xr, ldx = _as_rows(x, rows, cols)
+    rr, ldr = (None, 0) if residual is None else _as_rows(residual, rows, cols)
+    w = None if weight is None else weight.contiguous()
+    y = torch.empty(x.shape, dtype=torch.float8_e4m3fn if quantize else x.dtype, device=x.device)
+    scale = torch.empty(rows, dtype=torch.float32, device=x.device) if quantize else None
+    s = x if residual is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    a = RmsNormC(rows, cols, code, 3 if quantize else code, degrees, float(eps), _ptr(xr), ldx, _ptr(rr), ldr, _ptr(w),
+                 _ptr(y), cols, _ptr(scale), None if residual is None else _ptr(s), cols)
+    _call("mp_rms_norm", a, x.device)
+    if not quantize:
+        return y, s
+    return y, scale.view(x.shape[:-2] if degrees and x.shape[-1] != cols else x.shape[:-1]), s
+
+
+def mp_rms_norm_grad(g, s, weight=None, g_s=None, eps: float = 1e-6):
+    """Gradient of mp_rms_norm: (g_x, g_weight) from g = dE/dy, the s it returned, and g_s = dE/ds of the
+    other uses of s (or None).  g_x is dE/dx and dE/dresidual; g_weight is None without a weight."""
+    torch = _torch()
+    rows, cols, degrees = _norm_rows(s, weight, "s")
+    code = _dtype_code(s.dtype, "s")
+    _on(s.device, s.dtype, weight=weight, g=g, g_s=g_s)
+    _like(g, s.shape, "g")
+    _like(g_s, s.shape, "g_s")
+    sr, lds = _as_rows(s, rows, cols)
+    gr, ldg = _as_rows(g, rows, cols)
+    tr, ldt = (None, 0) if g_s is None else _as_rows(g_s, rows, cols)
+    w = None if weight is None else weight.contiguous()
+    g_x = torch.empty(s.shape, dtype=s.dtype, device=s.device)
+    g_w = None if weight is None else torch.empty(weight.shape, dtype=s.dtype, device=s.device)
+    a = RmsNormGradC(rows, cols, code, degrees, float(eps), _ptr(gr), ldg, _ptr(sr), lds, _ptr(tr), ldt, _ptr(w),
+                     _ptr(g_x), cols, _ptr(g_w))
+    _call("mp_rms_norm_grad", a, s.device)
+    return g_x, g_w
+
+
+def _dense_shapes(x, weight, activation):
+    if not x.is_cuda or x.dim() < 1 or weight.dim() != 2 or x.shape[-1] != weight.shape[1]:
+        raise EmpError(f"x [..., K] and weight [N, K] must agree: {tuple(x.shape)}, {tuple(weight.shape)}")
+    if activation not in _ACTIVATIONS:
+        raise EmpError(f"activation must be one of {sorted(_ACTIVATIONS)}")
+    N, K = weight.shape
+    if K == 0 or N == 0:
+        raise EmpError("weight has no elements")
+    return x.numel() // K, K, N
+
+
+def mp_dense(x, weight, bias=None, activation: str = "none", residual=None, x_scale=None, w_scale=None, out_dtype=None,
+             keep_z: bool = False):
+    """Dense layer on rows (see include/emp.h): y = activation(x W^T + bias) + residual.
+
+    x [..., K], weight [N, K] of one type: float32 (kept at FP32 accuracy), bfloat16, float16, or
+    float8_e4m3fn with x_scale [...] and w_scale [N] (float32; what mp_rms_norm(quantize=True) returns).
+    bias [N] (float32 for 8-bit inputs, else x's type); residual [..., N] and y are of x's type, or for 8-bit
+    inputs of out_dtype (bfloat16 unless given).  activation: "none", "silu", "gelu".  keep_z: returns
+    (y, z) with z = x W^T + bias, which mp_dense_grad takes.  No autograd."""
+    torch = _torch()
+    rows, K, N = _dense_shapes(x, weight, activation)
+    code = _dtype_code(x.dtype, "x", e4m3=True)
+    if code == 3:
+        out = torch.bfloat16 if out_dtype is None else out_dtype
+        if x_scale is None or w_scale is None:
+            raise EmpError("8-bit inputs need x_scale and w_scale")
+    else:
+        out = x.dtype if out_dtype is None else out_dtype
+        if out != x.dtype or x_scale is not None or w_scale is not None:
+            raise EmpError("out_dtype and scales are for 8-bit inputs")
+    ycode = _dtype_code(out, "out_dtype")
+    _on(x.device, x.dtype, weight=weight)
+    _on(x.device, torch.float32 if code == 3 else x.dtype, bias=bias)
+    _on(x.device, torch.float32, x_scale=x_scale, w_scale=w_scale)
+    _on(x.device, out, residual=residual)
+    shape = (*x.shape[:-1], N)
+    _like(residual, shape, "residual")
+    _like(x_scale, x.shape[:-1], "x_scale")
+    bias, w_scale = _vector(bias, N, "bias"), _vector(w_scale, N, "w_scale")
+    xs = None if x_scale is None else x_scale.contiguous()
+    xr, ldx = _as_rows(x, rows, K)
+    wr, ldw = _as_rows(weight, N, K)
+    rr, ldr = (None, 0) if residual is None else _as_rows(residual, rows, N)
+    y = torch.empty(shape, dtype=out, device=x.device)
+    z = torch.empty(shape, dtype=out, device=x.device) if keep_z else None
+    a = DenseC(rows, K, N, code, ycode, _ACTIVATIONS[activation], _ptr(xr), ldx, _ptr(xs), _ptr(wr), ldw, _ptr(w_scale),
+               _ptr(bias), _ptr(rr), ldr, _ptr(y), N, _ptr(z), N)
+    _call("mp_dense", a, x.device)
+    return (y, z) if keep_z else y
+
+
+def mp_dense_grad(g, x, weight, z=None, activation: str = "none", need_x: bool = True, need_weight: bool = True,
+                  need_bias: bool = True):
+    """Gradient of mp_dense: (g_x, g_weight, g_bias) from g = dE/dy [..., N] (also dE/dresidual), the layer's
+    x [..., K] and weight [N, K], and with an activation the z that mp_dense(keep_z=True) returned.  What is
+    not needed is not computed and comes back as None.  Types are x's: float32, bfloat16 or float16."""
+    torch = _torch()
+    rows, K, N = _dense_shapes(x, weight, activation)
+    code = _dtype_code(x.dtype, "x")
+    if (z is None) != (activation == "none"):
+        raise EmpError("z goes with an activation")
+    _on(x.device, x.dtype, weight=weight, g=g, z=z)
+    shape = (*x.shape[:-1], N)
+    _like(g, shape, "g")
+    _like(z, shape, "z")
+    gr, ldg = _as_rows(g, rows, N)
+    zr, ldz = (None, 0) if z is None else _as_rows(z, rows, N)
+    xr, ldx = _as_rows(x, rows, K)
+    wr, ldw = _as_rows(weight, N, K)
+    new = lambda s, need: torch.empty(s, dtype=x.dtype, device=x.device) if need else None  # noqa: E731
+    g_x, g_w, g_b = new(x.shape, need_x), new((N, K), need_weight), new((N,), need_bias)
+    a = DenseGradC(rows, K, N, code, _ACTIVATIONS[activation], _ptr(gr), ldg, _ptr(zr), ldz, _ptr(xr), ldx, _ptr(wr), ldw,
+                   _ptr(g_x), K, _ptr(g_w), _ptr(g_b))
+    _call("mp_dense_grad", a, x.device)
+    return g_x, g_w, g_b

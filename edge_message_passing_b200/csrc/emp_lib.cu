@@ -17,6 +17,8 @@
 #include "end_layers.cuh"
 #include "tables.cuh"
 #include "radial_tc.cuh"
+#include "norm.cuh"
+#include "dense.cuh"
 
 using namespace emp;
 
@@ -1715,3 +1717,5 @@ int mp_radial_chain(const void* chain, int64_t E, const float* x, float* kc, flo
 }
 
 }  // extern "C"
+
+#include "rows_api.cuh"

@@ -1,0 +1,131 @@
+// Typed rows for the row-wise operators (norm.cuh, dense.cuh): loads and stores of fp32, bf16, fp16 and
+// e4m3 elements as fp32 values, the activations, and the fixed-order join of per-block column sums.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include "emp_common.cuh"
+
+namespace emp {
+
+__host__ __device__ constexpr int dtype_size(int t) { return t == EMP_F32 ? 4 : t == EMP_E4M3 ? 1 : 2; }
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f(__nv_fp8_e4m3 v) { return (float)v; }
+template <typename T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+
+// V consecutive elements as floats; V > 1 needs p aligned to V * sizeof(T) bytes (16 at most)
+template <typename T, int V>
+__device__ __forceinline__ void load_v(const T* p, float (&v)[V]) {
+  if constexpr (V == 1) {
+    v[0] = to_f(*p);
+  } else {
+    static_assert(V * sizeof(T) == 16 || V * sizeof(T) == 8, "vector bytes");
+    T e[V];
+    if constexpr (V * sizeof(T) == 16) *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
+    else *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = to_f(e[i]);
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
+  if constexpr (V == 1) {
+    *p = from_f<T>(v[0]);
+  } else {
+    T e[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) e[i] = from_f<T>(v[i]);
+    if constexpr (V * sizeof(T) == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(e);
+    else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(e);
+  }
+}
+// V values rounded to e4m3 (to nearest even; beyond +-448 to +-448; NaN kept)
+template <int V>
+__device__ __forceinline__ void store_e4m3(__nv_fp8_storage_t* p, const float (&v)[V]) {
+  if constexpr (V == 1) {
+    *p = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
+  } else {
+    __nv_fp8x2_storage_t e[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) e[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+    if constexpr (V == 4) *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(e);
+    else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(e);
+  }
+}
+
+// one element of a buffer whose type is known at run time only (edges, small operands)
+__device__ __forceinline__ float load_any(const void* p, size_t i, int t) {
+  switch (t) {
+    case EMP_F32: return static_cast<const float*>(p)[i];
+    case EMP_BF16: return to_f(static_cast<const __nv_bfloat16*>(p)[i]);
+    case EMP_F16: return to_f(static_cast<const __half*>(p)[i]);
+    default: return to_f(static_cast<const __nv_fp8_e4m3*>(p)[i]);
+  }
+}
+__device__ __forceinline__ void store_any(void* p, size_t i, int t, float v) {
+  switch (t) {
+    case EMP_F32: static_cast<float*>(p)[i] = v; break;
+    case EMP_BF16: static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v); break;
+    default: static_cast<__half*>(p)[i] = __float2half_rn(v); break;
+  }
+}
+
+// degree of component lm = l*l + l + m
+__device__ __forceinline__ int degree_of(int lm) { return (lm > 0) + (lm > 3) + (lm > 8); }
+
+// ------------------------------------------------------------- activations
+// SiLU z/(1+exp(-z)) and GELU z Phi(z) (Phi by erf, no tanh form), and their derivatives
+__device__ __forceinline__ float act_f(int act, float z) {
+  if (act == EMP_ACT_SILU) return silu_f(z);
+  if (act == EMP_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  return z;
+}
+__device__ __forceinline__ float dact_f(int act, float z) {
+  if (act == EMP_ACT_SILU) return dsilu_f(z);
+  if (act == EMP_ACT_GELU)
+    return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+  return 1.0f;
+}
+
+// ------------------------------------------------------------- join of column sums
+// out[o] = sum over blocks b in order of part[b][j], for every column j that maps to o: j = o without
+// degrees; with degrees, o = (l, c) of [4][C] and the columns (lm, c) of its 2l + 1 components.
+// 32 columns per block, JOIN_WARPS warps over the rows (warp w takes rows w, w + JOIN_WARPS, ...; the
+// warps' sums are added in warp order), so the order is fixed.
+constexpr int JOIN_WARPS = 16;
+__global__ void __launch_bounds__(32 * JOIN_WARPS)
+    k_col_join(int nb, int cols, int nout, int degrees, const float* __restrict__ part, void* __restrict__ out, int dtype) {
+  __shared__ float sm[JOIN_WARPS][33];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int o = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (o < nout) {
+    int first = o, count = 1, step = 0;
+    if (degrees) {
+      const int C = cols / NCOMP, l = o / C, c = o % C;
+      first = l * l * C + c;
+      count = 2 * l + 1;
+      step = C;
+    }
+    for (int b = w; b < nb; b += JOIN_WARPS) {
+      const float* row = part + (size_t)b * cols + first;
+      for (int q = 0; q < count; ++q) s += row[(size_t)q * step];
+    }
+  }
+  sm[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && o < nout) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < JOIN_WARPS; ++i) t += sm[i][lane];
+    store_any(out, (size_t)o, dtype, t);
+  }
+}
+
+}  // namespace emp

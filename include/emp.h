@@ -270,6 +270,130 @@ void mp_chain_destroy(void* chain);
 int mp_radial_chain(const void* chain, int64_t E, const float* x, float* kc, float* y0,
                     const float* g_kc, const float* g_y0, float* g_x, cudaStream_t stream);
 
+/* ------------------------------------------------------------ row-wise operators
+ * What goes between two calls of mp_forward in a model a user stacks from single layers: the
+ * update with a norm, and dense layers on node or edge rows (no counterpart on the pages; the
+ * message-passing models' node blocks use them).  Rows have a pitch in ELEMENTS, so degree-0
+ * channels of node features [N][16][C] are rows of C with pitch 16 C.  A row's elements are
+ * contiguous.  Pointers need the alignment of their element; 16-byte aligned pointers and
+ * pitches that are multiples of 16 bytes run faster.  Nothing behind the last row or the last
+ * column is read or written.  Zero rows are allowed (no launch; row pointers may then be NULL). */
+typedef enum {
+  EMP_F32 = 0,
+  EMP_BF16 = 1,
+  EMP_F16 = 2,
+  EMP_E4M3 = 3      /* 8 bits: 4 exponent, 3 mantissa bits, largest value 448, no infinity */
+} emp_dtype;
+typedef enum {
+  EMP_ACT_NONE = 0,
+  EMP_ACT_SILU = 1, /* z / (1 + exp(-z)) */
+  EMP_ACT_GELU = 2  /* z Phi(z), Phi the normal distribution function (by erf) */
+} emp_activation;
+
+#define EMP_NORM_MAX_COLS 8192
+typedef struct {
+  int64_t rows;
+  int32_t cols;             /* 1 .. EMP_NORM_MAX_COLS */
+  int32_t dtype;            /* of x, residual, weight and s: EMP_F32, EMP_BF16 or EMP_F16 */
+  int32_t y_dtype;          /* dtype, or EMP_E4M3 */
+  int32_t degrees;          /* 0: weight [cols]; 1: cols = 16 C, weight [4][C], one per degree and channel */
+  float eps;                /* > 0 */
+  const void* x;
+  int64_t ldx;
+  const void* residual;     /* or NULL */
+  int64_t ldr;
+  const void* weight;       /* or NULL: 1 */
+  void* y;
+  int64_t ldy;
+  float* scale;             /* [rows] with EMP_E4M3, else NULL */
+  void* s;                  /* x + residual rounded to dtype, or NULL */
+  int64_t lds;
+} emp_rms_norm;
+
+/* Root-mean-square norm of rows with the residual's addition:
+ *   s = x + residual,  y_j = s_j weight_j / sqrt(mean_j s_j^2 + eps)
+ * (y from the unrounded s; sums in FP32, so |s| up to 1e18).  With degrees, a row is an atom's
+ * [16][C] features and the weight depends on degree and channel alone: the norm then commutes
+ * with rotations.  y_dtype EMP_E4M3: scale = max_j |y_j| / 448 and y / scale rounded to e4m3
+ * (ties to even); a row with max |y| < 2^-110 has scale 1; a row with a NaN or an infinity in s has
+ * NaN values and scale.  Errors: EMP_ERR_ARG, EMP_ERR_UNSUPPORTED. */
+int mp_rms_norm(const emp_rms_norm* a, cudaStream_t stream);
+
+typedef struct {
+  int64_t rows;
+  int32_t cols, dtype, degrees;
+  float eps;
+  const void* g;            /* dE/dy */
+  int64_t ldg;
+  const void* s;            /* x + residual, as mp_rms_norm stored it (x itself without a residual) */
+  int64_t lds;
+  const void* g_s;          /* dE/ds from the uses of s other than the norm, or NULL */
+  int64_t ldgs;
+  const void* weight;       /* or NULL */
+  void* g_x;                /* dE/dx, which is dE/dresidual too */
+  int64_t ldgx;
+  void* g_weight;           /* [cols] or [4][C], contiguous, or NULL */
+} emp_rms_norm_grad;
+
+/* Gradient of mp_rms_norm (y not in 8 bits).  Types are dtype throughout; sums over rows in FP32
+ * in a fixed order.  Workspace only with g_weight.  Zero rows: g_weight is zeroed. */
+size_t mp_rms_norm_grad_workspace_bytes(const emp_rms_norm_grad* a);
+int mp_rms_norm_grad(const emp_rms_norm_grad* a, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+typedef struct {
+  int64_t rows;             /* < 2^31 - 256 */
+  int32_t fan_in, fan_out;  /* 1 .. 65536 */
+  int32_t dtype;            /* of x and weight: EMP_F32, EMP_BF16, EMP_F16 or EMP_E4M3 */
+  int32_t y_dtype;          /* of y, z and residual: dtype; for EMP_E4M3 one of the other three */
+  int32_t activation;       /* emp_activation */
+  const void* x;            /* [rows][fan_in] */
+  int64_t ldx;
+  const float* x_scale;     /* [rows] with EMP_E4M3 (x stands for x_scale x), else NULL */
+  const void* weight;       /* [fan_out][fan_in] */
+  int64_t ldw;
+  const float* w_scale;     /* [fan_out] with EMP_E4M3, else NULL */
+  const void* bias;         /* [fan_out] of dtype (float for EMP_E4M3), or NULL */
+  const void* residual;     /* or NULL */
+  int64_t ldr;
+  void* y;                  /* [rows][fan_out] */
+  int64_t ldy;
+  void* z;                  /* x W^T + bias before the activation, for mp_dense_grad, or NULL */
+  int64_t ldz;
+} emp_dense;
+
+/* Dense layer on rows:  z = x W^T + bias,  y = activation(z) + residual.
+ * FP32 inputs keep FP32 accuracy; 16-bit and 8-bit inputs are multiplied as they are and summed in FP32; y and
+ * z are rounded once, at the end.  An infinite or NaN input makes outputs of its row (of x) or
+ * column (of weight) NaN or infinite, and no others.  Errors: EMP_ERR_ARG, EMP_ERR_UNSUPPORTED,
+ * EMP_ERR_WORKSPACE (ws_bytes below mp_dense_workspace_bytes(a); 0 for many shapes). */
+size_t mp_dense_workspace_bytes(const emp_dense* a);
+int mp_dense(const emp_dense* a, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+typedef struct {
+  int64_t rows;
+  int32_t fan_in, fan_out;
+  int32_t dtype;            /* EMP_F32, EMP_BF16 or EMP_F16 */
+  int32_t activation;
+  const void* g;            /* dE/dy [rows][fan_out]; dE/dresidual is g itself */
+  int64_t ldg;
+  const void* z;            /* as mp_dense stored it; NULL with EMP_ACT_NONE */
+  int64_t ldz;
+  const void* x;            /* NULL without g_weight */
+  int64_t ldx;
+  const void* weight;       /* NULL without g_x */
+  int64_t ldw;
+  void* g_x;                /* [rows][fan_in], or NULL */
+  int64_t ldgx;
+  void* g_weight;           /* [fan_out][fan_in], contiguous, or NULL */
+  void* g_bias;             /* [fan_out], or NULL */
+} emp_dense_grad;
+
+/* Gradient of mp_dense:  gz = g activation'(z),  g_x = gz W,  g_weight = gz^T x,  g_bias = sum gz.
+ * For 16-bit types gz is rounded to dtype as an operand of the two products (g_bias sums it
+ * unrounded).  Sums over rows in FP32 in a fixed order.  Zero rows: g_weight and g_bias are zeroed. */
+size_t mp_dense_grad_workspace_bytes(const emp_dense_grad* a);
+int mp_dense_grad(const emp_dense_grad* a, void* ws, size_t ws_bytes, cudaStream_t stream);
+
 /* ------------------------------------------------------------ timing
  * Every kernel launch of the library is counted.  With profiling enabled, a
  * pair of CUDA events is recorded on the launching stream around each launch,
