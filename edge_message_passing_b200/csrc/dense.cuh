@@ -26,57 +26,82 @@ __device__ __forceinline__ void put_one(const Epi& e, long long m, int n, float 
   store_any(e.y, (size_t)m * e.ldy + n, e.y_dtype, v);
 }
 
-// ------------------------------------------------------------------ a product in FP32 on SIMT
-// out[m][n] = sum_k A(m, k) B(n, k), A(m, k) = a[m am + k ak], B(n, k) = b[n bn + k bk]: any strides,
-// any type.  64 x 64 tiles, 4 x 4 outputs a thread.  Splits of the k axis (gridDim.z) leave partial
-// products in part[z][M][N], joined in order by k_join.
-struct Prod {
-  long long M, K;
-  int N, dtype;
-  const void *a, *b;
-  long long am, ak, bn, bk;
-  float* part;
-};
-constexpr int T_M = 64, T_K = 16;
+// ------------------------------------------------------------------ few rows
+// Up to FEW_ROWS rows: the product reads W once and little else, so it runs on SIMT with a warp on
+// FEW_COLS columns of the output and up to 8 rows at a time (x in shared memory as floats, K_PART of k at
+// once; a lane takes V elements of k, 32 V apart), in FP32 throughout.
+constexpr int FEW_ROWS = 16, FEW_COLS = 2, FEW_WARPS = 4, FEW_M = 8, K_PART = 1024;
 
-__global__ void __launch_bounds__(256) k_dense_simt(const Prod p, const Epi e) {
-  __shared__ float as[T_K][T_M + 1], bs[T_K][T_M + 1];
-  const long long m0 = (long long)blockIdx.x * T_M;
-  const int n0 = blockIdx.y * T_M;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const long long per = ((p.K + gridDim.z - 1) / gridDim.z + T_K - 1) / T_K * T_K;
-  const long long k_first = per * blockIdx.z, k_end = k_first + per < p.K ? k_first + per : p.K;
-  float acc[4][4] = {};
-  for (long long k0 = k_first; k0 < k_end; k0 += T_K) {
-    for (int i = threadIdx.x; i < T_K * T_M; i += 256) {
-      const int k = p.ak == 1 ? i % T_K : i / T_M, m = p.ak == 1 ? i / T_K : i % T_M;
-      as[k][m] = m0 + m < p.M && k0 + k < k_end ? load_any(p.a, (size_t)((m0 + m) * p.am + (k0 + k) * p.ak), p.dtype) : 0.f;
-    }
-    for (int i = threadIdx.x; i < T_K * T_M; i += 256) {
-      const int k = p.bk == 1 ? i % T_K : i / T_M, n = p.bk == 1 ? i / T_K : i % T_M;
-      bs[k][n] = n0 + n < p.N && k0 + k < k_end ? load_any(p.b, (size_t)((n0 + n) * p.bn + (k0 + k) * p.bk), p.dtype) : 0.f;
+struct Few {
+  int M, N, K;
+  const void *x, *w;
+  long long ldx, ldw;
+};
+
+template <typename T, int V>
+__global__ void __launch_bounds__(32 * FEW_WARPS) k_dense_few(const Few p, const Epi e) {
+  __shared__ __align__(16) float xs[FEW_M][K_PART];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n0 = (blockIdx.x * FEW_WARPS + warp) * FEW_COLS, m0 = blockIdx.y * FEW_M;
+  float acc[FEW_COLS][FEW_M] = {};
+  for (int k0 = 0; k0 < p.K; k0 += K_PART) {
+    const int kn = min(K_PART, p.K - k0);
+    if (k0) __syncthreads();
+    for (int i = threadIdx.x * V; i < FEW_M * K_PART; i += 32 * FEW_WARPS * V) {
+      const int r = i / K_PART, k = i % K_PART;
+      float v[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = 0.f;
+      if (m0 + r < p.M && k < kn) load_v<T, V>(static_cast<const T*>(p.x) + (m0 + r) * p.ldx + k0 + k, v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) xs[r][k + j] = v[j];
     }
     __syncthreads();
+    for (int k = lane * V; k < kn; k += 32 * V) {
+      float w[FEW_COLS][V];
 #pragma unroll
-    for (int k = 0; k < T_K; ++k)
+      for (int c = 0; c < FEW_COLS; ++c) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < V; ++j) w[c][j] = 0.f;
+        if (n0 + c < p.N) load_v<T, V>(static_cast<const T*>(p.w) + (n0 + c) * p.ldw + k0 + k, w[c]);
+      }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += as[k][ty + 16 * i] * bs[k][tx + 16 * j];
-    __syncthreads();
+      for (int r = 0; r < FEW_M; ++r)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float x = xs[r][k + j];
+#pragma unroll
+          for (int c = 0; c < FEW_COLS; ++c) acc[c][r] += w[c][j] * x;
+        }
+    }
   }
+  float mine = 0.f;                       // lane c FEW_M + r keeps output (r, c)
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int c = 0; c < FEW_COLS; ++c)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const long long m = m0 + ty + 16 * i;
-      const int n = n0 + tx + 16 * j;
-      if (m >= p.M || n >= p.N) continue;
-      if (p.part) p.part[((size_t)blockIdx.z * p.M + m) * p.N + n] = acc[i][j];
-      else put_one(e, m, n, acc[i][j]);
+    for (int r = 0; r < FEW_M; ++r) {
+      float a = acc[c][r];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+      if (lane == c * FEW_M + r) mine = a;
     }
+  const int m = m0 + lane % FEW_M, n = n0 + lane / FEW_M;
+  if (lane < FEW_COLS * FEW_M && m < p.M && n < p.N) put_one(e, m, n, mine);
 }
 
+// ------------------------------------------------------------------ operands TMA cannot read
+// Rows whose start or pitch is not a multiple of 16 bytes are copied once to rows that are.
+template <typename B>
+__global__ void k_pack(long long rows, int cols, const B* __restrict__ src, long long ld, B* __restrict__ dst, long long ldd) {
+  const long long total = rows * cols;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long long)gridDim.x * blockDim.x) {
+    const long long r = i / cols;
+    const int c = (int)(i - r * cols);
+    dst[r * ldd + c] = src[r * ld + c];
+  }
+}
+
+// ------------------------------------------------------------------ join of the k splits, in order
 __global__ void k_join(long long M, int N, int splits, const float* __restrict__ part, const Epi e) {
   const size_t total = (size_t)M * N;
   for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (size_t)gridDim.x * blockDim.x) {

@@ -18,7 +18,7 @@
 #include "tables.cuh"
 #include "radial_tc.cuh"
 #include "norm.cuh"
-#include "dense.cuh"
+#include "dense_tc.cuh"
 
 using namespace emp;
 

@@ -25,41 +25,141 @@ bool norm_sizes_ok(long long rows, int cols, int dtype, int degrees, float eps) 
 }
 
 // ------------------------------------------------------------------ dense
-// splits of a product's k axis: enough tiles for every SM, at least 256 of k each
-int simt_splits(long long M, long long N, long long K) {
-  const long long tiles = ((M + dense::T_M - 1) / dense::T_M) * ((N + dense::T_M - 1) / dense::T_M);
-  return (int)std::max<long long>(1, std::min<long long>((296 + tiles - 1) / tiles, K / 256));
+// An operand of the tensor-core products: as it is if TMA can read it, else its packed copy at ws + off.
+struct Packed {
+  bool copy = false;
+  size_t off = 0;
+  long long ld = 0;
+};
+template <typename Take>
+Packed packed(const void* p, long long ld, long long rows, int cols, int t, Take& take) {
+  Packed k;
+  k.ld = ld;
+  if (rows == 1) k.ld = ld = (cols * dtype_size(t) + 15) / 16 * 16 / dtype_size(t);    // one row: any pitch will do
+  if (dtc::tma_ok(p, ld, t)) return k;
+  const int es = dtype_size(t);
+  k.copy = true;
+  k.ld = (cols * es + 15) / 16 * 16 / es;
+  k.off = take((size_t)rows * k.ld * es);
+  return k;
 }
+const void* pack(const Packed& k, const void* p, long long ld, long long rows, int cols, int t, void* ws, cudaStream_t s) {
+  if (!k.copy) return p;
+  void* d = at<char>(ws, k.off);
+  Scope sc_("dense_pack", s);
+  const int grid = grid_for(rows * cols, 1024);
+  switch (dtype_size(t)) {
+    case 4: dense::k_pack<<<grid, 256, 0, s>>>(rows, cols, static_cast<const uint32_t*>(p), ld, static_cast<uint32_t*>(d), k.ld); break;
+    case 2: dense::k_pack<<<grid, 256, 0, s>>>(rows, cols, static_cast<const uint16_t*>(p), ld, static_cast<uint16_t*>(d), k.ld); break;
+    default: dense::k_pack<<<grid, 256, 0, s>>>(rows, cols, static_cast<const uint8_t*>(p), ld, static_cast<uint8_t*>(d), k.ld);
+  }
+  return d;
+}
+
+struct DenseLayout {
+  bool few = false;
+  Packed x, w;
+  dtc::Shape h{};
+  size_t part = 0, total = 0;
+};
+DenseLayout dense_layout(const emp_dense& a) {
+  DenseLayout L;
+  L.few = a.rows <= dense::FEW_ROWS;
+  if (L.few) return L;
+  auto take = [&](size_t bytes) { size_t r = L.total; L.total = align_up(L.total + bytes); return r; };
+  L.x = packed(a.x, a.ldx, a.rows, a.fan_in, a.dtype, take);
+  L.w = packed(a.weight, a.ldw, a.fan_out, a.fan_in, a.dtype, take);
+  L.h = dtc::shape_for(a.rows, a.fan_out, a.fan_in, a.dtype);
+  L.part = take(L.h.splits > 1 ? (size_t)L.h.splits * a.rows * a.fan_out * 4 : 0);
+  return L;
+}
+
 struct DenseGradLayout {
-  size_t gz, colsum, part, total;
-  long long ldgz;
-  int gz_blocks, splits;
+  size_t gz = 0, colsum = 0, part_x = 0, part_w = 0, total = 0;
+  long long ldgz = 0;
+  bool prep = false;             // gz is written (an activation, or g that TMA cannot read)
+  int gz_blocks = 0;
+  Packed x, w;
+  dtc::Shape hx{}, hw{};
 };
 DenseGradLayout dense_grad_layout(const emp_dense_grad& a) {
   DenseGradLayout L{};
   const int es = dtype_size(a.dtype);
-  size_t o = 0;
-  auto take = [&](size_t bytes) { size_t r = o; o = align_up(o + bytes); return r; };
+  auto take = [&](size_t bytes) { size_t r = L.total; L.total = align_up(L.total + bytes); return r; };
+  const bool products = a.g_x || a.g_weight;
   L.ldgz = (a.fan_out * es + 15) / 16 * 16 / es;
-  L.gz = take(a.activation != EMP_ACT_NONE && (a.g_x || a.g_weight) ? (size_t)a.rows * L.ldgz * es : 0);
+  L.prep = products && (a.activation != EMP_ACT_NONE || !dtc::tma_ok(a.g, a.rows == 1 ? 0 : a.ldg, a.dtype));
+  L.gz = take(L.prep ? (size_t)a.rows * L.ldgz * es : 0);
+  if (!L.prep && a.rows > 1) L.ldgz = a.ldg;
   L.gz_blocks = (int)std::max<long long>(1, std::min<long long>((a.rows + 63) / 64, std::max(1, 592 * 32 / a.fan_out)));
   L.colsum = take(a.g_bias ? (size_t)L.gz_blocks * a.fan_out * 4 : 0);
-  L.splits = simt_splits(a.fan_out, a.fan_in, a.rows);
-  L.part = take(a.g_weight && L.splits > 1 ? (size_t)L.splits * a.fan_out * a.fan_in * 4 : 0);
-  L.total = o;
+  if (a.g_x) {
+    L.w = packed(a.weight, a.ldw, a.fan_out, a.fan_in, a.dtype, take);
+    L.hx = dtc::shape_for(a.rows, a.fan_in, a.fan_out, a.dtype);
+    L.part_x = take(L.hx.splits > 1 ? (size_t)L.hx.splits * a.rows * a.fan_in * 4 : 0);
+  }
+  if (a.g_weight) {
+    L.x = packed(a.x, a.ldx, a.rows, a.fan_in, a.dtype, take);
+    L.hw = dtc::shape_for(a.fan_out, a.fan_in, a.rows, a.dtype);
+    L.part_w = take(L.hw.splits > 1 ? (size_t)L.hw.splits * a.fan_out * a.fan_in * 4 : 0);
+  }
   return L;
 }
 bool dense_sizes_ok(long long rows, int fan_in, int fan_out, int act) {
   return rows >= 0 && rows < (1ll << 31) - 256 && fan_in >= 1 && fan_in <= 65536 && fan_out >= 1 && fan_out <= 65536 &&
          act >= EMP_ACT_NONE && act <= EMP_ACT_GELU;
 }
-void dense_product(const dense::Prod& p, const dense::Epi& e, int splits, cudaStream_t s) {
-  const dim3 grid((unsigned)((p.M + dense::T_M - 1) / dense::T_M), (unsigned)((p.N + dense::T_M - 1) / dense::T_M), splits);
-  { Scope sc_("dense", s); dense::k_dense_simt<<<grid, 256, 0, s>>>(p, e); }
-  if (p.part) {
-    Scope sc_("dense_join", s);
-    dense::k_join<<<grid_for((long long)p.M * p.N, 256), 256, 0, s>>>(p.M, p.N, splits, p.part, e);
-  }
+bool dense_args_ok(const emp_dense& a) {
+  const bool q = a.dtype == EMP_E4M3;
+  if (!dense_sizes_ok(a.rows, a.fan_in, a.fan_out, a.activation) || (!q && !row_dtype(a.dtype)) || !row_dtype(a.y_dtype) ||
+      (!q && a.y_dtype != a.dtype))
+    return false;
+  if (a.rows == 0) return true;
+  return rows_ok(a.x, a.ldx, a.fan_in, a.rows, a.dtype) && rows_ok(a.weight, a.ldw, a.fan_in, a.fan_out, a.dtype) &&
+         q == (a.x_scale != nullptr) && q == (a.w_scale != nullptr) && on_element(a.x_scale, EMP_F32) &&
+         on_element(a.w_scale, EMP_F32) && on_element(a.bias, q ? EMP_F32 : a.dtype) &&
+         rows_ok_or_null(a.residual, a.ldr, a.fan_out, a.rows, a.y_dtype) &&
+         rows_ok(a.y, a.ldy, a.fan_out, a.rows, a.y_dtype) && rows_ok_or_null(a.z, a.ldz, a.fan_out, a.rows, a.y_dtype);
+}
+bool dense_grad_args_ok(const emp_dense_grad& a) {
+  if (!dense_sizes_ok(a.rows, a.fan_in, a.fan_out, a.activation) || !row_dtype(a.dtype) || !on_element(a.g_weight, a.dtype) ||
+      !on_element(a.g_bias, a.dtype))
+    return false;
+  if (a.rows == 0) return true;
+  return rows_ok(a.g, a.ldg, a.fan_out, a.rows, a.dtype) && (a.z != nullptr) == (a.activation != EMP_ACT_NONE) &&
+         rows_ok_or_null(a.z, a.ldz, a.fan_out, a.rows, a.dtype) &&
+         (!a.g_x || (rows_ok(a.g_x, a.ldgx, a.fan_in, a.rows, a.dtype) && rows_ok(a.weight, a.ldw, a.fan_in, a.fan_out, a.dtype))) &&
+         (!a.g_weight || rows_ok(a.x, a.ldx, a.fan_in, a.rows, a.dtype));
+}
+// rows of y, z and residual that allow 16-byte accesses
+bool epi_vec(const dense::Epi& e, int N) {
+  const int es = dtype_size(e.y_dtype);
+  auto ok = [&](const void* p, long long ld) { return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0); };
+  return N * es % 16 == 0 && ok(e.y, e.ldy) && ok(e.z, e.ldz) && ok(e.residual, e.ldr);
+}
+int dense_product(long long M, int N, long long K, int t, const dtc::Operand& a, const dtc::Operand& b, const dense::Epi& e,
+                  const dtc::Shape& h, float* part, cudaStream_t s) {
+  int st;
+  { Scope sc_("dense", s); st = dtc::launch(M, N, K, t, a, b, e, h, h.splits > 1 ? part : nullptr, epi_vec(e, N), s); }
+  if (st != EMP_OK || h.splits == 1) return st;
+  Scope sc_("dense_join", s);
+  dense::k_join<<<grid_for(M * N, 256), 256, 0, s>>>(M, N, h.splits, part, e);
+  return cudaGetLastError() == cudaSuccess ? EMP_OK : EMP_ERR_CUDA;
+}
+template <typename T>
+void dense_few(const emp_dense& a, const dense::Epi& e, cudaStream_t s) {
+  constexpr int V = sizeof(T) == 1 ? 8 : 16 / sizeof(T);
+  const dense::Few p{(int)a.rows, a.fan_out, a.fan_in, a.x, a.weight, a.ldx, a.ldw};
+  const dim3 grid((a.fan_out + dense::FEW_WARPS * dense::FEW_COLS - 1) / (dense::FEW_WARPS * dense::FEW_COLS),
+                  ((int)a.rows + dense::FEW_M - 1) / dense::FEW_M);
+  auto ok = [&](const void* q, long long ld, long long rows) {
+    return reinterpret_cast<uintptr_t>(q) % (V * sizeof(T)) == 0 && (rows == 1 || ld % V == 0);
+  };
+  Scope sc_("dense_few", s);
+  if (a.fan_in % V == 0 && ok(a.x, a.ldx, a.rows) && ok(a.weight, a.ldw, a.fan_out))
+    dense::k_dense_few<T, V><<<grid, 32 * dense::FEW_WARPS, 0, s>>>(p, e);
+  else
+    dense::k_dense_few<T, 1><<<grid, 32 * dense::FEW_WARPS, 0, s>>>(p, e);
 }
 
 }  // namespace
@@ -124,61 +224,57 @@ int mp_rms_norm_grad(const emp_rms_norm_grad* a, void* ws, size_t ws_bytes, cuda
 }
 
 size_t mp_dense_workspace_bytes(const emp_dense* a) {
-  (void)a;
-  return 0;
+  if (!a || !dense_args_ok(*a)) return 0;
+  return dense_layout(*a).total;
 }
 
 int mp_dense(const emp_dense* a, void* ws, size_t ws_bytes, cudaStream_t stream) {
-  (void)ws; (void)ws_bytes;
-  if (!a || !dense_sizes_ok(a->rows, a->fan_in, a->fan_out, a->activation)) return EMP_ERR_ARG;
-  const bool q = a->dtype == EMP_E4M3;
-  if ((!q && !row_dtype(a->dtype)) || !row_dtype(a->y_dtype) || (!q && a->y_dtype != a->dtype)) return EMP_ERR_ARG;
+  if (!a || !dense_args_ok(*a)) return EMP_ERR_ARG;
   if (a->rows == 0) return EMP_OK;
-  const int bt = q ? EMP_F32 : a->dtype;
-  if (!rows_ok(a->x, a->ldx, a->fan_in, a->rows, a->dtype) || !rows_ok(a->weight, a->ldw, a->fan_in, a->fan_out, a->dtype) ||
-      q != (a->x_scale != nullptr) || q != (a->w_scale != nullptr) || !on_element(a->x_scale, EMP_F32) ||
-      !on_element(a->w_scale, EMP_F32) || !on_element(a->bias, bt) ||
-      !rows_ok_or_null(a->residual, a->ldr, a->fan_out, a->rows, a->y_dtype) ||
-      !rows_ok(a->y, a->ldy, a->fan_out, a->rows, a->y_dtype) || !rows_ok_or_null(a->z, a->ldz, a->fan_out, a->rows, a->y_dtype))
-    return EMP_ERR_ARG;
+  const DenseLayout L = dense_layout(*a);
+  if (L.total && (!ws || reinterpret_cast<uintptr_t>(ws) % 256)) return EMP_ERR_ARG;
+  if (ws_bytes < L.total) return EMP_ERR_WORKSPACE;
   int st = check_device();
   if (st != EMP_OK) return st;
+  const int bt = a->dtype == EMP_E4M3 ? EMP_F32 : a->dtype;
   const dense::Epi e{a->activation, a->y_dtype, bt, a->x_scale, a->w_scale, a->bias, a->residual, a->ldr, a->y, a->z, a->ldy, a->ldz};
-  const dense::Prod p{a->rows, a->fan_in, a->fan_out, a->dtype, a->x, a->weight, a->ldx, 1, a->ldw, 1, nullptr};
-  dense_product(p, e, 1, stream);
-  return cudaGetLastError() == cudaSuccess ? EMP_OK : EMP_ERR_CUDA;
+  if (L.few) {
+    if (a->dtype == EMP_F32) dense_few<float>(*a, e, stream);
+    else if (a->dtype == EMP_BF16) dense_few<__nv_bfloat16>(*a, e, stream);
+    else if (a->dtype == EMP_F16) dense_few<__half>(*a, e, stream);
+    else dense_few<__nv_fp8_e4m3>(*a, e, stream);
+    return cudaGetLastError() == cudaSuccess ? EMP_OK : EMP_ERR_CUDA;
+  }
+  st = dtc::init();
+  if (st != EMP_OK) return st;
+  const dtc::Operand x{pack(L.x, a->x, a->ldx, a->rows, a->fan_in, a->dtype, ws, stream), L.x.ld, 0};
+  const dtc::Operand w{pack(L.w, a->weight, a->ldw, a->fan_out, a->fan_in, a->dtype, ws, stream), L.w.ld, 0};
+  return dense_product(a->rows, a->fan_out, a->fan_in, a->dtype, x, w, e, L.h, at<float>(ws, L.part), stream);
 }
 
 size_t mp_dense_grad_workspace_bytes(const emp_dense_grad* a) {
-  return a && row_dtype(a->dtype) && dense_sizes_ok(a->rows, a->fan_in, a->fan_out, a->activation) ? dense_grad_layout(*a).total : 0;
+  if (!a || !dense_grad_args_ok(*a) || a->rows == 0) return 0;
+  return dense_grad_layout(*a).total;
 }
 
 int mp_dense_grad(const emp_dense_grad* a, void* ws, size_t ws_bytes, cudaStream_t stream) {
-  if (!a || !dense_sizes_ok(a->rows, a->fan_in, a->fan_out, a->activation) || !row_dtype(a->dtype)) return EMP_ERR_ARG;
+  if (!a || !dense_grad_args_ok(*a)) return EMP_ERR_ARG;
   const int es = dtype_size(a->dtype);
-  if (!on_element(a->g_weight, a->dtype) || !on_element(a->g_bias, a->dtype)) return EMP_ERR_ARG;
   if (a->rows == 0) {
     if (a->g_weight) EMP_CUDA_TRY(cudaMemsetAsync(a->g_weight, 0, (size_t)a->fan_out * a->fan_in * es, stream));
     if (a->g_bias) EMP_CUDA_TRY(cudaMemsetAsync(a->g_bias, 0, (size_t)a->fan_out * es, stream));
     return EMP_OK;
   }
-  if (!rows_ok(a->g, a->ldg, a->fan_out, a->rows, a->dtype) || (a->z != nullptr) != (a->activation != EMP_ACT_NONE) ||
-      !rows_ok_or_null(a->z, a->ldz, a->fan_out, a->rows, a->dtype))
-    return EMP_ERR_ARG;
-  if (a->g_x && (!rows_ok(a->g_x, a->ldgx, a->fan_in, a->rows, a->dtype) || !rows_ok(a->weight, a->ldw, a->fan_in, a->fan_out, a->dtype)))
-    return EMP_ERR_ARG;
-  if (a->g_weight && !rows_ok(a->x, a->ldx, a->fan_in, a->rows, a->dtype)) return EMP_ERR_ARG;
   const DenseGradLayout L = dense_grad_layout(*a);
   if (L.total && (!ws || reinterpret_cast<uintptr_t>(ws) % 256)) return EMP_ERR_ARG;
   if (ws_bytes < L.total) return EMP_ERR_WORKSPACE;
   int st = check_device();
   if (st != EMP_OK) return st;
-  const bool prep = a->activation != EMP_ACT_NONE && (a->g_x || a->g_weight);
-  const void* gz = prep ? at<char>(ws, L.gz) : static_cast<const char*>(a->g);
-  const long long ldgz = prep ? L.ldgz : a->ldg;
-  if (prep || a->g_bias) {
+  st = dtc::init();
+  if (st != EMP_OK) return st;
+  if (L.prep || a->g_bias) {
     const dense::GzArgs z{a->rows, a->fan_out, a->dtype, a->activation, a->g, a->z, a->ldg, a->ldz, L.ldgz,
-                          prep ? at<char>(ws, L.gz) : nullptr, a->g_bias ? at<float>(ws, L.colsum) : nullptr};
+                          L.prep ? at<char>(ws, L.gz) : nullptr, a->g_bias ? at<float>(ws, L.colsum) : nullptr};
     { Scope sc_("dense_gz", stream);
       dense::k_dense_gz<<<dim3(L.gz_blocks, (a->fan_out + 31) / 32), 32 * dense::GZ_ROWS, 0, stream>>>(z); }
     if (a->g_bias) {
@@ -186,18 +282,19 @@ int mp_dense_grad(const emp_dense_grad* a, void* ws, size_t ws_bytes, cudaStream
       k_col_join<<<(a->fan_out + 31) / 32, 32 * JOIN_WARPS, 0, stream>>>(L.gz_blocks, a->fan_out, a->fan_out, 0, z.part, a->g_bias, a->dtype);
     }
   }
+  const void* gz = L.prep ? at<char>(ws, L.gz) : static_cast<const char*>(a->g);
   if (a->g_x) {
     const dense::Epi e{EMP_ACT_NONE, a->dtype, 0, nullptr, nullptr, nullptr, nullptr, 0, a->g_x, nullptr, a->ldgx, 0};
-    const dense::Prod p{a->rows, a->fan_out, a->fan_in, a->dtype, gz, a->weight, ldgz, 1, 1, a->ldw, nullptr};
-    dense_product(p, e, 1, stream);
+    const dtc::Operand w{pack(L.w, a->weight, a->ldw, a->fan_out, a->fan_in, a->dtype, ws, stream), L.w.ld, 1};
+    st = dense_product(a->rows, a->fan_in, a->fan_out, a->dtype, {gz, L.ldgz, 0}, w, e, L.hx, at<float>(ws, L.part_x), stream);
+    if (st != EMP_OK) return st;
   }
   if (a->g_weight) {
     const dense::Epi e{EMP_ACT_NONE, a->dtype, 0, nullptr, nullptr, nullptr, nullptr, 0, a->g_weight, nullptr, a->fan_in, 0};
-    const dense::Prod p{a->fan_out, a->rows, a->fan_in, a->dtype, gz, a->x, 1, ldgz, 1, a->ldx,
-                        L.splits > 1 ? at<float>(ws, L.part) : nullptr};
-    dense_product(p, e, L.splits, stream);
+    const dtc::Operand x{pack(L.x, a->x, a->ldx, a->rows, a->fan_in, a->dtype, ws, stream), L.x.ld, 1};
+    st = dense_product(a->fan_out, a->fan_in, a->rows, a->dtype, {gz, L.ldgz, 1}, x, e, L.hw, at<float>(ws, L.part_w), stream);
   }
-  return cudaGetLastError() == cudaSuccess ? EMP_OK : EMP_ERR_CUDA;
+  return st != EMP_OK ? st : cudaGetLastError() == cudaSuccess ? EMP_OK : EMP_ERR_CUDA;
 }
 
 }  // extern "C"
