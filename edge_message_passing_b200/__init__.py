@@ -618,76 +618,87 @@ def mp_radial_chain(chain: Chain, x, g_kc=None, g_y0=None, out=None):
 
 
 # ------------------------------------------------------------------ row-wise operators
+# These calls are short (a few microseconds on the device for a few hundred rows), so the host's part is
+# kept short too: torch is looked up once, and contiguous tensors take no reshape.
 _ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
+_T = None                  # torch
+_CODES: Dict[object, int] = {}
 
 
-def _dtype_code(t, what: str, e4m3: bool = False) -> int:
-    torch = _torch()
-    codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    if e4m3:
-        codes[torch.float8_e4m3fn] = 3
-    if t not in codes:
-        raise EmpError(f"{what}: type {t} is not supported")
-    return codes[t]
+def _row_torch():
+    global _T
+    if _T is None:
+        _T = _torch()
+        _CODES.update({_T.float32: 0, _T.bfloat16: 1, _T.float16: 2, _T.float8_e4m3fn: 3})
+    return _T
 
 
-def _on(device, dtype, **tensors):
-    """Every tensor given is on `device` and of `dtype`."""
-    for name, t in tensors.items():
-        if t is not None and (t.device != device or t.dtype != dtype):
-            raise EmpError(f"{name} must be a {dtype} tensor on {device}, not {t.dtype} on {t.device}")
+def _row_input(x, name: str):
+    """x's device index and type code (EmpError for what is not a CUDA tensor of rows)."""
+    torch = _row_torch()
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() < 1:
+        raise EmpError(f"{name} must be a CUDA tensor of rows")
+    code = _CODES.get(x.dtype)
+    if code is None:
+        raise EmpError(f"{name}: type {x.dtype} is not supported")
+    return x.get_device(), code
+
+
+def _same(t, shape, dtype, dev: int, name: str):
+    """t has this shape and type and is on this device."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev:
+        raise EmpError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, not {t.dtype} "
+                       f"{tuple(t.shape)} on {t.device}")
 
 
 def _as_rows(t, rows: int, cols: int):
     """t seen as [rows, cols] with contiguous elements in a row (copied if its strides do not allow it),
     and its row pitch."""
+    if t.is_contiguous():
+        return t, cols
     t = t.reshape(rows, cols)
     if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
         t = t.contiguous()
     return t, (t.stride(0) if rows > 1 else cols)
 
 
-def _vector(t, n: int, name: str):
-    if t is None:
-        return None
-    if tuple(t.shape) != (n,):
-        raise EmpError(f"{name} must have the shape ({n},), not {tuple(t.shape)}")
-    return t.contiguous()
+def _vector(t, n: int, dtype, dev: int, name: str):
+    _same(t, (n,), dtype, dev, name)
+    return t if t.is_contiguous() else t.contiguous()
 
 
-def _like(t, shape, name: str):
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise EmpError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+def _launch(fn, args, dev: int, workspace=None):
+    """Call an entry point on device `dev` and its current stream.  Its workspace is its own (allocated on
+    that stream), so calls on two streams or in two captured graphs share nothing."""
+    torch = _T
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(fn, args, dev, workspace)
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if workspace is None:
+        return fn(ctypes.byref(args), stream)
+    nbytes = workspace(ctypes.byref(args))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}") if nbytes else None
+    return fn(ctypes.byref(args), _ptr(ws), nbytes, stream)
 
 
-def _call(name: str, args, device):
-    """Call an entry point on the tensors' device and that device's current stream; its workspace is
-    its own (allocated on that stream), so calls on two streams or in two captured graphs share nothing."""
-    torch = _torch()
-    fn = getattr(lib(), name)
-    with torch.cuda.device(device):
-        stream = torch.cuda.current_stream().cuda_stream
-        if name == "mp_rms_norm":
-            _check(fn(ctypes.byref(args), stream), name)
-            return
-        nbytes = getattr(lib(), name + "_workspace_bytes")(ctypes.byref(args))
-        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-        _check(fn(ctypes.byref(args), _ptr(ws), nbytes, stream), name)
-
-
-def _norm_rows(x, weight, what: str):
+def _norm_rows(x, weight, code: int, dev: int, what: str):
     """(rows, cols, degrees): rows are x's last dimension, or, with a weight [4, C], an atom's 16 C features
     (x [..., 16, C] or [..., 16 C])."""
-    if not x.is_cuda or x.dim() < 1:
-        raise EmpError(f"{what} must be a CUDA tensor of rows")
-    cols, degrees = x.shape[-1], 0
-    if weight is not None and weight.dim() == 2:
-        C = weight.shape[1]
-        if weight.shape[0] != 4 or not (cols == 16 * C or (x.dim() >= 2 and tuple(x.shape[-2:]) == (16, C))):
-            raise EmpError(f"weight [4, C] needs {what} [..., 16, C] or [..., 16 C], not {tuple(x.shape)}")
-        cols, degrees = 16 * C, 1
-    elif weight is not None and tuple(weight.shape) != (cols,):
-        raise EmpError(f"weight must have the shape ({cols},) or (4, C), not {tuple(weight.shape)}")
+    if code == 3:
+        raise EmpError(f"{what}: type {x.dtype} is not supported")
+    shape = x.shape
+    cols, degrees = shape[-1], 0
+    if weight is not None:
+        wshape = weight.shape
+        if len(wshape) == 2:
+            C = wshape[1]
+            if wshape[0] != 4 or not (cols == 16 * C or (len(shape) >= 2 and shape[-2] == 16 and cols == C)):
+                raise EmpError(f"weight [4, C] needs {what} [..., 16, C] or [..., 16 C], not {tuple(shape)}")
+            cols, degrees = 16 * C, 1
+        elif wshape != (cols,):
+            raise EmpError(f"weight must have the shape ({cols},) or (4, C), not {tuple(wshape)}")
+        _same(weight, wshape, x.dtype, dev, "weight")
     if cols == 0:
         raise EmpError(f"{what} has rows without elements")
     return x.numel() // cols, cols, degrees
@@ -701,55 +712,58 @@ def mp_rms_norm(x, weight=None, residual=None, eps: float = 1e-6, quantize: bool
     dimension), or [4, C] for node features [N, 16, C] (or rows of 16 C), one weight per degree and channel.
     Returns (y, s), or with quantize (y in float8_e4m3fn, its scale per row (float32), s); s is x itself
     without a residual.  No autograd: mp_rms_norm_grad is the gradient."""
-    torch = _torch()
-    rows, cols, degrees = _norm_rows(x, weight, "x")
-    code = _dtype_code(x.dtype, "x")
-    _on(x.device, x.dtype, weight=weight, residual=residual)
-    _like(residual, x.shape, "residual")
+    dev, code = _row_input(x, "x")
+    torch, L = _T, lib()
+    rows, cols, degrees = _norm_rows(x, weight, code, dev, "x")
     xr, ldx = _as_rows(x, rows, cols)
-    rr, ldr = (None, 0) if residual is None else _as_rows(residual, rows, cols)
-    w = None if weight is None else weight.contiguous()
-    y = torch.empty(x.shape, dtype=torch.float8_e4m3fn if quantize else x.dtype, device=x.device)
-    scale = torch.empty(rows, dtype=torch.float32, device=x.device) if quantize else None
-    s = x if residual is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    a = RmsNormC(rows, cols, code, 3 if quantize else code, degrees, float(eps), _ptr(xr), ldx, _ptr(rr), ldr, _ptr(w),
-                 _ptr(y), cols, _ptr(scale), None if residual is None else _ptr(s), cols)
-    _call("mp_rms_norm", a, x.device)
-    if not quantize:
-        return y, s
-    return y, scale.view(x.shape[:-2] if degrees and x.shape[-1] != cols else x.shape[:-1]), s
+    rr, ldr, s, sp = None, 0, x, None
+    if residual is not None:
+        _same(residual, x.shape, x.dtype, dev, "residual")
+        rr, ldr = _as_rows(residual, rows, cols)
+        s = torch.empty_like(x, memory_format=torch.contiguous_format)
+        sp = s.data_ptr()
+    w = weight if weight is None or weight.is_contiguous() else weight.contiguous()
+    y = torch.empty_like(x, dtype=torch.float8_e4m3fn if quantize else None, memory_format=torch.contiguous_format)
+    scale = torch.empty(x.shape[:-2] if degrees and x.shape[-1] != cols else x.shape[:-1], dtype=torch.float32,
+                        device=x.device) if quantize else None
+    a = RmsNormC(rows, cols, code, 3 if quantize else code, degrees, eps, xr.data_ptr(), ldx, _ptr(rr), ldr, _ptr(w),
+                 y.data_ptr(), cols, _ptr(scale), sp, cols)
+    _check(_launch(L.mp_rms_norm, a, dev), "mp_rms_norm")
+    return (y, scale, s) if quantize else (y, s)
 
 
 def mp_rms_norm_grad(g, s, weight=None, g_s=None, eps: float = 1e-6):
     """Gradient of mp_rms_norm: (g_x, g_weight) from g = dE/dy, the s it returned, and g_s = dE/ds of the
     other uses of s (or None).  g_x is dE/dx and dE/dresidual; g_weight is None without a weight."""
-    torch = _torch()
-    rows, cols, degrees = _norm_rows(s, weight, "s")
-    code = _dtype_code(s.dtype, "s")
-    _on(s.device, s.dtype, weight=weight, g=g, g_s=g_s)
-    _like(g, s.shape, "g")
-    _like(g_s, s.shape, "g_s")
+    dev, code = _row_input(s, "s")
+    torch, L = _T, lib()
+    rows, cols, degrees = _norm_rows(s, weight, code, dev, "s")
+    _same(g, s.shape, s.dtype, dev, "g")
     sr, lds = _as_rows(s, rows, cols)
     gr, ldg = _as_rows(g, rows, cols)
-    tr, ldt = (None, 0) if g_s is None else _as_rows(g_s, rows, cols)
-    w = None if weight is None else weight.contiguous()
-    g_x = torch.empty(s.shape, dtype=s.dtype, device=s.device)
-    g_w = None if weight is None else torch.empty(weight.shape, dtype=s.dtype, device=s.device)
-    a = RmsNormGradC(rows, cols, code, degrees, float(eps), _ptr(gr), ldg, _ptr(sr), lds, _ptr(tr), ldt, _ptr(w),
-                     _ptr(g_x), cols, _ptr(g_w))
-    _call("mp_rms_norm_grad", a, s.device)
+    tr, ldt = None, 0
+    if g_s is not None:
+        _same(g_s, s.shape, s.dtype, dev, "g_s")
+        tr, ldt = _as_rows(g_s, rows, cols)
+    w = weight if weight is None or weight.is_contiguous() else weight.contiguous()
+    g_x = torch.empty_like(s, memory_format=torch.contiguous_format)
+    g_w = None if w is None else torch.empty_like(w)
+    a = RmsNormGradC(rows, cols, code, degrees, eps, gr.data_ptr(), ldg, sr.data_ptr(), lds, _ptr(tr), ldt, _ptr(w),
+                     g_x.data_ptr(), cols, _ptr(g_w))
+    _check(_launch(L.mp_rms_norm_grad, a, dev, L.mp_rms_norm_grad_workspace_bytes), "mp_rms_norm_grad")
     return g_x, g_w
 
 
-def _dense_shapes(x, weight, activation):
-    if not x.is_cuda or x.dim() < 1 or weight.dim() != 2 or x.shape[-1] != weight.shape[1]:
-        raise EmpError(f"x [..., K] and weight [N, K] must agree: {tuple(x.shape)}, {tuple(weight.shape)}")
-    if activation not in _ACTIVATIONS:
+def _dense_shapes(x, weight, activation, dev: int):
+    wshape = weight.shape
+    if len(wshape) != 2 or x.shape[-1] != wshape[1] or wshape[0] == 0 or wshape[1] == 0:
+        raise EmpError(f"x [..., K] and weight [N, K] must agree: {tuple(x.shape)}, {tuple(wshape)}")
+    _same(weight, wshape, x.dtype, dev, "weight")
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
         raise EmpError(f"activation must be one of {sorted(_ACTIVATIONS)}")
-    N, K = weight.shape
-    if K == 0 or N == 0:
-        raise EmpError("weight has no elements")
-    return x.numel() // K, K, N
+    N, K = wshape
+    return x.numel() // K, K, N, act
 
 
 def mp_dense(x, weight, bias=None, activation: str = "none", residual=None, x_scale=None, w_scale=None, out_dtype=None,
@@ -761,35 +775,36 @@ def mp_dense(x, weight, bias=None, activation: str = "none", residual=None, x_sc
     bias [N] (float32 for 8-bit inputs, else x's type); residual [..., N] and y are of x's type, or for 8-bit
     inputs of out_dtype (bfloat16 unless given).  activation: "none", "silu", "gelu".  keep_z: returns
     (y, z) with z = x W^T + bias, which mp_dense_grad takes.  No autograd."""
-    torch = _torch()
-    rows, K, N = _dense_shapes(x, weight, activation)
-    code = _dtype_code(x.dtype, "x", e4m3=True)
+    dev, code = _row_input(x, "x")
+    torch, L = _T, lib()
+    rows, K, N, act = _dense_shapes(x, weight, activation, dev)
+    out, ycode = x.dtype, code
     if code == 3:
         out = torch.bfloat16 if out_dtype is None else out_dtype
+        ycode = _CODES.get(out, 3)
+        if ycode == 3:
+            raise EmpError(f"out_dtype: type {out} is not supported")
         if x_scale is None or w_scale is None:
             raise EmpError("8-bit inputs need x_scale and w_scale")
-    else:
-        out = x.dtype if out_dtype is None else out_dtype
-        if out != x.dtype or x_scale is not None or w_scale is not None:
-            raise EmpError("out_dtype and scales are for 8-bit inputs")
-    ycode = _dtype_code(out, "out_dtype")
-    _on(x.device, x.dtype, weight=weight)
-    _on(x.device, torch.float32 if code == 3 else x.dtype, bias=bias)
-    _on(x.device, torch.float32, x_scale=x_scale, w_scale=w_scale)
-    _on(x.device, out, residual=residual)
-    shape = (*x.shape[:-1], N)
-    _like(residual, shape, "residual")
-    _like(x_scale, x.shape[:-1], "x_scale")
-    bias, w_scale = _vector(bias, N, "bias"), _vector(w_scale, N, "w_scale")
-    xs = None if x_scale is None else x_scale.contiguous()
+        _same(x_scale, x.shape[:-1], torch.float32, dev, "x_scale")
+        w_scale = _vector(w_scale, N, torch.float32, dev, "w_scale")
+        x_scale = x_scale if x_scale.is_contiguous() else x_scale.contiguous()
+    elif x_scale is not None or w_scale is not None or (out_dtype is not None and out_dtype != out):
+        raise EmpError("out_dtype and scales are for 8-bit inputs")
+    if bias is not None:
+        bias = _vector(bias, N, torch.float32 if code == 3 else out, dev, "bias")
+    shape = x.shape[:-1] + (N,)
     xr, ldx = _as_rows(x, rows, K)
     wr, ldw = _as_rows(weight, N, K)
-    rr, ldr = (None, 0) if residual is None else _as_rows(residual, rows, N)
+    rr, ldr = None, 0
+    if residual is not None:
+        _same(residual, shape, out, dev, "residual")
+        rr, ldr = _as_rows(residual, rows, N)
     y = torch.empty(shape, dtype=out, device=x.device)
-    z = torch.empty(shape, dtype=out, device=x.device) if keep_z else None
-    a = DenseC(rows, K, N, code, ycode, _ACTIVATIONS[activation], _ptr(xr), ldx, _ptr(xs), _ptr(wr), ldw, _ptr(w_scale),
-               _ptr(bias), _ptr(rr), ldr, _ptr(y), N, _ptr(z), N)
-    _call("mp_dense", a, x.device)
+    z = torch.empty_like(y) if keep_z else None
+    a = DenseC(rows, K, N, code, ycode, act, xr.data_ptr(), ldx, _ptr(x_scale), wr.data_ptr(), ldw, _ptr(w_scale), _ptr(bias),
+               _ptr(rr), ldr, y.data_ptr(), N, _ptr(z), N)
+    _check(_launch(L.mp_dense, a, dev, L.mp_dense_workspace_bytes), "mp_dense")
     return (y, z) if keep_z else y
 
 
@@ -798,22 +813,26 @@ def mp_dense_grad(g, x, weight, z=None, activation: str = "none", need_x: bool =
     """Gradient of mp_dense: (g_x, g_weight, g_bias) from g = dE/dy [..., N] (also dE/dresidual), the layer's
     x [..., K] and weight [N, K], and with an activation the z that mp_dense(keep_z=True) returned.  What is
     not needed is not computed and comes back as None.  Types are x's: float32, bfloat16 or float16."""
-    torch = _torch()
-    rows, K, N = _dense_shapes(x, weight, activation)
-    code = _dtype_code(x.dtype, "x")
-    if (z is None) != (activation == "none"):
+    dev, code = _row_input(x, "x")
+    torch, L = _T, lib()
+    rows, K, N, act = _dense_shapes(x, weight, activation, dev)
+    if code == 3:
+        raise EmpError("8-bit inputs have no gradient")
+    if (z is None) != (act == 0):
         raise EmpError("z goes with an activation")
-    _on(x.device, x.dtype, weight=weight, g=g, z=z)
-    shape = (*x.shape[:-1], N)
-    _like(g, shape, "g")
-    _like(z, shape, "z")
+    shape = x.shape[:-1] + (N,)
+    _same(g, shape, x.dtype, dev, "g")
     gr, ldg = _as_rows(g, rows, N)
-    zr, ldz = (None, 0) if z is None else _as_rows(z, rows, N)
+    zr, ldz = None, 0
+    if z is not None:
+        _same(z, shape, x.dtype, dev, "z")
+        zr, ldz = _as_rows(z, rows, N)
     xr, ldx = _as_rows(x, rows, K)
     wr, ldw = _as_rows(weight, N, K)
-    new = lambda s, need: torch.empty(s, dtype=x.dtype, device=x.device) if need else None  # noqa: E731
-    g_x, g_w, g_b = new(x.shape, need_x), new((N, K), need_weight), new((N,), need_bias)
-    a = DenseGradC(rows, K, N, code, _ACTIVATIONS[activation], _ptr(gr), ldg, _ptr(zr), ldz, _ptr(xr), ldx, _ptr(wr), ldw,
+    g_x = torch.empty_like(x, memory_format=torch.contiguous_format) if need_x else None
+    g_w = torch.empty_like(weight, memory_format=torch.contiguous_format) if need_weight else None
+    g_b = torch.empty(N, dtype=x.dtype, device=x.device) if need_bias else None
+    a = DenseGradC(rows, K, N, code, act, gr.data_ptr(), ldg, _ptr(zr), ldz, xr.data_ptr(), ldx, wr.data_ptr(), ldw,
                    _ptr(g_x), K, _ptr(g_w), _ptr(g_b))
-    _call("mp_dense_grad", a, x.device)
+    _check(_launch(L.mp_dense_grad, a, dev, L.mp_dense_grad_workspace_bytes), "mp_dense_grad")
     return g_x, g_w, g_b
