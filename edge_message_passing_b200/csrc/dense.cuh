@@ -90,14 +90,27 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) k_dense_few(const Few p, const
 }
 
 // ------------------------------------------------------------------ operands TMA cannot read
-// Rows whose start or pitch is not a multiple of 16 bytes are copied once to rows that are.
-template <typename B>
-__global__ void k_pack(long long rows, int cols, const B* __restrict__ src, long long ld, B* __restrict__ dst, long long ldd) {
-  const long long total = rows * cols;
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long long)gridDim.x * blockDim.x) {
-    const long long r = i / cols;
-    const int c = (int)(i - r * cols);
-    dst[r * ldd + c] = src[r * ld + c];
+// Rows whose start or pitch is not a multiple of 16 bytes are copied once to rows that are.  A thread
+// writes 16 bytes, put together by funnel shifts from the (up to five) aligned words that hold them; words
+// past the row's last byte are not read.  x: 16-byte chunks of a row, y: rows.
+__global__ void __launch_bounds__(256) k_pack(long long rows, int row_bytes, const unsigned char* __restrict__ src, long long pitch,
+                                              unsigned char* __restrict__ dst, long long pitch_d) {
+  const int chunk = blockIdx.x * 32 + threadIdx.x;
+  if (chunk * 16 >= row_bytes) return;
+  for (long long r = (long long)blockIdx.y * 8 + threadIdx.y; r < rows; r += (long long)gridDim.y * 8) {
+    const unsigned char* s = src + r * pitch + chunk * 16;
+    const unsigned char* end = src + r * pitch + row_bytes;
+    const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(s) & 3);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(s - off);
+    uint32_t v[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) v[i] = reinterpret_cast<const unsigned char*>(w + i) < end ? w[i] : 0u;
+    uint4 o;
+    o.x = __funnelshift_r(v[0], v[1], off * 8);
+    o.y = __funnelshift_r(v[1], v[2], off * 8);
+    o.z = __funnelshift_r(v[2], v[3], off * 8);
+    o.w = __funnelshift_r(v[3], v[4], off * 8);
+    *reinterpret_cast<uint4*>(dst + r * pitch_d + chunk * 16) = o;
   }
 }
 
@@ -114,36 +127,70 @@ __global__ void k_join(long long M, int N, int splits, const float* __restrict__
 // ------------------------------------------------------------------ g act'(z) and the bias gradient
 // gz = g act'(z), rounded to the operands' type (it is an operand of both products, which take that
 // type), and part[block][n] = the block's column sums of the unrounded values (bias gradient).
-constexpr int GZ_ROWS = 8;
+// A warp takes 32 V neighbouring columns of every 8 gridDim.x-th row, GZ_BATCH rows' loads at a time.
+// Bound by HBM: g and z in, gz out.
+constexpr int GZ_WARPS = 8, GZ_BATCH = 4;
 struct GzArgs {
   long long rows;
-  int cols, dtype, act;
+  int cols, act;
   const void *g, *z;
   long long ldg, ldz, ldo;
-  void* gz;                    // null without an activation
+  void* gz;                    // null: the bias gradient alone
   float* part;                 // null without a bias gradient
 };
-__global__ void __launch_bounds__(32 * GZ_ROWS) k_dense_gz(const GzArgs p) {
-  __shared__ float sm[GZ_ROWS][33];
-  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
-  const int c = blockIdx.y * 32 + lane;
-  float s = 0.f;
-  if (c < p.cols)
-    for (long long m = (long long)blockIdx.x * GZ_ROWS + r; m < p.rows; m += (long long)gridDim.x * GZ_ROWS) {
-      float v = load_any(p.g, (size_t)(m * p.ldg + c), p.dtype);
-      // a rounded product (no contraction into the sum), so that g_bias has the same bits with and without gz
-      if (p.z) v = __fmul_rn(v, dact_f(p.act, load_any(p.z, (size_t)(m * p.ldz + c), p.dtype)));
-      if (p.gz) store_any(p.gz, (size_t)(m * p.ldo + c), p.dtype, v);
-      s += v;
+template <typename T, int V>
+__global__ void __launch_bounds__(32 * GZ_WARPS) k_dense_gz(const GzArgs p) {
+  __shared__ float sm[GZ_WARPS][32 * V];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c = (blockIdx.y * 32 + lane) * V;
+  float s[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) s[i] = 0.f;
+  if (c < p.cols) {
+    const T* g = static_cast<const T*>(p.g) + c;
+    const T* z = static_cast<const T*>(p.z) + c;
+    T* o = static_cast<T*>(p.gz) + c;
+    const long long step = (long long)gridDim.x * GZ_WARPS;
+    for (long long m0 = (long long)blockIdx.x * GZ_WARPS + w; m0 < p.rows; m0 += GZ_BATCH * step) {
+      float a[GZ_BATCH][V], b[GZ_BATCH][V];
+#pragma unroll
+      for (int k = 0; k < GZ_BATCH; ++k) {
+        const long long m = m0 + k * step;
+#pragma unroll
+        for (int i = 0; i < V; ++i) a[k][i] = b[k][i] = 0.f;
+        if (m < p.rows) {
+          load_v<T, V>(g + m * p.ldg, a[k]);
+          if (p.z) load_v<T, V>(z + m * p.ldz, b[k]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < GZ_BATCH; ++k) {
+        const long long m = m0 + k * step;
+        if (m >= p.rows) break;
+        // a rounded product (no contraction into the sum), so that g_bias has the same bits with and without gz
+        if (p.act == EMP_ACT_SILU) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) a[k][i] = __fmul_rn(a[k][i], dsilu_fast(b[k][i]));
+        } else if (p.act == EMP_ACT_GELU) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) a[k][i] = __fmul_rn(a[k][i], dact_f(EMP_ACT_GELU, b[k][i]));
+        }
+        if (p.gz) store_v<T, V>(o + m * p.ldo, a[k]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] += a[k][i];
+      }
     }
+  }
   if (!p.part) return;
-  sm[r][lane] = s;
+#pragma unroll
+  for (int i = 0; i < V; ++i) sm[w][i * 32 + lane] = s[i];
   __syncthreads();
-  if (r == 0 && c < p.cols) {
+  for (int j = threadIdx.x; j < 32 * V; j += 32 * GZ_WARPS) {
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < GZ_ROWS; ++i) t += sm[i][lane];
-    p.part[(size_t)blockIdx.x * p.cols + c] = t;
+    for (int i = 0; i < GZ_WARPS; ++i) t += sm[i][j];
+    const int col = (blockIdx.y * 32 + (j & 31)) * V + (j >> 5);
+    if (col < p.cols) p.part[(size_t)blockIdx.x * p.cols + col] = t;
   }
 }
 

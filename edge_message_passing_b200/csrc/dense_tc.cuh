@@ -39,10 +39,10 @@ constexpr int SPLIT_GROUPS = 2, SPLIT_WARPS = 4 * SPLIT_GROUPS;
 constexpr int A_BYTES = BM * 128;                       // one stage of A
 constexpr int MAX_STAGES = 8;
 constexpr int RING_BYTES = 4 * (A_BYTES + 256 * 128);   // 192 KB: four stages of 128 x 256 tiles
-constexpr int LAND = 3;                                 // FP32: stages as they land ...
+constexpr int LAND = 4;                                 // FP32: stages as they land (a multiple of the split groups) ...
 constexpr int LAND_BYTES = 2 * A_BYTES;
 constexpr int HL_BYTES = 2 * A_BYTES;                   // ... and B's hi and lo, a slot per split group
-static_assert(LAND * LAND_BYTES + SPLIT_GROUPS * HL_BYTES <= RING_BYTES, "FP32 rings");
+static_assert(LAND * LAND_BYTES + SPLIT_GROUPS * HL_BYTES <= RING_BYTES && LAND % SPLIT_GROUPS == 0, "FP32 rings");
 constexpr int STAGING = EPI_WARPS * 32 * 32 * 4;        // a 32 x 32 tile per epilogue warp
 constexpr int BAR_BYTES = 512;
 constexpr int SMEM = 1024 + RING_BYTES + STAGING + BAR_BYTES;
@@ -59,7 +59,6 @@ struct Plan {
   int kind;                                      // 0: f16 / bf16, 1: e4m3
   uint32_t idesc;
   float* part;                                   // [splits][M][N] or null
-  int vec;                                       // rows of y, z and residual allow 16-byte accesses
 };
 
 __device__ __forceinline__ uint64_t sdesc_mn(uint32_t addr, uint32_t chunk_bytes) {
@@ -83,16 +82,23 @@ __device__ __forceinline__ void mma_tf32_ts(uint32_t d, uint32_t a, uint64_t b, 
 __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
       ::"r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
-        "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]),
-        "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]),
-        "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+        "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr) : "memory");
 }
 
 // 32 k of row r of a landed FP32 stage: k-major rows of 128 bytes (128-byte swizzle), or mn-major,
@@ -112,76 +118,98 @@ __device__ __forceinline__ void read_row(const unsigned char* src, int r, int mn
 }
 
 // ------------------------------------------------------------------ rows of a 32 x 32 tile
-// v: the accumulator's row m0 + lane, columns n0 .. n0 + 31.  The tile is turned through the warp's staging
-// (16-byte chunks XORed with the row) so that a row's lanes access whole segments of memory.
-template <typename T>
-__device__ __forceinline__ void out_vec(const dense::Epi& e, long long M, int N, long long m0, int n0, const float* stg, int lane) {
-  constexpr int V = 16 / sizeof(T), L = 32 / V;          // elements and lanes of a row segment
-  const int c = (lane % L) * V, n = n0 + c;
-  if (n >= N) return;                                    // N is a multiple of V
-  float b[V], ws[V];
+// The accumulator comes a row per lane.  The tile is turned through the warp's staging (16-byte chunks
+// XORed with the row), so that the lanes of a row then access a whole segment of memory: V elements
+// each, 16 bytes, or single elements where rows are not 16-byte aligned.  What the epilogue reads of memory
+// (Ahead) is loaded a tile ahead of its use, eight passes of rows at once; the FP32 kernel, whose sums
+// take 64 registers, loads four passes at a time when they are needed.
+template <typename T, int V, int MOST>
+struct Ahead {
+  static constexpr int L = 32 / V, RP = 32 / L, PASSES = 32 / RP;   // lanes of a row segment, rows of a pass
+  static constexpr int B = PASSES < MOST ? PASSES : MOST;           // passes whose loads are in flight together
+  T res[B][V];
+  float xs[B];
+};
+
+template <typename T, int V, bool SCALED, int MOST>
+struct Out {
+  using A = Ahead<T, V, MOST>;
+  static constexpr int L = A::L, RP = A::RP, B = A::B;
+
+  static __device__ __forceinline__ void load(A& h, const dense::Epi& e, int rows, long long m0, int n, int N, int k0, int lane) {
+    const int r0 = k0 * RP + lane / L;
+    if (SCALED) {
+      const float* xs = e.x_scale + m0 + r0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    b[i] = e.bias ? load_any(e.bias, n + i, e.bias_dtype) : 0.f;
-    ws[i] = e.w_scale ? e.w_scale[n + i] : 1.f;
-  }
-#pragma unroll
-  for (int k = 0; k < 32; k += 32 / L) {
-    const int r = k + lane / L;
-    const long long m = m0 + r;
-    if (m >= M) break;
-    float v[V];
-#pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const float4 a = *reinterpret_cast<const float4*>(stg + r * 32 + (((c + i) / 4) ^ (r & 7)) * 4);
-      v[i] = a.x; v[i + 1] = a.y; v[i + 2] = a.z; v[i + 3] = a.w;
-    }
-    if (e.x_scale) {
-      const float xs = e.x_scale[m];
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] *= xs * ws[i];
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] += b[i];
-    if (e.z) store_v<T, V>(static_cast<T*>(e.z) + m * e.ldz + n, v);
-    if (e.act == EMP_ACT_SILU) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = silu_fast(v[i]);
-    } else if (e.act == EMP_ACT_GELU) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = act_f(EMP_ACT_GELU, v[i]);
+      for (int k = 0; k < B; ++k) h.xs[k] = r0 + k * RP < rows ? xs[k * RP] : 0.f;
     }
     if (e.residual) {
-      float a[V];
-      load_v<T, V>(static_cast<const T*>(e.residual) + m * e.ldr + n, a);
+      const T* res = static_cast<const T*>(e.residual) + (m0 + r0) * e.ldr + n;
+      const long long step = RP * e.ldr;
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] += a[i];
+      for (int k = 0; k < B; ++k, res += step) {
+        if (r0 + k * RP < rows && n < N) {
+          if constexpr (V == 1) h.res[k][0] = *res;
+          else *reinterpret_cast<uint4*>(h.res[k]) = *reinterpret_cast<const uint4*>(res);
+        }
+      }
     }
-    store_v<T, V>(static_cast<T*>(e.y) + m * e.ldy + n, v);
   }
-}
 
-__device__ __forceinline__ void out_tile(const Plan& p, const dense::Epi& e, int split, long long m0, int n0, const float (&v)[32],
-                                         float* stg, int lane) {
+  // passes k0 .. k0 + B of the staged tile
+  static __device__ __forceinline__ void store(const A& h, const dense::Epi& e, int rows, long long m0, int n, int N, int k0,
+                                               const float (&b)[V], const float (&ws)[V], const float* stg, int lane) {
+    if (n >= N) return;                                   // V > 1: N is a multiple of V
+    const int c = (lane % L) * V, r0 = k0 * RP + lane / L;
+    T* y = static_cast<T*>(e.y) + (m0 + r0) * e.ldy + n;
+    T* z = static_cast<T*>(e.z) + (m0 + r0) * e.ldz + n;
+    const long long ystep = RP * e.ldy, zstep = RP * e.ldz;
+#pragma unroll
+    for (int k = 0; k < B; ++k, y += ystep, z += zstep) {
+      const int r = r0 + k * RP;
+      if (r >= rows) break;
+      float v[V];
+      if constexpr (V == 1) {
+        v[0] = stg[r * 32 + (((c >> 2) ^ (r & 7)) << 2) + (c & 3)];
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+          const float4 a = *reinterpret_cast<const float4*>(stg + r * 32 + (((c + i) / 4) ^ (r & 7)) * 4);
+          v[i] = a.x; v[i + 1] = a.y; v[i + 2] = a.z; v[i + 3] = a.w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = SCALED ? fmaf(v[i], h.xs[k] * ws[i], b[i]) : v[i] + b[i];
+      if (e.z) store_v<T, V>(z, v);
+      if (e.act == EMP_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = silu_fast(v[i]);
+      } else if (e.act == EMP_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = act_f(EMP_ACT_GELU, v[i]);
+      }
+      if (e.residual) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += to_f(h.res[k][i]);
+      }
+      store_v<T, V>(y, v);
+    }
+  }
+};
+
+// a row per lane (v) into the warp's staging
+__device__ __forceinline__ void stage_rows(const float (&v)[32], float* stg, int lane) {
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     *reinterpret_cast<float4*>(stg + lane * 32 + ((j ^ (lane & 7)) << 2)) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
   __syncwarp();
-  if (p.part) {
-    float* o = p.part + (size_t)split * p.M * p.N;
-    const int n = n0 + lane;
-    if (n < p.N)
-      for (int r = 0; r < 32 && m0 + r < p.M; ++r) o[(size_t)(m0 + r) * p.N + n] = stg[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)];
-  } else if (p.vec) {
-    if (e.y_dtype == EMP_F32) out_vec<float>(e, p.M, p.N, m0, n0, stg, lane);
-    else if (e.y_dtype == EMP_BF16) out_vec<__nv_bfloat16>(e, p.M, p.N, m0, n0, stg, lane);
-    else out_vec<__half>(e, p.M, p.N, m0, n0, stg, lane);
-  } else {
-    const int n = n0 + lane;
-    if (n < p.N)
-      for (int r = 0; r < 32 && m0 + r < p.M; ++r) dense::put_one(e, m0 + r, n, stg[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)]);
-  }
-  __syncwarp();
+}
+__device__ __forceinline__ void store_part(float* o, long long M, int N, long long m0, int n0, const float* stg, int lane) {
+  const int n = n0 + lane, rows = (int)(M - m0 < 32 ? M - m0 : 32);
+  if (n >= N) return;
+  o += m0 * N + n;
+#pragma unroll 8
+  for (int r = 0; r < rows; ++r, o += N) *o = stg[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)];
 }
 
 struct Item {
@@ -200,9 +228,9 @@ __device__ __forceinline__ Item item_at(const Plan& p, long long w) {
   return t;
 }
 
-template <bool SPLIT>
+template <bool SPLIT, typename T, int V, bool SCALED>
 __global__ void __launch_bounds__(threads(SPLIT), 1)
-    k_dense_tc(const Plan p, const dense::Epi e, const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb) {
+    k_dense_tc(const __grid_constant__ Plan p, const __grid_constant__ dense::Epi e, const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb) {
   extern __shared__ __align__(1024) unsigned char dtc_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dtc_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* hl = sm + LAND * LAND_BYTES;                           // FP32: B's hi and lo
@@ -326,15 +354,57 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
     tc::mbar_wait(drain, 0);
   } else if (warp >= 2 && warp < 2 + EPI_WARPS) {
     // ---------------------------------------------------------------- epilogue
+    using O = Out<T, V, SCALED, SPLIT ? 4 : 8>;
     const int q = warp & 3, half = (warp - 2) >> 2;          // TMEM lanes q * 32 ..; chunks half, half + 2, ...
     float* stg = staging + (warp - 2) * 32 * 32;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     const int nch = p.bn / 32;
+    const int cl = (lane % O::L) * V;
+    typename O::A ahead;
+    float bias[V], ws[V];
+    // what the epilogue of chunk c of an item reads
+    auto fetch = [&](const Item& t, int c) {
+      const long long m0 = t.m0 + q * 32;
+      const int n = t.n0 + c * 32 + cl;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        bias[i] = ws[i] = 0.f;
+        if (n < p.N) {
+          if (e.bias) bias[i] = SCALED ? static_cast<const float*>(e.bias)[n + i] : to_f(static_cast<const T*>(e.bias)[n + i]);
+          if (SCALED) ws[i] = e.w_scale[n + i];
+        }
+      }
+      O::load(ahead, e, (int)min((long long)32, p.M - m0), m0, n, p.N, 0, lane);
+    };
+    // the staged chunk c of an item; fetches chunk `next` of item tn in between
+    auto put = [&](const Item& t, int c, const Item& tn, int next) {
+      const long long m0 = t.m0 + q * 32;
+      const int n = t.n0 + c * 32 + cl, rows = (int)min((long long)32, p.M - m0);
+      if (p.part) {
+        store_part(p.part + (size_t)t.split * p.M * p.N, p.M, p.N, m0, t.n0 + c * 32, stg, lane);
+      } else {
+        if (SPLIT) fetch(t, c);
+        typename O::A h = ahead;
+        float b[V], w[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) { b[i] = bias[i]; w[i] = ws[i]; }
+        if (!SPLIT && next >= 0) fetch(tn, next);
+        O::store(h, e, rows, m0, n, p.N, 0, b, w, stg, lane);
+#pragma unroll 1
+        for (int k0 = O::B; k0 < O::A::PASSES; k0 += O::B) {
+          O::load(h, e, rows, m0, n, p.N, k0, lane);
+          O::store(h, e, rows, m0, n, p.N, k0, b, w, stg, lane);
+        }
+      }
+      __syncwarp();
+    };
     long long ch = 0;
     bool ok = true;
+    if (!SPLIT && !p.part && blockIdx.x < p.items) fetch(item_at(p, blockIdx.x), half);
     for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x) {
       const Item t = item_at(p, w);
-      const long long m0 = t.m0 + q * 32;
+      const bool more = w + gridDim.x < p.items;
+      const Item tn = more ? item_at(p, w + gridDim.x) : t;
       if (SPLIT) {
         float acc[2][32];
 #pragma unroll
@@ -346,10 +416,13 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             if (half + 2 * c < nch) {
-              float v[32];
-              tc::tmem_ld32(lanes + (uint32_t)(buf * 128 + (half + 2 * c) * 32), v);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) acc[c][i] += v[i];
+              for (int j = 0; j < 32; j += 16) {
+                float v[16];
+                tmem_ld16(lanes + (uint32_t)(buf * 128 + (half + 2 * c) * 32 + j), v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[c][j + i] += v[i];
+              }
             }
           }
           tc::fence_before();
@@ -359,7 +432,11 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
         if (!ok) break;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          if (half + 2 * c < nch) out_tile(p, e, t.split, m0, t.n0 + (half + 2 * c) * 32, acc[c], stg, lane);
+          if (half + 2 * c < nch) {
+            stage_rows(acc[c], stg, lane);
+            const bool last = half + 2 * c + 2 >= nch;
+            put(t, half + 2 * c, last ? tn : t, last ? (more ? half : -1) : half + 2 * c + 2);
+          }
       } else {
         const int buf = (int)(ch & 1);
         if (!__all_sync(0xffffffffu, tc::mbar_wait(&acc_full[buf], (uint32_t)((ch >> 1) & 1)))) break;
@@ -368,12 +445,14 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
         for (int c = half; c < nch; c += 2) {
           float v[32];
           tc::tmem_ld32(lanes + (uint32_t)(buf * 256 + c * 32), v);
-          if (c + 2 >= nch) {                                // the last read of this accumulator
+          const bool last = c + 2 >= nch;
+          if (last) {                                        // the last read of this accumulator
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&acc_empty[buf]);
           }
-          out_tile(p, e, t.split, m0, t.n0 + c * 32, v, stg, lane);
+          stage_rows(v, stg, lane);
+          put(t, c, last ? tn : t, last ? (more ? half : -1) : c + 2);
         }
         ++ch;
       }
@@ -392,36 +471,40 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
         if (it % SPLIT_GROUPS != g) continue;
         const int s = (int)(it % LAND);
         const long long u = it / SPLIT_GROUPS;
-        // first this group's slot (its stage it - 2 multiplied, hence every stage up to it - 2 read), then the
-        // landing: stage it - 3, the one before in the same place, has then landed, and the parity is unambiguous
-        if (u >= 1 && !__all_sync(0xffffffffu, tc::mbar_wait(&sempty[g], (uint32_t)((u - 1) & 1)))) { ok = false; break; }
+        // a landing place always has the same reader group (LAND is a multiple of the groups), so a phase's
+        // parity is unambiguous; the stage is read, and its place freed, before the wait for the MMAs
         if (!__all_sync(0xffffffffu, tc::mbar_wait(&full[s], (uint32_t)((it / LAND) & 1)))) { ok = false; break; }
-        tc::fence_after();
         const unsigned char* land = sm + s * LAND_BYTES;
-        float v[32], h[32];
+        float v[32], x[32];
         read_row(land, r, p.a_mn, BM, v);
+        if (r < p.bn) read_row(land + A_BYTES, r, p.b_mn, p.bn, x);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&empty[s]);
+        if (u >= 1 && !__all_sync(0xffffffffu, tc::mbar_wait(&sempty[g], (uint32_t)((u - 1) & 1)))) { ok = false; break; }
+        tc::fence_after();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) h[i] = tf32_rna(v[i]);
-        tmem_st32(ta, h);
+        for (int j = 0; j < 32; j += 16) {
+          float h[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = tf32_rna(v[i] - h[i]);
-        tmem_st32(ta + 32, v);
+          for (int i = 0; i < 16; ++i) h[i] = tf32_rna(v[j + i]);
+          tmem_st16(ta + j, h);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) h[i] = tf32_rna(v[j + i] - h[i]);
+          tmem_st16(ta + 32 + j, h);
+        }
         if (r < p.bn) {
-          read_row(land + A_BYTES, r, p.b_mn, p.bn, v);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             float4 hi, lo;
-            hi.x = tf32_rna(v[4 * j]);     lo.x = tf32_rna(v[4 * j] - hi.x);
-            hi.y = tf32_rna(v[4 * j + 1]); lo.y = tf32_rna(v[4 * j + 1] - hi.y);
-            hi.z = tf32_rna(v[4 * j + 2]); lo.z = tf32_rna(v[4 * j + 2] - hi.z);
-            hi.w = tf32_rna(v[4 * j + 3]); lo.w = tf32_rna(v[4 * j + 3] - hi.w);
+            hi.x = tf32_rna(x[4 * j]);     lo.x = tf32_rna(x[4 * j] - hi.x);
+            hi.y = tf32_rna(x[4 * j + 1]); lo.y = tf32_rna(x[4 * j + 1] - hi.y);
+            hi.z = tf32_rna(x[4 * j + 2]); lo.z = tf32_rna(x[4 * j + 2] - hi.z);
+            hi.w = tf32_rna(x[4 * j + 3]); lo.w = tf32_rna(x[4 * j + 3] - hi.w);
             const int o = r * 128 + ((j ^ (r & 7)) << 4);
             *reinterpret_cast<float4*>(bhi + o) = hi;
             *reinterpret_cast<float4*>(bhi + A_BYTES + o) = lo;
           }
         }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&empty[s]);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc::fence_before();
@@ -492,6 +575,28 @@ struct Operand {
   long long ld;
   int mn;
 };
+struct Launch {
+  const Plan& p;
+  const dense::Epi& e;
+  const CUtensorMap &ma, &mb;
+  unsigned grid;
+  cudaStream_t st;
+  template <bool SPLIT, typename T, int V, bool SCALED>
+  int go() const {
+    auto k = k_dense_tc<SPLIT, T, V, SCALED>;
+    // the shared-memory limit is set once per device and kernel
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    EMP_CUDA_TRY(cudaGetDevice(&dev));
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev > 63 || !(done.load() & bit)) {
+      EMP_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM));
+      done.fetch_or(bit);
+    }
+    k<<<grid, threads(SPLIT), SMEM, st>>>(p, e, ma, mb);
+    return cudaGetLastError() == cudaSuccess ? EMP_OK : EMP_ERR_CUDA;
+  }
+};
 inline int launch(long long M, int N, long long K, int t, const Operand& a, const Operand& b, const dense::Epi& e, const Shape& h,
                   float* part, bool vec, cudaStream_t st) {
   const int es = dtype_size(t), kw = 128 / es;
@@ -506,28 +611,23 @@ inline int launch(long long M, int N, long long K, int t, const Operand& a, cons
   p.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(h.bn >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
   if (!split) p.idesc |= ((uint32_t)a.mn << 15) | ((uint32_t)b.mn << 16);
   p.part = part;
-  p.vec = vec;
   CUtensorMap ma, mb;
   const bool ok_a = a.mn ? make_map(&ma, a.p, t, M, K, a.ld, split ? BM : 64, kw, !split) : make_map(&ma, a.p, t, K, M, a.ld, kw, BM, true);
   const bool ok_b = b.mn ? make_map(&mb, b.p, t, N, K, b.ld, split ? h.bn : 64, kw, !split) : make_map(&mb, b.p, t, K, N, b.ld, kw, h.bn, true);
   if (!ok_a || !ok_b) return EMP_ERR_CUDA;
   const unsigned grid = (unsigned)std::min<long long>(p.items, tc::num_sms());
-  if (split) k_dense_tc<true><<<grid, threads(true), SMEM, st>>>(p, e, ma, mb);
-  else k_dense_tc<false><<<grid, threads(false), SMEM, st>>>(p, e, ma, mb);
-  return cudaGetLastError() == cudaSuccess ? EMP_OK : EMP_ERR_CUDA;
-}
-
-// once per device
-inline int init() {
-  static std::atomic<unsigned long long> done{0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || !tc::encode_fn()) return EMP_ERR_UNSUPPORTED;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (dev < 64 && (done.load() & bit)) return EMP_OK;
-  EMP_CUDA_TRY(cudaFuncSetAttribute(k_dense_tc<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM));
-  EMP_CUDA_TRY(cudaFuncSetAttribute(k_dense_tc<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM));
-  done.fetch_or(bit);
-  return EMP_OK;
+  Launch l{p, e, ma, mb, grid, st};
+  if (split) return vec ? l.go<true, float, 4, false>() : l.go<true, float, 1, false>();
+  const bool sc = t == EMP_E4M3;
+  switch (e.y_dtype) {
+    case EMP_F32: return vec ? l.go<false, float, 4, true>() : l.go<false, float, 1, true>();      // of 8-bit inputs only
+    case EMP_BF16:
+      return sc ? (vec ? l.go<false, __nv_bfloat16, 8, true>() : l.go<false, __nv_bfloat16, 1, true>())
+                : (vec ? l.go<false, __nv_bfloat16, 8, false>() : l.go<false, __nv_bfloat16, 1, false>());
+    default:
+      return sc ? (vec ? l.go<false, __half, 8, true>() : l.go<false, __half, 1, true>())
+                : (vec ? l.go<false, __half, 8, false>() : l.go<false, __half, 1, false>());
+  }
 }
 
 }  // namespace dtc

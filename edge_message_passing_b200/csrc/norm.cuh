@@ -38,7 +38,7 @@ struct GradArgs {
   float eps;
   const void *g, *s, *g_s, *w;
   void* g_x;
-  float* part;                 // [gridDim.x][cols] column sums of g n (null: no weight gradient)
+  float* part;                 // [gridDim.x][weights] sums of g n (null: no weight gradient)
   long long ldg, lds, ldgs, ldgx;
 };
 
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm(const Args p) {
 // every row, so its part of g_w stays in registers until the end.
 template <typename T, int V, int SL>
 __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm_grad(const GradArgs p) {
-  extern __shared__ float acc_sm[];              // [cols] when the block has several rows
+  extern __shared__ float acc_sm[];              // [cols] when the block has several rows or there are degrees
   __shared__ float red[2][2][32];
   const int G = blockDim.x, t = threadIdx.x, r = threadIdx.y, R = blockDim.y;
   const int C = p.cols / NCOMP;
@@ -215,7 +215,9 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm_grad(const GradArgs p)
     }
   }
   if (!p.part) return;
-  float* part = p.part + (size_t)blockIdx.x * p.cols;
+  const int nout = p.degrees ? 4 * C : p.cols;
+  float* part = p.part + (size_t)blockIdx.x * nout;
+  const bool direct = R == 1 && !p.degrees;
   // the block's row groups, added in order
   for (int q = 0; q < R; ++q) {
     if (q) __syncthreads();
@@ -226,10 +228,21 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm_grad(const GradArgs p)
       if (c >= p.cols) continue;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float a = q ? acc_sm[c + i] + acc[k][i] : acc[k][i];
-        if (q == R - 1) part[c + i] = a;
-        else acc_sm[c + i] = a;
+        if (direct) part[c + i] = acc[k][i];
+        else acc_sm[c + i] = q ? acc_sm[c + i] + acc[k][i] : acc[k][i];
       }
+    }
+  }
+  if (direct) return;
+  __syncthreads();
+  for (int o = r * G + t; o < nout; o += G * R) {
+    if (!p.degrees) {
+      part[o] = acc_sm[o];
+    } else {                                     // the 2 l + 1 components of degree l
+      const int l = o / C, c = o - l * C;
+      float a = 0.f;
+      for (int q = l * l; q < (l + 1) * (l + 1); ++q) a += acc_sm[q * C + c];
+      part[o] = a;
     }
   }
 }
@@ -288,7 +301,7 @@ inline int grad_blocks(long long rows, int R) { return (int)std::min<long long>(
 
 template <typename T, int V, int SL>
 void launch_grad2(const GradArgs& a, const Shape& h, cudaStream_t st) {
-  k_rms_norm_grad<T, V, SL><<<grad_blocks(a.rows, h.R), dim3(h.G, h.R), h.R > 1 ? a.cols * 4 : 0, st>>>(a);
+  k_rms_norm_grad<T, V, SL><<<grad_blocks(a.rows, h.R), dim3(h.G, h.R), h.R > 1 || a.degrees ? a.cols * 4 : 0, st>>>(a);
 }
 template <typename T>
 Shape grad_shape(const GradArgs& a) {

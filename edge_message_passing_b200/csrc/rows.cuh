@@ -94,37 +94,33 @@ __device__ __forceinline__ float dact_f(int act, float z) {
 }
 
 // ------------------------------------------------------------- join of column sums
-// out[o] = sum over blocks b in order of part[b][j], for every column j that maps to o: j = o without
-// degrees; with degrees, o = (l, c) of [4][C] and the columns (lm, c) of its 2l + 1 components.
-// 32 columns per block, JOIN_WARPS warps over the rows (warp w takes rows w, w + JOIN_WARPS, ...; the
-// warps' sums are added in warp order), so the order is fixed.
-constexpr int JOIN_WARPS = 16;
+// out[j] = sum over b of part[b][j].  32 columns per block, JOIN_WARPS warps over the rows (warp w takes
+// rows w, w + JOIN_WARPS, ..., JOIN_BATCH loads at a time; the warps' sums are added in warp order), so the
+// order is fixed.  Bound by the latency of its few loads.
+constexpr int JOIN_WARPS = 32, JOIN_BATCH = 10;
 __global__ void __launch_bounds__(32 * JOIN_WARPS)
-    k_col_join(int nb, int cols, int nout, int degrees, const float* __restrict__ part, void* __restrict__ out, int dtype) {
+    k_col_join(int nb, int cols, const float* __restrict__ part, void* __restrict__ out, int dtype) {
   __shared__ float sm[JOIN_WARPS][33];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int o = blockIdx.x * 32 + lane;
+  const int j = blockIdx.x * 32 + lane;
   float s = 0.f;
-  if (o < nout) {
-    int first = o, count = 1, step = 0;
-    if (degrees) {
-      const int C = cols / NCOMP, l = o / C, c = o % C;
-      first = l * l * C + c;
-      count = 2 * l + 1;
-      step = C;
+  for (int b0 = w; b0 < nb; b0 += JOIN_WARPS * JOIN_BATCH) {
+    float v[JOIN_BATCH];
+#pragma unroll
+    for (int i = 0; i < JOIN_BATCH; ++i) {
+      const int b = b0 + i * JOIN_WARPS;
+      v[i] = b < nb && j < cols ? part[(size_t)b * cols + j] : 0.f;
     }
-    for (int b = w; b < nb; b += JOIN_WARPS) {
-      const float* row = part + (size_t)b * cols + first;
-      for (int q = 0; q < count; ++q) s += row[(size_t)q * step];
-    }
+#pragma unroll
+    for (int i = 0; i < JOIN_BATCH; ++i) s += v[i];
   }
   sm[w][lane] = s;
   __syncthreads();
-  if (w == 0 && o < nout) {
+  if (w == 0 && j < cols) {
     float t = 0.f;
 #pragma unroll
     for (int i = 0; i < JOIN_WARPS; ++i) t += sm[i][lane];
-    store_any(out, (size_t)o, dtype, t);
+    store_any(out, (size_t)j, dtype, t);
   }
 }
 

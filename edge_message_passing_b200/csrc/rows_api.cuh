@@ -47,12 +47,10 @@ const void* pack(const Packed& k, const void* p, long long ld, long long rows, i
   if (!k.copy) return p;
   void* d = at<char>(ws, k.off);
   Scope sc_("dense_pack", s);
-  const int grid = grid_for(rows * cols, 1024);
-  switch (dtype_size(t)) {
-    case 4: dense::k_pack<<<grid, 256, 0, s>>>(rows, cols, static_cast<const uint32_t*>(p), ld, static_cast<uint32_t*>(d), k.ld); break;
-    case 2: dense::k_pack<<<grid, 256, 0, s>>>(rows, cols, static_cast<const uint16_t*>(p), ld, static_cast<uint16_t*>(d), k.ld); break;
-    default: dense::k_pack<<<grid, 256, 0, s>>>(rows, cols, static_cast<const uint8_t*>(p), ld, static_cast<uint8_t*>(d), k.ld);
-  }
+  const int es = dtype_size(t);
+  const dim3 grid((cols * es + 511) / 512, (unsigned)std::min<long long>((rows + 7) / 8, 4736));
+  dense::k_pack<<<grid, dim3(32, 8), 0, s>>>(rows, cols * es, static_cast<const unsigned char*>(p), ld * es,
+                                             static_cast<unsigned char*>(d), k.ld * es);
   return d;
 }
 
@@ -77,11 +75,26 @@ DenseLayout dense_layout(const emp_dense& a) {
 struct DenseGradLayout {
   size_t gz = 0, colsum = 0, part_x = 0, part_w = 0, total = 0;
   long long ldgz = 0;
+  bool gz_vec = false;           // g and z (and gz) in 16-byte vectors
   bool prep = false;             // gz is written (an activation, or g that TMA cannot read)
   int gz_blocks = 0;
   Packed x, w;
   dtc::Shape hx{}, hw{};
 };
+bool gz_vec(const emp_dense_grad& a, const DenseGradLayout& L) {
+  const int es = dtype_size(a.dtype);
+  auto ok = [&](const void* p, long long ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (a.rows == 1 || ld * es % 16 == 0); };
+  return a.fan_out * es % 16 == 0 && ok(a.g, a.ldg) && ok(a.z, a.ldz);
+}
+template <typename T>
+void dense_gz(const dense::GzArgs& z, int blocks, bool vec, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  const int per = 32 * (vec ? V : 1);
+  const dim3 grid(blocks, (z.cols + per - 1) / per);
+  Scope sc_("dense_gz", s);
+  if (vec) dense::k_dense_gz<T, V><<<grid, 32 * dense::GZ_WARPS, 0, s>>>(z);
+  else dense::k_dense_gz<T, 1><<<grid, 32 * dense::GZ_WARPS, 0, s>>>(z);
+}
 DenseGradLayout dense_grad_layout(const emp_dense_grad& a) {
   DenseGradLayout L{};
   const int es = dtype_size(a.dtype);
@@ -91,7 +104,9 @@ DenseGradLayout dense_grad_layout(const emp_dense_grad& a) {
   L.prep = products && (a.activation != EMP_ACT_NONE || !dtc::tma_ok(a.g, a.rows == 1 ? 0 : a.ldg, a.dtype));
   L.gz = take(L.prep ? (size_t)a.rows * L.ldgz * es : 0);
   if (!L.prep && a.rows > 1) L.ldgz = a.ldg;
-  L.gz_blocks = (int)std::max<long long>(1, std::min<long long>((a.rows + 63) / 64, std::max(1, 592 * 32 / a.fan_out)));
+  L.gz_vec = gz_vec(a, L);
+  const int per = 32 * (L.gz_vec ? 16 / es : 1);             // columns of a block; about four blocks per SM
+  L.gz_blocks = (int)std::max<long long>(1, std::min<long long>((a.rows + 31) / 32, 592 / ((a.fan_out + per - 1) / per)));
   L.colsum = take(a.g_bias ? (size_t)L.gz_blocks * a.fan_out * 4 : 0);
   if (a.g_x) {
     L.w = packed(a.weight, a.ldw, a.fan_out, a.fan_in, a.dtype, take);
@@ -218,7 +233,7 @@ int mp_rms_norm_grad(const emp_rms_norm_grad* a, void* ws, size_t ws_bytes, cuda
   }
   if (a->g_weight) {
     Scope sc_("col_join", stream);
-    k_col_join<<<(nout + 31) / 32, 32 * JOIN_WARPS, 0, stream>>>(blocks, a->cols, nout, a->degrees, p.part, a->g_weight, a->dtype);
+    k_col_join<<<(nout + 31) / 32, 32 * JOIN_WARPS, 0, stream>>>(blocks, nout, p.part, a->g_weight, a->dtype);
   }
   return cudaGetLastError() == cudaSuccess ? EMP_OK : EMP_ERR_CUDA;
 }
@@ -245,8 +260,6 @@ int mp_dense(const emp_dense* a, void* ws, size_t ws_bytes, cudaStream_t stream)
     else dense_few<__nv_fp8_e4m3>(*a, e, stream);
     return cudaGetLastError() == cudaSuccess ? EMP_OK : EMP_ERR_CUDA;
   }
-  st = dtc::init();
-  if (st != EMP_OK) return st;
   const dtc::Operand x{pack(L.x, a->x, a->ldx, a->rows, a->fan_in, a->dtype, ws, stream), L.x.ld, 0};
   const dtc::Operand w{pack(L.w, a->weight, a->ldw, a->fan_out, a->fan_in, a->dtype, ws, stream), L.w.ld, 0};
   return dense_product(a->rows, a->fan_out, a->fan_in, a->dtype, x, w, e, L.h, at<float>(ws, L.part), stream);
@@ -270,16 +283,15 @@ int mp_dense_grad(const emp_dense_grad* a, void* ws, size_t ws_bytes, cudaStream
   if (ws_bytes < L.total) return EMP_ERR_WORKSPACE;
   int st = check_device();
   if (st != EMP_OK) return st;
-  st = dtc::init();
-  if (st != EMP_OK) return st;
   if (L.prep || a->g_bias) {
-    const dense::GzArgs z{a->rows, a->fan_out, a->dtype, a->activation, a->g, a->z, a->ldg, a->ldz, L.ldgz,
+    const dense::GzArgs z{a->rows, a->fan_out, a->activation, a->g, a->z, a->ldg, a->ldz, L.ldgz,
                           L.prep ? at<char>(ws, L.gz) : nullptr, a->g_bias ? at<float>(ws, L.colsum) : nullptr};
-    { Scope sc_("dense_gz", stream);
-      dense::k_dense_gz<<<dim3(L.gz_blocks, (a->fan_out + 31) / 32), 32 * dense::GZ_ROWS, 0, stream>>>(z); }
+    if (a->dtype == EMP_F32) dense_gz<float>(z, L.gz_blocks, L.gz_vec, stream);
+    else if (a->dtype == EMP_BF16) dense_gz<__nv_bfloat16>(z, L.gz_blocks, L.gz_vec, stream);
+    else dense_gz<__half>(z, L.gz_blocks, L.gz_vec, stream);
     if (a->g_bias) {
       Scope sc_("col_join", stream);
-      k_col_join<<<(a->fan_out + 31) / 32, 32 * JOIN_WARPS, 0, stream>>>(L.gz_blocks, a->fan_out, a->fan_out, 0, z.part, a->g_bias, a->dtype);
+      k_col_join<<<(a->fan_out + 31) / 32, 32 * JOIN_WARPS, 0, stream>>>(L.gz_blocks, a->fan_out, z.part, a->g_bias, a->dtype);
     }
   }
   const void* gz = L.prep ? at<char>(ws, L.gz) : static_cast<const char*>(a->g);
