@@ -39,22 +39,25 @@ constexpr int SPLIT_GROUPS = 2, SPLIT_WARPS = 4 * SPLIT_GROUPS;
 constexpr int A_BYTES = BM * 128;                       // one stage of A
 constexpr int MAX_STAGES = 8;
 constexpr int RING_BYTES = 4 * (A_BYTES + 256 * 128);   // 192 KB: four stages of 128 x 256 tiles
-constexpr int LAND = 4;                                 // FP32: stages as they land (a multiple of the split groups) ...
+constexpr int LAND = 3, SLOTS = 3;                      // FP32: stages as they land; split stages (A in TMEM, B's hi and lo here)
 constexpr int LAND_BYTES = 2 * A_BYTES;
-constexpr int HL_BYTES = 2 * A_BYTES;                   // ... and B's hi and lo, a slot per split group
-static_assert(LAND * LAND_BYTES + SPLIT_GROUPS * HL_BYTES <= RING_BYTES && LAND % SPLIT_GROUPS == 0, "FP32 rings");
+constexpr int HL_BYTES = 2 * A_BYTES;
+static_assert(LAND * LAND_BYTES + SLOTS * HL_BYTES <= RING_BYTES, "FP32 rings");
 constexpr int STAGING = EPI_WARPS * 32 * 32 * 4;        // a 32 x 32 tile per epilogue warp
+constexpr int BIAS_BYTES = EPI_WARPS * 32 * 4;          // and its columns' bias
 constexpr int BAR_BYTES = 512;
-constexpr int SMEM = 1024 + RING_BYTES + STAGING + BAR_BYTES;
+constexpr int SMEM = 1024 + RING_BYTES + STAGING + BIAS_BYTES + BAR_BYTES;
 static_assert(SMEM <= 232448, "shared memory of a CTA");
 constexpr int CHUNK_STAGES = 2;                         // FP32: K_CHUNK = 64
 constexpr int A_COL = 256;                              // FP32: TMEM columns of A's slots (64 each: hi, lo)
+static_assert(A_COL + SLOTS * 64 <= 512, "TMEM columns");
 
 __host__ __device__ constexpr int threads(bool split) { return 32 * (2 + EPI_WARPS + (split ? SPLIT_WARPS : 0)); }
 
 struct Plan {
   long long M, items;
   int N, nk, per, bn, mtiles, ntiles, splits;    // nk k-stages, `per` of them per split
+  int step_n, step_m, step_s;                    // the grid's size in tiles of n, m and splits
   int a_mn, b_mn, stages;
   int kind;                                      // 0: f16 / bf16, 1: e4m3
   uint32_t idesc;
@@ -81,6 +84,23 @@ __device__ __forceinline__ void mma_tf32_ts(uint32_t d, uint32_t a, uint64_t b, 
 }
 __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+// Bounded wait.  A waiting warp is put to sleep by the hardware until the phase completes or WAIT_NS have
+// passed: eighteen warps polling would take issue slots from the ones at work.
+constexpr uint32_t WAIT_NS = 20000;
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  do {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}\n"
+                 : "=r"(ok) : "r"(tc::smem_u32(bar)), "r"(parity), "r"(WAIT_NS) : "memory");
+    if (ok) return true;
+  } while (clock64() - t0 <= tc::g_wait_cycles);
+  set_device_error(DEV_ERR_TIMEOUT);
+  return false;
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
   asm volatile(
@@ -118,84 +138,68 @@ __device__ __forceinline__ void read_row(const unsigned char* src, int r, int mn
 }
 
 // ------------------------------------------------------------------ rows of a 32 x 32 tile
-// The accumulator comes a row per lane.  The tile is turned through the warp's staging (16-byte chunks
-// XORed with the row), so that the lanes of a row then access a whole segment of memory: V elements
-// each, 16 bytes, or single elements where rows are not 16-byte aligned.  What the epilogue reads of memory
-// (Ahead) is loaded a tile ahead of its use, eight passes of rows at once; the FP32 kernel, whose sums
-// take 64 registers, loads four passes at a time when they are needed.
-template <typename T, int V, int MOST>
-struct Ahead {
-  static constexpr int L = 32 / V, RP = 32 / L, PASSES = 32 / RP;   // lanes of a row segment, rows of a pass
-  static constexpr int B = PASSES < MOST ? PASSES : MOST;           // passes whose loads are in flight together
-  T res[B][V];
-  float xs[B];
-};
+// The accumulator comes a row per lane.  Where TMA can write the rows of y, a lane finishes its row's 32
+// columns, packs them into the warp's staging (swizzled) and one TMA store writes the tile; the residual
+// comes into the same place by a TMA load beforehand (one chunk ahead of its use for 16-bit types, which
+// have two places), so the epilogue waits for no load and issues no addresses.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t"
+               "cp.async.bulk.commit_group;"
+               ::"l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(src)), "r"(x), "r"(y) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void stores_read() {            // all but the N latest stores have read their place
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
 
-template <typename T, int V, bool SCALED, int MOST>
-struct Out {
-  using A = Ahead<T, V, MOST>;
-  static constexpr int L = A::L, RP = A::RP, B = A::B;
+// 16-byte chunk j of row r of a staged tile: rows of 64 bytes (16-bit types; 64-byte swizzle) or 128 (128-byte)
+template <typename T>
+__device__ __forceinline__ uint4* staged(unsigned char* place, int r, int j) {
+  return reinterpret_cast<uint4*>(sizeof(T) == 4 ? place + r * 128 + ((j ^ (r & 7)) << 4) : place + r * 64 + (((j ^ (r >> 1)) & 3) << 4));
+}
 
-  static __device__ __forceinline__ void load(A& h, const dense::Epi& e, int rows, long long m0, int n, int N, int k0, int lane) {
-    const int r0 = k0 * RP + lane / L;
-    if (SCALED) {
-      const float* xs = e.x_scale + m0 + r0;
+// Where it cannot (rows off 16-byte boundaries), the tile is turned through the staging (16-byte chunks XORed
+// with the row) and a lane takes one column, B rows at a time so that their loads are in flight together.
+template <typename T, bool SCALED>
+__device__ __forceinline__ void put_columns(const dense::Epi& e, long long M, int N, long long m0, int n0, const float* stg, int lane) {
+  constexpr int B = 8;
+  const int n = n0 + lane, rows = (int)min((long long)32, M - m0);
+  if (n >= N) return;
+  float b = 0.f, ws = 1.f;
+  if (e.bias) b = SCALED ? static_cast<const float*>(e.bias)[n] : to_f(static_cast<const T*>(e.bias)[n]);
+  if (SCALED) ws = e.w_scale[n];
+#pragma unroll 1
+  for (int k0 = 0; k0 < rows; k0 += B) {
+    float v[B], res[B], xs[B];
+    const T* rp = static_cast<const T*>(e.residual) + (m0 + k0) * e.ldr + n;
 #pragma unroll
-      for (int k = 0; k < B; ++k) h.xs[k] = r0 + k * RP < rows ? xs[k * RP] : 0.f;
+    for (int k = 0; k < B; ++k, rp += e.ldr) {
+      const int r = k0 + k;
+      res[k] = e.residual && r < rows ? to_f(*rp) : 0.f;
+      xs[k] = SCALED && r < rows ? e.x_scale[m0 + r] : 0.f;
+      v[k] = stg[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)];
     }
-    if (e.residual) {
-      const T* res = static_cast<const T*>(e.residual) + (m0 + r0) * e.ldr + n;
-      const long long step = RP * e.ldr;
 #pragma unroll
-      for (int k = 0; k < B; ++k, res += step) {
-        if (r0 + k * RP < rows && n < N) {
-          if constexpr (V == 1) h.res[k][0] = *res;
-          else *reinterpret_cast<uint4*>(h.res[k]) = *reinterpret_cast<const uint4*>(res);
-        }
-      }
+    for (int k = 0; k < B; ++k) v[k] = SCALED ? fmaf(v[k], xs[k] * ws, b) : v[k] + b;
+    if (e.z) {
+      T* z = static_cast<T*>(e.z) + (m0 + k0) * e.ldz + n;
+#pragma unroll
+      for (int k = 0; k < B; ++k, z += e.ldz)
+        if (k0 + k < rows) *z = from_f<T>(v[k]);
     }
+    if (e.act == EMP_ACT_SILU) {
+#pragma unroll
+      for (int k = 0; k < B; ++k) v[k] = silu_fast(v[k]);
+    } else if (e.act == EMP_ACT_GELU) {
+#pragma unroll
+      for (int k = 0; k < B; ++k) v[k] = act_f(EMP_ACT_GELU, v[k]);
+    }
+    T* y = static_cast<T*>(e.y) + (m0 + k0) * e.ldy + n;
+#pragma unroll
+    for (int k = 0; k < B; ++k, y += e.ldy)
+      if (k0 + k < rows) *y = from_f<T>(v[k] + res[k]);
   }
-
-  // passes k0 .. k0 + B of the staged tile
-  static __device__ __forceinline__ void store(const A& h, const dense::Epi& e, int rows, long long m0, int n, int N, int k0,
-                                               const float (&b)[V], const float (&ws)[V], const float* stg, int lane) {
-    if (n >= N) return;                                   // V > 1: N is a multiple of V
-    const int c = (lane % L) * V, r0 = k0 * RP + lane / L;
-    T* y = static_cast<T*>(e.y) + (m0 + r0) * e.ldy + n;
-    T* z = static_cast<T*>(e.z) + (m0 + r0) * e.ldz + n;
-    const long long ystep = RP * e.ldy, zstep = RP * e.ldz;
-#pragma unroll
-    for (int k = 0; k < B; ++k, y += ystep, z += zstep) {
-      const int r = r0 + k * RP;
-      if (r >= rows) break;
-      float v[V];
-      if constexpr (V == 1) {
-        v[0] = stg[r * 32 + (((c >> 2) ^ (r & 7)) << 2) + (c & 3)];
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; i += 4) {
-          const float4 a = *reinterpret_cast<const float4*>(stg + r * 32 + (((c + i) / 4) ^ (r & 7)) * 4);
-          v[i] = a.x; v[i + 1] = a.y; v[i + 2] = a.z; v[i + 3] = a.w;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[i] = SCALED ? fmaf(v[i], h.xs[k] * ws[i], b[i]) : v[i] + b[i];
-      if (e.z) store_v<T, V>(z, v);
-      if (e.act == EMP_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = silu_fast(v[i]);
-      } else if (e.act == EMP_ACT_GELU) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = act_f(EMP_ACT_GELU, v[i]);
-      }
-      if (e.residual) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] += to_f(h.res[k][i]);
-      }
-      store_v<T, V>(y, v);
-    }
-  }
-};
+}
 
 // a row per lane (v) into the warp's staging
 __device__ __forceinline__ void stage_rows(const float (&v)[32], float* stg, int lane) {
@@ -212,36 +216,58 @@ __device__ __forceinline__ void store_part(float* o, long long M, int N, long lo
   for (int r = 0; r < rows; ++r, o += N) *o = stg[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)];
 }
 
+// A CTA's items are blockIdx.x, blockIdx.x + gridDim.x, ...; the tile advances by the grid's own (n, m, split)
+// digits with carries, without divisions.
 struct Item {
-  int split, k_first, k_n, n0;
+  int nt, mt, split, k_first, k_n, n0;
   long long m0;
+  __device__ __forceinline__ void set(const Plan& p) {
+    n0 = nt * p.bn;
+    m0 = (long long)mt * BM;
+    k_first = split * p.per;
+    k_n = min(p.per, p.nk - k_first);
+  }
+  __device__ __forceinline__ Item next(const Plan& p) const {
+    Item t;
+    t.nt = nt + p.step_n;
+    t.mt = mt + p.step_m;
+    t.split = split + p.step_s;
+    if (t.nt >= p.ntiles) { t.nt -= p.ntiles; ++t.mt; }
+    if (t.mt >= p.mtiles) { t.mt -= p.mtiles; ++t.split; }
+    t.set(p);
+    return t;
+  }
 };
-__device__ __forceinline__ Item item_at(const Plan& p, long long w) {
+__device__ __forceinline__ Item first_item(const Plan& p) {
   Item t;
-  const int nt = (int)(w % p.ntiles);
-  const long long q = w / p.ntiles;
-  t.n0 = nt * p.bn;
-  t.m0 = (q % p.mtiles) * BM;
-  t.split = (int)(q / p.mtiles);
-  t.k_first = t.split * p.per;
-  t.k_n = min(p.per, p.nk - t.k_first);
+  t.nt = (int)blockIdx.x % p.ntiles;
+  const int q = (int)blockIdx.x / p.ntiles;
+  t.mt = q % p.mtiles;
+  t.split = q / p.mtiles;
+  t.set(p);
   return t;
 }
 
-template <bool SPLIT, typename T, int V, bool SCALED>
+struct Maps {
+  CUtensorMap a, b, y, z, res;
+};
+
+// T: the type of y, z and residual; ROWS: their rows by TMA; SCALED: 8-bit operands with scales
+template <bool SPLIT, typename T, bool ROWS, bool SCALED>
 __global__ void __launch_bounds__(threads(SPLIT), 1)
-    k_dense_tc(const __grid_constant__ Plan p, const __grid_constant__ dense::Epi e, const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb) {
+    k_dense_tc(const Plan p, const dense::Epi e, const __grid_constant__ Maps maps) {
   extern __shared__ __align__(1024) unsigned char dtc_raw[];
-  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dtc_raw) + 1023) & ~(uintptr_t)1023);
+  unsigned char* sm = dtc_raw + (1024 - (tc::smem_u32(dtc_raw) & 1023)) % 1024;
   unsigned char* hl = sm + LAND * LAND_BYTES;                           // FP32: B's hi and lo
-  float* staging = reinterpret_cast<float*>(sm + RING_BYTES);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + RING_BYTES + STAGING);   // [MAX_STAGES] landed
+  float* bias_sm = reinterpret_cast<float*>(sm + RING_BYTES + STAGING);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + RING_BYTES + STAGING + BIAS_BYTES);   // [MAX_STAGES] landed
   uint64_t* empty = full + MAX_STAGES;                                  // [MAX_STAGES] read
-  uint64_t* sfull = empty + MAX_STAGES;                                 // [SPLIT_GROUPS] hi and lo written
-  uint64_t* sempty = sfull + SPLIT_GROUPS;                              // [SPLIT_GROUPS] MMAs done with them
-  uint64_t* acc_full = sempty + SPLIT_GROUPS;                           // [2]
+  uint64_t* sfull = empty + MAX_STAGES;                                 // [SLOTS] hi and lo written
+  uint64_t* sempty = sfull + SLOTS;                                     // [SLOTS] MMAs done with them
+  uint64_t* acc_full = sempty + SLOTS;                                  // [2]
   uint64_t* acc_empty = acc_full + 2;                                   // [2]
-  uint64_t* drain = acc_empty + 2;
+  uint64_t* res_full = acc_empty + 2;                                   // [EPI_WARPS][2] residual chunks landed
+  uint64_t* drain = res_full + 2 * EPI_WARPS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stages = SPLIT ? LAND : p.stages;
@@ -252,7 +278,8 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], SPLIT ? 4 : 1);
     }
-    for (int s = 0; s < SPLIT_GROUPS; ++s) {
+    for (int i = 0; i < 2 * EPI_WARPS; ++i) tc::mbar_init(&res_full[i], 1);
+    for (int s = 0; s < SLOTS; ++s) {
       tc::mbar_init(&sfull[s], 4);
       tc::mbar_init(&sempty[s], 1);
     }
@@ -274,51 +301,51 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
 
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------------------- TMA producer
-    long long it = 0;
+    uint32_t it = 0;
     bool ok = true;
     const int kw = SPLIT ? 32 : p.kind ? 128 : 64;                       // k of a stage
-    for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x) {
-      const Item t = item_at(p, w);
+    Item t = first_item(p);
+    for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x, t = t.next(p)) {
       for (int k = 0; k < t.k_n; ++k, ++it) {
         const int s = (int)(it % stages);
-        if (it >= stages && !tc::mbar_wait(&empty[s], (uint32_t)(((it / stages) - 1) & 1))) { ok = false; break; }
+        if (it >= (uint32_t)stages && !wait(&empty[s], (uint32_t)(((it / stages) - 1) & 1))) { ok = false; break; }
         unsigned char* a = sm + s * stage_bytes;
         unsigned char* b = a + A_BYTES;
         const int k0 = (t.k_first + k) * kw;
         tc::mbar_expect_tx(&full[s], A_BYTES + p.bn * 128);
         if (SPLIT || !p.a_mn) {
-          tc::tma_load(a, &ma, &full[s], p.a_mn ? (int)t.m0 : k0, p.a_mn ? k0 : (int)t.m0);
+          tc::tma_load(a, &maps.a, &full[s], p.a_mn ? (int)t.m0 : k0, p.a_mn ? k0 : (int)t.m0);
         } else {
-          tc::tma_load(a, &ma, &full[s], (int)t.m0, k0);
-          tc::tma_load(a + 8192, &ma, &full[s], (int)t.m0 + 64, k0);
+          tc::tma_load(a, &maps.a, &full[s], (int)t.m0, k0);
+          tc::tma_load(a + 8192, &maps.a, &full[s], (int)t.m0 + 64, k0);
         }
         if (SPLIT || !p.b_mn) {
-          tc::tma_load(b, &mb, &full[s], p.b_mn ? t.n0 : k0, p.b_mn ? k0 : t.n0);
+          tc::tma_load(b, &maps.b, &full[s], p.b_mn ? t.n0 : k0, p.b_mn ? k0 : t.n0);
         } else {
-          for (int c = 0; c < p.bn; c += 64) tc::tma_load(b + c * 128, &mb, &full[s], t.n0 + c, k0);
+          for (int c = 0; c < p.bn; c += 64) tc::tma_load(b + c * 128, &maps.b, &full[s], t.n0 + c, k0);
         }
       }
     }
     // copies in flight can only be among the last `stages`
-    for (long long j = it > stages ? it - stages : 0; j < it; ++j) tc::mbar_wait(&full[j % stages], (uint32_t)((j / stages) & 1));
+    for (uint32_t j = it > (uint32_t)stages ? it - stages : 0; j < it; ++j) wait(&full[j % stages], (uint32_t)((j / stages) & 1));
   } else if (warp == 1 && lane == 0) {
     // ---------------------------------------------------------------- MMA issuer
-    long long it = 0, ch = 0;
+    uint32_t it = 0, ch = 0;
     bool ok = true;
-    for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x) {
-      const Item t = item_at(p, w);
+    Item t = first_item(p);
+    for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x, t = t.next(p)) {
       uint32_t d = 0;
       for (int k = 0; k < t.k_n; ++k, ++it) {
         const bool first = SPLIT ? k % CHUNK_STAGES == 0 : k == 0;
         const bool last = k == t.k_n - 1 || (SPLIT && k % CHUNK_STAGES == CHUNK_STAGES - 1);
         const int buf = (int)(ch & 1);
         if (first) {
-          if (ch >= 2 && !tc::mbar_wait(&acc_empty[buf], (uint32_t)(((ch >> 1) - 1) & 1))) { ok = false; break; }
+          if (ch >= 2 && !wait(&acc_empty[buf], (uint32_t)(((ch >> 1) - 1) & 1))) { ok = false; break; }
           d = tmem + (uint32_t)(buf * (SPLIT ? 128 : 256));
         }
         if (SPLIT) {
-          const int g = (int)(it % SPLIT_GROUPS);
-          if (!tc::mbar_wait(&sfull[g], (uint32_t)((it / SPLIT_GROUPS) & 1))) { ok = false; break; }
+          const int g = (int)(it % SLOTS);
+          if (!wait(&sfull[g], (uint32_t)((it / SLOTS) & 1))) { ok = false; break; }
           tc::fence_after();
           const uint32_t ahi = tmem + A_COL + g * 64, alo = ahi + 32;
           const uint32_t bhi = tc::smem_u32(hl + g * HL_BYTES), blo = bhi + A_BYTES;
@@ -332,7 +359,7 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
           commit(&sempty[g]);
         } else {
           const int s = (int)(it % stages);
-          if (!tc::mbar_wait(&full[s], (uint32_t)((it / stages) & 1))) { ok = false; break; }
+          if (!wait(&full[s], (uint32_t)((it / stages) & 1))) { ok = false; break; }
           tc::fence_after();
           const uint32_t a = tc::smem_u32(sm + s * stage_bytes), b = a + A_BYTES;
 #pragma unroll
@@ -351,67 +378,136 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
       }
     }
     commit(drain);
-    tc::mbar_wait(drain, 0);
+    wait(drain, 0);
   } else if (warp >= 2 && warp < 2 + EPI_WARPS) {
     // ---------------------------------------------------------------- epilogue
-    using O = Out<T, V, SCALED, SPLIT ? 4 : 8>;
+    constexpr int V = 16 / sizeof(T), PLACES = sizeof(T) == 4 ? 1 : 2, PLACE_BYTES = 32 * 32 * sizeof(T);
     const int q = warp & 3, half = (warp - 2) >> 2;          // TMEM lanes q * 32 ..; chunks half, half + 2, ...
-    float* stg = staging + (warp - 2) * 32 * 32;
+    unsigned char* place = sm + RING_BYTES + (warp - 2) * 4096;
+    float* bsm = bias_sm + (warp - 2) * 32;
+    uint64_t* rbar = res_full + (warp - 2) * 2;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     const int nch = p.bn / 32;
-    const int cl = (lane % O::L) * V;
-    typename O::A ahead;
-    float bias[V], ws[V];
-    // what the epilogue of chunk c of an item reads
-    auto fetch = [&](const Item& t, int c) {
-      const long long m0 = t.m0 + q * 32;
-      const int n = t.n0 + c * 32 + cl;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        bias[i] = ws[i] = 0.f;
-        if (n < p.N) {
-          if (e.bias) bias[i] = SCALED ? static_cast<const float*>(e.bias)[n + i] : to_f(static_cast<const T*>(e.bias)[n + i]);
-          if (SCALED) ws[i] = e.w_scale[n + i];
-        }
+    const bool rows_out = ROWS && !p.part;
+    uint32_t done = 0;                                       // chunks put through the places
+    bool ok = true, asked = false;                           // asked: the next chunk's residual is on its way
+    float bias_l = 0.f, ws_l = 0.f, xs_l = 0.f;              // of the next chunk: column lane's bias and scale, row lane's scale
+    auto here = [&](const Item& t, int c) { return t.m0 + q * 32 < p.M && t.n0 + c * 32 < p.N; };
+    auto ask_residual = [&](const Item& t, int c) {          // its place must be free
+      if (lane == 0) {
+        const int pl = done % PLACES;
+        tc::mbar_expect_tx(&rbar[pl], PLACE_BYTES);
+        tc::tma_load(place + pl * PLACE_BYTES, &maps.res, &rbar[pl], t.n0 + c * 32, (int)(t.m0 + q * 32));
       }
-      O::load(ahead, e, (int)min((long long)32, p.M - m0), m0, n, p.N, 0, lane);
     };
-    // the staged chunk c of an item; fetches chunk `next` of item tn in between
-    auto put = [&](const Item& t, int c, const Item& tn, int next) {
-      const long long m0 = t.m0 + q * 32;
-      const int n = t.n0 + c * 32 + cl, rows = (int)min((long long)32, p.M - m0);
-      if (p.part) {
-        store_part(p.part + (size_t)t.split * p.M * p.N, p.M, p.N, m0, t.n0 + c * 32, stg, lane);
-      } else {
-        if (SPLIT) fetch(t, c);
-        typename O::A h = ahead;
-        float b[V], w[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) { b[i] = bias[i]; w[i] = ws[i]; }
-        if (!SPLIT && next >= 0) fetch(tn, next);
-        O::store(h, e, rows, m0, n, p.N, 0, b, w, stg, lane);
-#pragma unroll 1
-        for (int k0 = O::B; k0 < O::A::PASSES; k0 += O::B) {
-          O::load(h, e, rows, m0, n, p.N, k0, lane);
-          O::store(h, e, rows, m0, n, p.N, k0, b, w, stg, lane);
-        }
+    // ask for what chunk c of an item needs
+    auto ask = [&](const Item& t, int c) {
+      const int n = t.n0 + c * 32 + lane;
+      const long long m = t.m0 + q * 32 + lane;
+      bias_l = ws_l = xs_l = 0.f;
+      if (n < p.N) {
+        if (e.bias) bias_l = SCALED ? static_cast<const float*>(e.bias)[n] : to_f(static_cast<const T*>(e.bias)[n]);
+        if (SCALED) ws_l = e.w_scale[n];
       }
+      if (SCALED && m < p.M) xs_l = e.x_scale[m];
+      if (e.residual && !e.z) ask_residual(t, c);
+      asked = true;
+    };
+    // the warp's rows, packed, into a place, and ready for a TMA store
+    auto stage = [&](unsigned char* pp, const float (&v)[32]) {
+#pragma unroll
+      for (int j = 0; j < 32 / V; ++j) {
+        float y[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[i] = v[j * V + i];
+        store_v<T, V>(reinterpret_cast<T*>(staged<T>(pp, lane, j)), y);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
     };
-    long long ch = 0;
-    bool ok = true;
-    if (!SPLIT && !p.part && blockIdx.x < p.items) fetch(item_at(p, blockIdx.x), half);
-    for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x) {
-      const Item t = item_at(p, w);
+    // chunk c of an item, a row per lane in v; `next` (chunk of item tn, or -1) is asked for on the way
+    auto put = [&](const Item& t, int c, float (&v)[32], const Item& tn, int next) {
+      const long long m0 = t.m0 + q * 32;
+      const int n0 = t.n0 + c * 32;
+      if (!here(t, c)) return;
+      if (!rows_out) {
+        float* stg = reinterpret_cast<float*>(place);
+        stage_rows(v, stg, lane);
+        if (p.part) store_part(p.part + (size_t)t.split * p.M * p.N, p.M, p.N, m0, n0, stg, lane);
+        else put_columns<T, SCALED>(e, p.M, p.N, m0, n0, stg, lane);
+        __syncwarp();
+        return;
+      }
+      if (lane == 0) stores_read<PLACES - 1>();              // this chunk's place is free
+      __syncwarp();
+      if (!asked) ask(t, c);
+      const int pl = done % PLACES;
+      unsigned char* pp = place + pl * PLACE_BYTES;
+      bsm[lane] = bias_l;
+      const float ws = ws_l, xs = xs_l;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        const float4 b = *reinterpret_cast<const float4*>(bsm + i);
+        if (SCALED) {
+          v[i] = fmaf(v[i], xs * __shfl_sync(0xffffffffu, ws, i), b.x);
+          v[i + 1] = fmaf(v[i + 1], xs * __shfl_sync(0xffffffffu, ws, i + 1), b.y);
+          v[i + 2] = fmaf(v[i + 2], xs * __shfl_sync(0xffffffffu, ws, i + 2), b.z);
+          v[i + 3] = fmaf(v[i + 3], xs * __shfl_sync(0xffffffffu, ws, i + 3), b.w);
+        } else {
+          v[i] += b.x; v[i + 1] += b.y; v[i + 2] += b.z; v[i + 3] += b.w;
+        }
+      }
+      if (e.z) {                                             // z takes the place first, the residual after it
+        stage(pp, v);
+        if (lane == 0) {
+          tma_store(&maps.z, pp, n0, (int)m0);
+          stores_read<0>();
+        }
+        __syncwarp();
+        if (e.residual) ask_residual(t, c);
+      }
+      // each step for the whole chunk: a branch per element would jump over the other activations' code every time
+      if (e.act == EMP_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = silu_fast(v[i]);
+      } else if (e.act == EMP_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = act_f(EMP_ACT_GELU, v[i]);
+      }
+      if (e.residual) {
+        if (!__all_sync(0xffffffffu, wait(&rbar[pl], (uint32_t)((done / PLACES) & 1)))) { ok = false; return; }
+#pragma unroll
+        for (int j = 0; j < 32 / V; ++j) {
+          float a[V];
+          unpack16<T, V>(*staged<T>(pp, lane, j), a);
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[j * V + i] += a[i];
+        }
+      }
+      stage(pp, v);
+      if (lane == 0) tma_store(&maps.y, pp, n0, (int)m0);
+      ++done;
+      asked = false;
+      if (next >= 0 && here(tn, next)) {
+        if (lane == 0) stores_read<PLACES - 1>();
+        ask(tn, next);
+      }
+    };
+    uint32_t ch = 0;
+    Item t = first_item(p);
+    if (rows_out && here(t, half)) ask(t, half);
+    Item tn;
+    for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x, t = tn) {
       const bool more = w + gridDim.x < p.items;
-      const Item tn = more ? item_at(p, w + gridDim.x) : t;
+      tn = t.next(p);
       if (SPLIT) {
         float acc[2][32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) acc[0][i] = acc[1][i] = 0.f;
         for (int k = 0; k < t.k_n; k += CHUNK_STAGES, ++ch) {
           const int buf = (int)(ch & 1);
-          if (!__all_sync(0xffffffffu, tc::mbar_wait(&acc_full[buf], (uint32_t)((ch >> 1) & 1)))) { ok = false; break; }
+          if (!__all_sync(0xffffffffu, wait(&acc_full[buf], (uint32_t)((ch >> 1) & 1)))) { ok = false; break; }
           tc::fence_after();
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -433,13 +529,12 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
           if (half + 2 * c < nch) {
-            stage_rows(acc[c], stg, lane);
             const bool last = half + 2 * c + 2 >= nch;
-            put(t, half + 2 * c, last ? tn : t, last ? (more ? half : -1) : half + 2 * c + 2);
+            put(t, half + 2 * c, acc[c], last ? tn : t, last ? (more ? half : -1) : half + 2 * c + 2);
           }
       } else {
         const int buf = (int)(ch & 1);
-        if (!__all_sync(0xffffffffu, tc::mbar_wait(&acc_full[buf], (uint32_t)((ch >> 1) & 1)))) break;
+        if (!__all_sync(0xffffffffu, wait(&acc_full[buf], (uint32_t)((ch >> 1) & 1)))) break;
         tc::fence_after();
 #pragma unroll 1
         for (int c = half; c < nch; c += 2) {
@@ -451,37 +546,35 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&acc_empty[buf]);
           }
-          stage_rows(v, stg, lane);
-          put(t, c, last ? tn : t, last ? (more ? half : -1) : c + 2);
+          put(t, c, v, last ? tn : t, last ? (more ? half : -1) : c + 2);
         }
         ++ch;
       }
     }
+    if (asked && e.residual && !e.z) wait(&rbar[done % PLACES], (uint32_t)((done / PLACES) & 1));   // a load in flight (after a timeout)
+    if (lane == 0) stores_read<0>();                         // the places outlive the stores' reads
   } else if (SPLIT && warp >= 2 + EPI_WARPS) {
     // ---------------------------------------------------------------- split warps: group g takes stages g, g + 2, ...
     const int sw = warp - (2 + EPI_WARPS), g = sw >> 2, q = warp & 3;
     const int r = q * 32 + lane;                             // row of A (its TMEM lane) and of B
-    const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + A_COL + g * 64;
-    unsigned char* bhi = hl + g * HL_BYTES;
-    long long it = 0;
+    uint32_t it = 0;
     bool ok = true;
-    for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x) {
-      const Item t = item_at(p, w);
+    Item t = first_item(p);
+    for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x, t = t.next(p)) {
       for (int k = 0; k < t.k_n; ++k, ++it) {
         if (it % SPLIT_GROUPS != g) continue;
-        const int s = (int)(it % LAND);
-        const long long u = it / SPLIT_GROUPS;
-        // a landing place always has the same reader group (LAND is a multiple of the groups), so a phase's
-        // parity is unambiguous; the stage is read, and its place freed, before the wait for the MMAs
-        if (!__all_sync(0xffffffffu, tc::mbar_wait(&full[s], (uint32_t)((it / LAND) & 1)))) { ok = false; break; }
-        const unsigned char* land = sm + s * LAND_BYTES;
-        float v[32], x[32];
-        read_row(land, r, p.a_mn, BM, v);
-        if (r < p.bn) read_row(land + A_BYTES, r, p.b_mn, p.bn, x);
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&empty[s]);
-        if (u >= 1 && !__all_sync(0xffffffffu, tc::mbar_wait(&sempty[g], (uint32_t)((u - 1) & 1)))) { ok = false; break; }
+        const int s = (int)(it % LAND), slot = (int)(it % SLOTS);
+        const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + A_COL + slot * 64;
+        unsigned char* bhi = hl + slot * HL_BYTES;
+        // first the slot (stage it - SLOTS multiplied, hence every stage before it landed), then the landing:
+        // the stage before in the same place, it - LAND, has landed, so its phase's parity is unambiguous
+        static_assert(LAND >= SLOTS, "order of the two waits");
+        if (it >= SLOTS && !__all_sync(0xffffffffu, wait(&sempty[slot], (uint32_t)(((it / SLOTS) - 1) & 1)))) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, wait(&full[s], (uint32_t)((it / LAND) & 1)))) { ok = false; break; }
         tc::fence_after();
+        const unsigned char* land = sm + s * LAND_BYTES;
+        float v[32];
+        read_row(land, r, p.a_mn, BM, v);
 #pragma unroll
         for (int j = 0; j < 32; j += 16) {
           float h[16];
@@ -493,6 +586,8 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
           tmem_st16(ta + 32 + j, h);
         }
         if (r < p.bn) {
+          float x[32];
+          read_row(land + A_BYTES, r, p.b_mn, p.bn, x);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             float4 hi, lo;
@@ -509,7 +604,10 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sfull[g]);
+        if (lane == 0) {
+          tc::mbar_arrive(&empty[s]);
+          tc::mbar_arrive(&sfull[slot]);
+        }
       }
     }
   }
@@ -529,7 +627,7 @@ inline CUtensorMapDataType map_type(int t) {
 }
 // rows of `cols` contiguous elements; a box of [rows_box][cols_box]
 inline bool make_map(CUtensorMap* m, const void* base, int t, long long cols, long long rows, long long ld, int cols_box,
-                     int rows_box, bool swizzle) {
+                     int rows_box, int swizzle_bytes) {
   auto fn = tc::encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
@@ -537,7 +635,8 @@ inline bool make_map(CUtensorMap* m, const void* base, int t, long long cols, lo
   cuuint32_t box[2] = {(cuuint32_t)cols_box, (cuuint32_t)rows_box};
   cuuint32_t estr[2] = {1, 1};
   return fn(m, map_type(t), 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -578,12 +677,12 @@ struct Operand {
 struct Launch {
   const Plan& p;
   const dense::Epi& e;
-  const CUtensorMap &ma, &mb;
+  const Maps& maps;
   unsigned grid;
   cudaStream_t st;
-  template <bool SPLIT, typename T, int V, bool SCALED>
+  template <bool SPLIT, typename T, bool ROWS, bool SCALED>
   int go() const {
-    auto k = k_dense_tc<SPLIT, T, V, SCALED>;
+    auto k = k_dense_tc<SPLIT, T, ROWS, SCALED>;
     // the shared-memory limit is set once per device and kernel
     static std::atomic<unsigned long long> done{0};
     int dev = 0;
@@ -593,12 +692,14 @@ struct Launch {
       EMP_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM));
       done.fetch_or(bit);
     }
-    k<<<grid, threads(SPLIT), SMEM, st>>>(p, e, ma, mb);
+    k<<<grid, threads(SPLIT), SMEM, st>>>(p, e, maps);
     return cudaGetLastError() == cudaSuccess ? EMP_OK : EMP_ERR_CUDA;
   }
+  template <bool SPLIT, typename T, bool SCALED>
+  int rows(bool by_tma) const { return by_tma ? go<SPLIT, T, true, SCALED>() : go<SPLIT, T, false, SCALED>(); }
 };
 inline int launch(long long M, int N, long long K, int t, const Operand& a, const Operand& b, const dense::Epi& e, const Shape& h,
-                  float* part, bool vec, cudaStream_t st) {
+                  float* part, cudaStream_t st) {
   const int es = dtype_size(t), kw = 128 / es;
   const bool split = t == EMP_F32;
   Plan p{};
@@ -611,22 +712,31 @@ inline int launch(long long M, int N, long long K, int t, const Operand& a, cons
   p.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(h.bn >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
   if (!split) p.idesc |= ((uint32_t)a.mn << 15) | ((uint32_t)b.mn << 16);
   p.part = part;
-  CUtensorMap ma, mb;
-  const bool ok_a = a.mn ? make_map(&ma, a.p, t, M, K, a.ld, split ? BM : 64, kw, !split) : make_map(&ma, a.p, t, K, M, a.ld, kw, BM, true);
-  const bool ok_b = b.mn ? make_map(&mb, b.p, t, N, K, b.ld, split ? h.bn : 64, kw, !split) : make_map(&mb, b.p, t, K, N, b.ld, kw, h.bn, true);
+  Maps maps{};
+  const bool ok_a = a.mn ? make_map(&maps.a, a.p, t, M, K, a.ld, split ? BM : 64, kw, 128 * !split) : make_map(&maps.a, a.p, t, K, M, a.ld, kw, BM, 128);
+  const bool ok_b = b.mn ? make_map(&maps.b, b.p, t, N, K, b.ld, split ? h.bn : 64, kw, 128 * !split) : make_map(&maps.b, b.p, t, K, N, b.ld, kw, h.bn, 128);
   if (!ok_a || !ok_b) return EMP_ERR_CUDA;
+  // rows of y, z and residual in 32 x 32 boxes
+  const int ys = dtype_size(e.y_dtype), one = (N * ys + 15) / 16 * 16 / ys;       // a single row: any pitch will do
+  auto fits = [&](const void* q, long long ld) { return !q || tma_ok(q, M == 1 ? one : ld, e.y_dtype); };
+  const bool rows = !part && fits(e.y, e.ldy) && fits(e.z, e.ldz) && fits(e.residual, e.ldr);
+  if (rows) {
+    auto map = [&](CUtensorMap* m, const void* q, long long ld) {
+      return !q || make_map(m, q, e.y_dtype, N, M, M == 1 ? one : ld, 32, 32, 32 * ys);
+    };
+    if (!map(&maps.y, e.y, e.ldy) || !map(&maps.z, e.z, e.ldz) || !map(&maps.res, e.residual, e.ldr)) return EMP_ERR_CUDA;
+  }
   const unsigned grid = (unsigned)std::min<long long>(p.items, tc::num_sms());
-  Launch l{p, e, ma, mb, grid, st};
-  if (split) return vec ? l.go<true, float, 4, false>() : l.go<true, float, 1, false>();
+  p.step_n = (int)(grid % p.ntiles);
+  p.step_m = (int)(grid / p.ntiles % p.mtiles);
+  p.step_s = (int)(grid / p.ntiles / p.mtiles);
+  Launch l{p, e, maps, grid, st};
+  if (split) return l.rows<true, float, false>(rows);
   const bool sc = t == EMP_E4M3;
   switch (e.y_dtype) {
-    case EMP_F32: return vec ? l.go<false, float, 4, true>() : l.go<false, float, 1, true>();      // of 8-bit inputs only
-    case EMP_BF16:
-      return sc ? (vec ? l.go<false, __nv_bfloat16, 8, true>() : l.go<false, __nv_bfloat16, 1, true>())
-                : (vec ? l.go<false, __nv_bfloat16, 8, false>() : l.go<false, __nv_bfloat16, 1, false>());
-    default:
-      return sc ? (vec ? l.go<false, __half, 8, true>() : l.go<false, __half, 1, true>())
-                : (vec ? l.go<false, __half, 8, false>() : l.go<false, __half, 1, false>());
+    case EMP_F32: return l.rows<false, float, true>(rows);                         // of 8-bit inputs only
+    case EMP_BF16: return sc ? l.rows<false, __nv_bfloat16, true>(rows) : l.rows<false, __nv_bfloat16, false>(rows);
+    default: return sc ? l.rows<false, __half, true>(rows) : l.rows<false, __half, false>(rows);
   }
 }
 

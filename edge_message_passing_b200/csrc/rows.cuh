@@ -19,30 +19,60 @@ template <> __device__ __forceinline__ float from_f<float>(float v) { return v; 
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
 
-// V consecutive elements as floats; V > 1 needs p aligned to V * sizeof(T) bytes (16 at most)
+// two neighbouring elements of a 32-bit word (16-bit types) as floats, and back; by value throughout, so that
+// no array of them ends up in local memory
+template <typename T> __device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b);
+template <> __device__ __forceinline__ void unpack2<__nv_bfloat16>(uint32_t w, float& a, float& b) {
+  a = __uint_as_float(w << 16);
+  b = __uint_as_float(w & 0xffff0000u);
+}
+template <> __device__ __forceinline__ void unpack2<__half>(uint32_t w, float& a, float& b) {
+  a = __half2float(__ushort_as_half((unsigned short)(w & 0xffffu)));
+  b = __half2float(__ushort_as_half((unsigned short)(w >> 16)));
+}
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(a)) | (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(b)) << 16;
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  return (uint32_t)__half_as_ushort(__float2half_rn(a)) | (uint32_t)__half_as_ushort(__float2half_rn(b)) << 16;
+}
+// 16 bytes as floats: four of fp32 or eight of a 16-bit type
+template <typename T, int V>
+__device__ __forceinline__ void unpack16(const uint4& u, float (&v)[V]) {
+  if constexpr (V == 4) {
+    v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y); v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
+  } else {
+    unpack2<T>(u.x, v[0], v[1]); unpack2<T>(u.y, v[2], v[3]); unpack2<T>(u.z, v[4], v[5]); unpack2<T>(u.w, v[6], v[7]);
+  }
+}
+// V consecutive elements as floats; V > 1: 16 bytes (8 of e4m3), p aligned to them
 template <typename T, int V>
 __device__ __forceinline__ void load_v(const T* p, float (&v)[V]) {
   if constexpr (V == 1) {
     v[0] = to_f(*p);
-  } else {
-    static_assert(V * sizeof(T) == 16 || V * sizeof(T) == 8, "vector bytes");
-    T e[V];
-    if constexpr (V * sizeof(T) == 16) *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
-    else *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
+  } else if constexpr (sizeof(T) == 1) {
+    static_assert(V == 8, "vector bytes");
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = to_f(e[i]);
+    for (int i = 0; i < 8; ++i) {
+      __nv_fp8_e4m3 e;
+      e.__x = (unsigned char)((i < 4 ? u.x : u.y) >> (8 * (i & 3)));
+      v[i] = (float)e;
+    }
+  } else {
+    static_assert(V * sizeof(T) == 16, "vector bytes");
+    unpack16<T, V>(*reinterpret_cast<const uint4*>(p), v);
   }
 }
 template <typename T, int V>
 __device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
   if constexpr (V == 1) {
     *p = from_f<T>(v[0]);
+  } else if constexpr (V == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   } else {
-    T e[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) e[i] = from_f<T>(v[i]);
-    if constexpr (V * sizeof(T) == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(e);
-    else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(e);
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
   }
 }
 // V values rounded to e4m3 (to nearest even; beyond +-448 to +-448; NaN kept)
@@ -51,11 +81,13 @@ __device__ __forceinline__ void store_e4m3(__nv_fp8_storage_t* p, const float (&
   if constexpr (V == 1) {
     *p = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
   } else {
-    __nv_fp8x2_storage_t e[V / 2];
+    uint32_t w[V / 4];
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) e[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-    if constexpr (V == 4) *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(e);
-    else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(e);
+    for (int i = 0; i < V; i += 4)
+      w[i / 4] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[i], v[i + 1]), __NV_SATFINITE, __NV_E4M3) |
+                 (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[i + 2], v[i + 3]), __NV_SATFINITE, __NV_E4M3) << 16;
+    if constexpr (V == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
+    else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
   }
 }
 

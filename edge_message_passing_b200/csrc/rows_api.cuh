@@ -146,16 +146,10 @@ bool dense_grad_args_ok(const emp_dense_grad& a) {
          (!a.g_x || (rows_ok(a.g_x, a.ldgx, a.fan_in, a.rows, a.dtype) && rows_ok(a.weight, a.ldw, a.fan_in, a.fan_out, a.dtype))) &&
          (!a.g_weight || rows_ok(a.x, a.ldx, a.fan_in, a.rows, a.dtype));
 }
-// rows of y, z and residual that allow 16-byte accesses
-bool epi_vec(const dense::Epi& e, int N) {
-  const int es = dtype_size(e.y_dtype);
-  auto ok = [&](const void* p, long long ld) { return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0); };
-  return N * es % 16 == 0 && ok(e.y, e.ldy) && ok(e.z, e.ldz) && ok(e.residual, e.ldr);
-}
 int dense_product(long long M, int N, long long K, int t, const dtc::Operand& a, const dtc::Operand& b, const dense::Epi& e,
                   const dtc::Shape& h, float* part, cudaStream_t s) {
   int st;
-  { Scope sc_("dense", s); st = dtc::launch(M, N, K, t, a, b, e, h, h.splits > 1 ? part : nullptr, epi_vec(e, N), s); }
+  { Scope sc_("dense", s); st = dtc::launch(M, N, K, t, a, b, e, h, h.splits > 1 ? part : nullptr, s); }
   if (st != EMP_OK || h.splits == 1) return st;
   Scope sc_("dense_join", s);
   dense::k_join<<<grid_for(M * N, 256), 256, 0, s>>>(M, N, h.splits, part, e);
