@@ -218,6 +218,15 @@ __device__ __forceinline__ void store_part(float* o, long long M, int N, long lo
 
 // A CTA's items are blockIdx.x, blockIdx.x + gridDim.x, ...; the tile advances by the grid's own (n, m, split)
 // digits with carries, without divisions.
+// Position in a ring of n places: the place and the parity of its current use.
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void advance(int n) {
+    if (++at == n) { at = 0; phase ^= 1; }
+  }
+};
+
 struct Item {
   int nt, mt, split, k_first, k_n, n0;
   long long m0;
@@ -301,14 +310,15 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
 
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------------------- TMA producer
+    Ring ring;
     uint32_t it = 0;
     bool ok = true;
     const int kw = SPLIT ? 32 : p.kind ? 128 : 64;                       // k of a stage
     Item t = first_item(p);
     for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x, t = t.next(p)) {
-      for (int k = 0; k < t.k_n; ++k, ++it) {
-        const int s = (int)(it % stages);
-        if (it >= (uint32_t)stages && !wait(&empty[s], (uint32_t)(((it / stages) - 1) & 1))) { ok = false; break; }
+      for (int k = 0; k < t.k_n; ++k, ++it, ring.advance(stages)) {
+        const int s = ring.at;
+        if (it >= (uint32_t)stages && !wait(&empty[s], ring.phase ^ 1)) { ok = false; break; }
         unsigned char* a = sm + s * stage_bytes;
         unsigned char* b = a + A_BYTES;
         const int k0 = (t.k_first + k) * kw;
@@ -330,6 +340,7 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
     for (uint32_t j = it > (uint32_t)stages ? it - stages : 0; j < it; ++j) wait(&full[j % stages], (uint32_t)((j / stages) & 1));
   } else if (warp == 1 && lane == 0) {
     // ---------------------------------------------------------------- MMA issuer
+    Ring ring;
     uint32_t it = 0, ch = 0;
     bool ok = true;
     Item t = first_item(p);
@@ -358,8 +369,9 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
           for (int kk = 0; kk < 4; ++kk) mma_tf32_ts(d, ahi + kk * 8, tc::sdesc128(bhi + kk * 32), p.idesc, 1u);
           commit(&sempty[g]);
         } else {
-          const int s = (int)(it % stages);
-          if (!wait(&full[s], (uint32_t)((it / stages) & 1))) { ok = false; break; }
+          const int s = ring.at;
+          if (!wait(&full[s], ring.phase)) { ok = false; break; }
+          ring.advance(stages);
           tc::fence_after();
           const uint32_t a = tc::smem_u32(sm + s * stage_bytes), b = a + A_BYTES;
 #pragma unroll
