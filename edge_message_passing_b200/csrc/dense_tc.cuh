@@ -59,28 +59,37 @@ struct Plan {
   int N, nk, per, bn, mtiles, ntiles, splits;    // nk k-stages, `per` of them per split
   int step_n, step_m, step_s;                    // the grid's size in tiles of n, m and splits
   int a_mn, b_mn, stages;
-  int kind;                                      // 0: f16 / bf16, 1: e4m3
   uint32_t idesc;
   float* part;                                   // [splits][M][N] or null
 };
 
-__device__ __forceinline__ uint64_t sdesc_mn(uint32_t addr, uint32_t chunk_bytes) {
-  // mn-major, 128-byte swizzle: 64-element runs of mn chunk_bytes apart, 8-k groups 1024 B apart
-  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(chunk_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Shared-memory matrix descriptors, 128-byte swizzle.  k-major: rows of 128 bytes of k, 8-row groups 1024 B
+// apart; mn-major: 64-element runs of mn 8192 B apart, 8-k groups 1024 B apart.  The upper word is the same;
+// the lower one is the address / 16 and the distance of the runs, and moves by a constant per MMA of
+// 32 bytes of k (k-major) or 16 k rows (mn-major).  The issuing warp only adds: it is alone on its critical path.
+constexpr uint32_t DESC_HI = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, int mn) {
+  return ((addr >> 4) & 0x3FFF) | ((mn ? 8192u >> 4 : 1u) << 16);
 }
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc));
+__device__ __forceinline__ uint64_t desc(uint32_t lo) { return ((uint64_t)DESC_HI << 32) | lo; }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p != 0;
 }
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc));
+template <bool F8>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t id, uint32_t acc) {
+  if constexpr (F8)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d), "l"(desc(a_lo)), "l"(desc(b_lo)), "r"(id), "r"(acc));
+  else
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d), "l"(desc(a_lo)), "l"(desc(b_lo)), "r"(id), "r"(acc));
 }
 // A in TMEM (128 lanes = rows, one 32-bit column per k)
-__device__ __forceinline__ void mma_tf32_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t id, uint32_t acc) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(acc));
+               "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d), "r"(a), "l"(desc(b_lo)), "r"(id), "r"(acc));
 }
 __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
@@ -308,88 +317,100 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
   tc::fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0 && lane == 0) {
-    // ---------------------------------------------------------------- TMA producer
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer (one elected lane issues)
     Ring ring;
     uint32_t it = 0;
     bool ok = true;
-    const int kw = SPLIT ? 32 : p.kind ? 128 : 64;                       // k of a stage
+    const int kw = SPLIT ? 32 : SCALED ? 128 : 64;                       // k of a stage
+    const uint32_t bytes = A_BYTES + p.bn * 128;
     Item t = first_item(p);
     for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x, t = t.next(p)) {
-      for (int k = 0; k < t.k_n; ++k, ++it, ring.advance(stages)) {
+      int k0 = t.k_first * kw;
+      const int m0 = (int)t.m0, n0 = t.n0;
+      for (int k = 0; k < t.k_n; ++k, ++it, k0 += kw, ring.advance(stages)) {
         const int s = ring.at;
-        if (it >= (uint32_t)stages && !wait(&empty[s], ring.phase ^ 1)) { ok = false; break; }
-        unsigned char* a = sm + s * stage_bytes;
-        unsigned char* b = a + A_BYTES;
-        const int k0 = (t.k_first + k) * kw;
-        tc::mbar_expect_tx(&full[s], A_BYTES + p.bn * 128);
-        if (SPLIT || !p.a_mn) {
-          tc::tma_load(a, &maps.a, &full[s], p.a_mn ? (int)t.m0 : k0, p.a_mn ? k0 : (int)t.m0);
-        } else {
-          tc::tma_load(a, &maps.a, &full[s], (int)t.m0, k0);
-          tc::tma_load(a + 8192, &maps.a, &full[s], (int)t.m0 + 64, k0);
+        if (it >= (uint32_t)stages && !__all_sync(0xffffffffu, wait(&empty[s], ring.phase ^ 1))) { ok = false; break; }
+        if (elect_one()) {
+          unsigned char* a = sm + s * stage_bytes;
+          unsigned char* b = a + A_BYTES;
+          uint64_t* bar = &full[s];
+          tc::mbar_expect_tx(bar, bytes);
+          if (!p.a_mn) {
+            tc::tma_load(a, &maps.a, bar, k0, m0);
+          } else {
+            tc::tma_load(a, &maps.a, bar, m0, k0);
+            if (!SPLIT) tc::tma_load(a + 8192, &maps.a, bar, m0 + 64, k0);
+          }
+          if (!p.b_mn) {
+            tc::tma_load(b, &maps.b, bar, k0, n0);
+          } else if (SPLIT) {
+            tc::tma_load(b, &maps.b, bar, n0, k0);
+          } else {
+            for (int c = 0; c < p.bn; c += 64) tc::tma_load(b + c * 128, &maps.b, bar, n0 + c, k0);
+          }
         }
-        if (SPLIT || !p.b_mn) {
-          tc::tma_load(b, &maps.b, &full[s], p.b_mn ? t.n0 : k0, p.b_mn ? k0 : t.n0);
-        } else {
-          for (int c = 0; c < p.bn; c += 64) tc::tma_load(b + c * 128, &maps.b, &full[s], t.n0 + c, k0);
-        }
+        __syncwarp();
       }
     }
     // copies in flight can only be among the last `stages`
-    for (uint32_t j = it > (uint32_t)stages ? it - stages : 0; j < it; ++j) wait(&full[j % stages], (uint32_t)((j / stages) & 1));
-  } else if (warp == 1 && lane == 0) {
-    // ---------------------------------------------------------------- MMA issuer
-    Ring ring;
-    uint32_t it = 0, ch = 0;
+    for (uint32_t j = it > (uint32_t)stages ? it - stages : 0; j < it; ++j) wait(&full[j % stages], (j / stages) & 1);
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer (one elected lane issues)
+    Ring ring, acc;
+    uint32_t ch = 0;
     bool ok = true;
+    const int ring_n = SPLIT ? SLOTS : stages;
+    const uint32_t step16 = SPLIT ? HL_BYTES >> 4 : stage_bytes >> 4;
+    const uint32_t a0 = SPLIT ? tmem + A_COL : desc_lo(tc::smem_u32(sm), p.a_mn);
+    const uint32_t b0 = SPLIT ? desc_lo(tc::smem_u32(hl), 0) : desc_lo(tc::smem_u32(sm + A_BYTES), p.b_mn);
+    const uint32_t sa = p.a_mn ? 2048 >> 4 : 32 >> 4, sb = p.b_mn ? 2048 >> 4 : 32 >> 4;
+    uint64_t* in = SPLIT ? sfull : full;
+    uint64_t* out = SPLIT ? sempty : empty;
+    const uint32_t id = p.idesc;
     Item t = first_item(p);
     for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x, t = t.next(p)) {
       uint32_t d = 0;
-      for (int k = 0; k < t.k_n; ++k, ++it) {
+      for (int k = 0; k < t.k_n; ++k, ring.advance(ring_n)) {
         const bool first = SPLIT ? k % CHUNK_STAGES == 0 : k == 0;
         const bool last = k == t.k_n - 1 || (SPLIT && k % CHUNK_STAGES == CHUNK_STAGES - 1);
-        const int buf = (int)(ch & 1);
         if (first) {
-          if (ch >= 2 && !wait(&acc_empty[buf], (uint32_t)(((ch >> 1) - 1) & 1))) { ok = false; break; }
-          d = tmem + (uint32_t)(buf * (SPLIT ? 128 : 256));
+          if (ch >= 2 && !__all_sync(0xffffffffu, wait(&acc_empty[acc.at], acc.phase ^ 1))) { ok = false; break; }
+          d = tmem + (uint32_t)(acc.at * (SPLIT ? 128 : 256));
         }
-        if (SPLIT) {
-          const int g = (int)(it % SLOTS);
-          if (!wait(&sfull[g], (uint32_t)((it / SLOTS) & 1))) { ok = false; break; }
-          tc::fence_after();
-          const uint32_t ahi = tmem + A_COL + g * 64, alo = ahi + 32;
-          const uint32_t bhi = tc::smem_u32(hl + g * HL_BYTES), blo = bhi + A_BYTES;
+        const int s = ring.at;
+        if (!__all_sync(0xffffffffu, wait(&in[s], ring.phase))) { ok = false; break; }
+        tc::fence_after();
+        if (elect_one()) {
+          const uint32_t b = b0 + s * step16;
+          if (SPLIT) {
+            const uint32_t hi = a0 + s * 64, lo = hi + 32, bl = b + (A_BYTES >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            mma_tf32_ts(d, alo + kk * 8, tc::sdesc128(bhi + kk * 32), p.idesc, !(first && kk == 0));
-            mma_tf32_ts(d, ahi + kk * 8, tc::sdesc128(blo + kk * 32), p.idesc, 1u);
+            for (int kk = 0; kk < 4; ++kk) {
+              mma_ts(d, lo + kk * 8, b + kk * 2, id, kk || !first);
+              mma_ts(d, hi + kk * 8, bl + kk * 2, id, 1u);
+            }
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) mma_ts(d, hi + kk * 8, b + kk * 2, id, 1u);
+          } else {
+            const uint32_t a = a0 + s * step16;
+            mma_ss<SCALED>(d, a, b, id, !first);
+            mma_ss<SCALED>(d, a + sa, b + sb, id, 1u);
+            mma_ss<SCALED>(d, a + 2 * sa, b + 2 * sb, id, 1u);
+            mma_ss<SCALED>(d, a + 3 * sa, b + 3 * sb, id, 1u);
           }
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_tf32_ts(d, ahi + kk * 8, tc::sdesc128(bhi + kk * 32), p.idesc, 1u);
-          commit(&sempty[g]);
-        } else {
-          const int s = ring.at;
-          if (!wait(&full[s], ring.phase)) { ok = false; break; }
-          ring.advance(stages);
-          tc::fence_after();
-          const uint32_t a = tc::smem_u32(sm + s * stage_bytes), b = a + A_BYTES;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {             // 32 bytes of k each (mn-major: 16 k rows of 128 bytes)
-            const uint64_t da = p.a_mn ? sdesc_mn(a + kk * 2048, 8192) : tc::sdesc128(a + kk * 32);
-            const uint64_t db = p.b_mn ? sdesc_mn(b + kk * 2048, 8192) : tc::sdesc128(b + kk * 32);
-            if (p.kind) mma_f8(d, da, db, p.idesc, !(first && kk == 0));
-            else mma_f16(d, da, db, p.idesc, !(first && kk == 0));
-          }
-          commit(&empty[s]);
+          commit(&out[s]);
+          if (last) commit(&acc_full[acc.at]);
         }
+        __syncwarp();
         if (last) {
-          commit(&acc_full[buf]);
+          acc.advance(2);
           ++ch;
         }
       }
     }
-    commit(drain);
+    if (elect_one()) commit(drain);
+    __syncwarp();
     wait(drain, 0);
   } else if (warp >= 2 && warp < 2 + EPI_WARPS) {
     // ---------------------------------------------------------------- epilogue
@@ -719,7 +740,6 @@ inline int launch(long long M, int N, long long K, int t, const Operand& a, cons
   p.items = (long long)h.mtiles * h.ntiles * h.splits;
   p.a_mn = a.mn; p.b_mn = b.mn;
   p.stages = std::min(MAX_STAGES, RING_BYTES / (A_BYTES + h.bn * 128));
-  p.kind = t == EMP_E4M3;
   const uint32_t fmt = t == EMP_F32 ? 2 : t == EMP_BF16 ? 1 : 0;
   p.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(h.bn >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
   if (!split) p.idesc |= ((uint32_t)a.mn << 15) | ((uint32_t)b.mn << 16);
