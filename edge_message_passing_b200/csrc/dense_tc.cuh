@@ -27,6 +27,7 @@
 // Every mbarrier wait is bounded; the producer waits out its own copies before exit.
 #pragma once
 #include <atomic>
+#include <type_traits>
 #include "so2_tc.cuh"
 #include "dense.cuh"
 
@@ -34,25 +35,37 @@ namespace emp {
 namespace dtc {
 
 constexpr int BM = 128;
-constexpr int EPI_WARPS = 8;
 constexpr int SPLIT_GROUPS = 2, SPLIT_WARPS = 4 * SPLIT_GROUPS;
 constexpr int A_BYTES = BM * 128;                       // one stage of A
-constexpr int MAX_STAGES = 8;
-constexpr int RING_BYTES = 4 * (A_BYTES + 256 * 128);   // 192 KB: four stages of 128 x 256 tiles
-constexpr int LAND = 3, SLOTS = 3;                      // FP32: stages as they land; split stages (A in TMEM, B's hi and lo here)
-constexpr int LAND_BYTES = 2 * A_BYTES;
-constexpr int HL_BYTES = 2 * A_BYTES;
-static_assert(LAND * LAND_BYTES + SLOTS * HL_BYTES <= RING_BYTES, "FP32 rings");
-constexpr int STAGING = EPI_WARPS * 32 * 32 * 4;        // a 32 x 32 tile per epilogue warp
-constexpr int BIAS_BYTES = EPI_WARPS * 32 * 4;          // and its columns' bias
-constexpr int BAR_BYTES = 512;
-constexpr int SMEM = 1024 + RING_BYTES + STAGING + BIAS_BYTES + BAR_BYTES;
-static_assert(SMEM <= 232448, "shared memory of a CTA");
+constexpr int MAX_STAGES = 8, MAX_EPI = 16;
+constexpr int LAND_BYTES = 2 * A_BYTES, HL_BYTES = 2 * A_BYTES;
 constexpr int CHUNK_STAGES = 2;                         // FP32: K_CHUNK = 64
 constexpr int A_COL = 256;                              // FP32: TMEM columns of A's slots (64 each: hi, lo)
-static_assert(A_COL + SLOTS * 64 <= 512, "TMEM columns");
 
-__host__ __device__ constexpr int threads(bool split) { return 32 * (2 + EPI_WARPS + (split ? SPLIT_WARPS : 0)); }
+// The kernel's forms: 16- and 8-bit operands; FP32; FP32 with k of one chunk at most (no sums to keep in registers).
+enum Path { DIRECT, SPLIT, SHORT };
+
+// T: the type of y, z and residual; ROWS: their rows by TMA; SCALED: 8-bit operands with scales.
+// Epilogue warps: an epilogue warp issues an instruction every nine cycles or so, so short k is bound by how
+// many there are: 16 where registers (65536 over the CTA) and staging (a tile of 32 x 32 each) allow, else 8.
+template <Path PATH, typename T, bool ROWS, bool SCALED>
+struct Cfg {
+  static constexpr bool FP32 = PATH != DIRECT;
+  static constexpr int EPI = PATH == SHORT || (PATH == DIRECT && sizeof(T) == 2 && ROWS && !SCALED) ? 16 : 8;
+  static constexpr int LAND = PATH == SHORT ? 2 : 3;    // FP32: stages as they land ...
+  static constexpr int SLOTS = LAND;                    // ... and split (A in TMEM, B's hi and lo in shared memory)
+  static constexpr int RING_BYTES = FP32 ? LAND * LAND_BYTES + SLOTS * HL_BYTES : 4 * (A_BYTES + 256 * 128);
+  static constexpr int PLACE_BYTES = ROWS ? 32 * 32 * (int)sizeof(T) : 4096;
+  static constexpr int PLACES = EPI == 8 && PLACE_BYTES == 2048 ? 2 : 1;      // of a warp
+  static constexpr int STAGING = EPI * PLACES * PLACE_BYTES;
+  static constexpr int BIAS = EPI * 32 * (SCALED ? 4 : (int)sizeof(T));
+  static constexpr int BARS = 512;
+  static constexpr int SMEM = 1024 + RING_BYTES + STAGING + BIAS + BARS;
+  static constexpr int THREADS = 32 * (2 + EPI + (FP32 ? SPLIT_WARPS : 0));
+  static_assert(SMEM <= 232448, "shared memory of a CTA");
+  static_assert(A_COL + SLOTS * 64 <= 512, "TMEM columns");
+  static_assert(LAND >= SLOTS, "order of the split warps' two waits");
+};
 
 struct Plan {
   long long M, items;
@@ -198,7 +211,7 @@ __device__ __forceinline__ void put_columns(const dense::Epi& e, long long M, in
     }
     if (e.act == EMP_ACT_SILU) {
 #pragma unroll
-      for (int k = 0; k < B; ++k) v[k] = silu_fast(v[k]);
+      for (int k = 0; k < B; k += 2) silu2(v[k], v[k + 1]);
     } else if (e.act == EMP_ACT_GELU) {
 #pragma unroll
       for (int k = 0; k < B; ++k) v[k] = act_f(EMP_ACT_GELU, v[k]);
@@ -270,33 +283,34 @@ struct Maps {
   CUtensorMap a, b, y, z, res;
 };
 
-// T: the type of y, z and residual; ROWS: their rows by TMA; SCALED: 8-bit operands with scales
-template <bool SPLIT, typename T, bool ROWS, bool SCALED>
-__global__ void __launch_bounds__(threads(SPLIT), 1)
+template <Path PATH, typename T, bool ROWS, bool SCALED>
+__global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
     k_dense_tc(const Plan p, const dense::Epi e, const __grid_constant__ Maps maps) {
+  using C = Cfg<PATH, T, ROWS, SCALED>;
+  constexpr bool FP32 = C::FP32;
+  constexpr int EPI_WARPS = C::EPI, PER_QUARTER = EPI_WARPS / 4, LAND = C::LAND, SLOTS = C::SLOTS;
   extern __shared__ __align__(1024) unsigned char dtc_raw[];
   unsigned char* sm = dtc_raw + (1024 - (tc::smem_u32(dtc_raw) & 1023)) % 1024;
   unsigned char* hl = sm + LAND * LAND_BYTES;                           // FP32: B's hi and lo
-  float* bias_sm = reinterpret_cast<float*>(sm + RING_BYTES + STAGING);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + RING_BYTES + STAGING + BIAS_BYTES);   // [MAX_STAGES] landed
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + C::RING_BYTES + C::STAGING + C::BIAS);   // [MAX_STAGES] landed
   uint64_t* empty = full + MAX_STAGES;                                  // [MAX_STAGES] read
   uint64_t* sfull = empty + MAX_STAGES;                                 // [SLOTS] hi and lo written
   uint64_t* sempty = sfull + SLOTS;                                     // [SLOTS] MMAs done with them
   uint64_t* acc_full = sempty + SLOTS;                                  // [2]
   uint64_t* acc_empty = acc_full + 2;                                   // [2]
-  uint64_t* res_full = acc_empty + 2;                                   // [EPI_WARPS][2] residual chunks landed
-  uint64_t* drain = res_full + 2 * EPI_WARPS;
+  uint64_t* res_full = acc_empty + 2;                                   // [MAX_EPI][2] residual chunks landed
+  uint64_t* drain = res_full + 2 * MAX_EPI;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stages = SPLIT ? LAND : p.stages;
-  const int stage_bytes = SPLIT ? LAND_BYTES : A_BYTES + p.bn * 128;
+  const int stages = FP32 ? LAND : p.stages;
+  const int stage_bytes = FP32 ? LAND_BYTES : A_BYTES + p.bn * 128;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       tc::mbar_init(&full[s], 1);
-      tc::mbar_init(&empty[s], SPLIT ? 4 : 1);
+      tc::mbar_init(&empty[s], FP32 ? 4 : 1);
     }
-    for (int i = 0; i < 2 * EPI_WARPS; ++i) tc::mbar_init(&res_full[i], 1);
+    for (int i = 0; i < 2 * MAX_EPI; ++i) tc::mbar_init(&res_full[i], 1);
     for (int s = 0; s < SLOTS; ++s) {
       tc::mbar_init(&sfull[s], 4);
       tc::mbar_init(&sempty[s], 1);
@@ -322,7 +336,7 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
     Ring ring;
     uint32_t it = 0;
     bool ok = true;
-    const int kw = SPLIT ? 32 : SCALED ? 128 : 64;                       // k of a stage
+    const int kw = FP32 ? 32 : SCALED ? 128 : 64;                       // k of a stage
     const uint32_t bytes = A_BYTES + p.bn * 128;
     Item t = first_item(p);
     for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x, t = t.next(p)) {
@@ -340,11 +354,11 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
             tc::tma_load(a, &maps.a, bar, k0, m0);
           } else {
             tc::tma_load(a, &maps.a, bar, m0, k0);
-            if (!SPLIT) tc::tma_load(a + 8192, &maps.a, bar, m0 + 64, k0);
+            if (!FP32) tc::tma_load(a + 8192, &maps.a, bar, m0 + 64, k0);
           }
           if (!p.b_mn) {
             tc::tma_load(b, &maps.b, bar, k0, n0);
-          } else if (SPLIT) {
+          } else if (FP32) {
             tc::tma_load(b, &maps.b, bar, n0, k0);
           } else {
             for (int c = 0; c < p.bn; c += 64) tc::tma_load(b + c * 128, &maps.b, bar, n0 + c, k0);
@@ -360,30 +374,30 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
     Ring ring, acc;
     uint32_t ch = 0;
     bool ok = true;
-    const int ring_n = SPLIT ? SLOTS : stages;
-    const uint32_t step16 = SPLIT ? HL_BYTES >> 4 : stage_bytes >> 4;
-    const uint32_t a0 = SPLIT ? tmem + A_COL : desc_lo(tc::smem_u32(sm), p.a_mn);
-    const uint32_t b0 = SPLIT ? desc_lo(tc::smem_u32(hl), 0) : desc_lo(tc::smem_u32(sm + A_BYTES), p.b_mn);
+    const int ring_n = FP32 ? SLOTS : stages;
+    const uint32_t step16 = FP32 ? HL_BYTES >> 4 : stage_bytes >> 4;
+    const uint32_t a0 = FP32 ? tmem + A_COL : desc_lo(tc::smem_u32(sm), p.a_mn);
+    const uint32_t b0 = FP32 ? desc_lo(tc::smem_u32(hl), 0) : desc_lo(tc::smem_u32(sm + A_BYTES), p.b_mn);
     const uint32_t sa = p.a_mn ? 2048 >> 4 : 32 >> 4, sb = p.b_mn ? 2048 >> 4 : 32 >> 4;
-    uint64_t* in = SPLIT ? sfull : full;
-    uint64_t* out = SPLIT ? sempty : empty;
+    uint64_t* in = FP32 ? sfull : full;
+    uint64_t* out = FP32 ? sempty : empty;
     const uint32_t id = p.idesc;
     Item t = first_item(p);
     for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x, t = t.next(p)) {
       uint32_t d = 0;
       for (int k = 0; k < t.k_n; ++k, ring.advance(ring_n)) {
-        const bool first = SPLIT ? k % CHUNK_STAGES == 0 : k == 0;
-        const bool last = k == t.k_n - 1 || (SPLIT && k % CHUNK_STAGES == CHUNK_STAGES - 1);
+        const bool first = FP32 ? k % CHUNK_STAGES == 0 : k == 0;
+        const bool last = k == t.k_n - 1 || (FP32 && k % CHUNK_STAGES == CHUNK_STAGES - 1);
         if (first) {
           if (ch >= 2 && !__all_sync(0xffffffffu, wait(&acc_empty[acc.at], acc.phase ^ 1))) { ok = false; break; }
-          d = tmem + (uint32_t)(acc.at * (SPLIT ? 128 : 256));
+          d = tmem + (uint32_t)(acc.at * (FP32 ? 128 : 256));
         }
         const int s = ring.at;
         if (!__all_sync(0xffffffffu, wait(&in[s], ring.phase))) { ok = false; break; }
         tc::fence_after();
         if (elect_one()) {
           const uint32_t b = b0 + s * step16;
-          if (SPLIT) {
+          if (FP32) {
             const uint32_t hi = a0 + s * 64, lo = hi + 32, bl = b + (A_BYTES >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
@@ -414,17 +428,19 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
     wait(drain, 0);
   } else if (warp >= 2 && warp < 2 + EPI_WARPS) {
     // ---------------------------------------------------------------- epilogue
-    constexpr int V = 16 / sizeof(T), PLACES = sizeof(T) == 4 ? 1 : 2, PLACE_BYTES = 32 * 32 * sizeof(T);
-    const int q = warp & 3, half = (warp - 2) >> 2;          // TMEM lanes q * 32 ..; chunks half, half + 2, ...
-    unsigned char* place = sm + RING_BYTES + (warp - 2) * 4096;
-    float* bsm = bias_sm + (warp - 2) * 32;
+    constexpr int V = 16 / sizeof(T), PLACE_BYTES = C::PLACE_BYTES, PLACES = C::PLACES;
+    using B = std::conditional_t<SCALED, float, T>;          // the bias's type
+    const int q = warp & 3, sub = (warp - 2) >> 2;           // TMEM lanes q * 32 ..; chunks sub, sub + PER_QUARTER, ...
+    unsigned char* place = sm + C::RING_BYTES + (warp - 2) * PLACES * PLACE_BYTES;
+    B* bsm = reinterpret_cast<B*>(sm + C::RING_BYTES + C::STAGING) + (warp - 2) * 32;
     uint64_t* rbar = res_full + (warp - 2) * 2;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     const int nch = p.bn / 32;
     const bool rows_out = ROWS && !p.part;
     uint32_t done = 0;                                       // chunks put through the places
     bool ok = true, asked = false;                           // asked: the next chunk's residual is on its way
-    float bias_l = 0.f, ws_l = 0.f, xs_l = 0.f;              // of the next chunk: column lane's bias and scale, row lane's scale
+    B bias_l = from_f<B>(0.f);
+    float ws_l = 0.f, xs_l = 0.f;                            // of the next chunk: column lane's bias and scale, row lane's scale
     auto here = [&](const Item& t, int c) { return t.m0 + q * 32 < p.M && t.n0 + c * 32 < p.N; };
     auto ask_residual = [&](const Item& t, int c) {          // its place must be free
       if (lane == 0) {
@@ -437,9 +453,10 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
     auto ask = [&](const Item& t, int c) {
       const int n = t.n0 + c * 32 + lane;
       const long long m = t.m0 + q * 32 + lane;
-      bias_l = ws_l = xs_l = 0.f;
+      ws_l = xs_l = 0.f;
+      bias_l = from_f<B>(0.f);
       if (n < p.N) {
-        if (e.bias) bias_l = SCALED ? static_cast<const float*>(e.bias)[n] : to_f(static_cast<const T*>(e.bias)[n]);
+        if (e.bias) bias_l = static_cast<const B*>(e.bias)[n];
         if (SCALED) ws_l = e.w_scale[n];
       }
       if (SCALED && m < p.M) xs_l = e.x_scale[m];
@@ -479,16 +496,14 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
       bsm[lane] = bias_l;
       const float ws = ws_l, xs = xs_l;
       __syncwarp();
+      if (SCALED || e.bias) {
+        constexpr int VB = 16 / sizeof(B);
 #pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        const float4 b = *reinterpret_cast<const float4*>(bsm + i);
-        if (SCALED) {
-          v[i] = fmaf(v[i], xs * __shfl_sync(0xffffffffu, ws, i), b.x);
-          v[i + 1] = fmaf(v[i + 1], xs * __shfl_sync(0xffffffffu, ws, i + 1), b.y);
-          v[i + 2] = fmaf(v[i + 2], xs * __shfl_sync(0xffffffffu, ws, i + 2), b.z);
-          v[i + 3] = fmaf(v[i + 3], xs * __shfl_sync(0xffffffffu, ws, i + 3), b.w);
-        } else {
-          v[i] += b.x; v[i + 1] += b.y; v[i + 2] += b.z; v[i + 3] += b.w;
+        for (int j = 0; j < 32; j += VB) {
+          float b[VB];
+          unpack16<B, VB>(*reinterpret_cast<const uint4*>(bsm + j), b);
+#pragma unroll
+          for (int i = 0; i < VB; ++i) v[j + i] = SCALED ? fmaf(v[j + i], xs * __shfl_sync(0xffffffffu, ws, j + i), b[i]) : v[j + i] + b[i];
         }
       }
       if (e.z) {                                             // z takes the place first, the residual after it
@@ -503,7 +518,7 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
       // each step for the whole chunk: a branch per element would jump over the other activations' code every time
       if (e.act == EMP_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = silu_fast(v[i]);
+        for (int i = 0; i < 32; i += 2) silu2(v[i], v[i + 1]);
       } else if (e.act == EMP_ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = act_f(EMP_ACT_GELU, v[i]);
@@ -529,12 +544,12 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
     };
     uint32_t ch = 0;
     Item t = first_item(p);
-    if (rows_out && here(t, half)) ask(t, half);
+    if (rows_out && sub < nch && here(t, sub)) ask(t, sub);
     Item tn;
     for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x, t = tn) {
       const bool more = w + gridDim.x < p.items;
       tn = t.next(p);
-      if (SPLIT) {
+      if constexpr (PATH == SPLIT) {
         float acc[2][32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) acc[0][i] = acc[1][i] = 0.f;
@@ -544,11 +559,11 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
           tc::fence_after();
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            if (half + 2 * c < nch) {
+            if (sub + 2 * c < nch) {
 #pragma unroll
               for (int j = 0; j < 32; j += 16) {
                 float v[16];
-                tmem_ld16(lanes + (uint32_t)(buf * 128 + (half + 2 * c) * 32 + j), v);
+                tmem_ld16(lanes + (uint32_t)(buf * 128 + (sub + 2 * c) * 32 + j), v);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[c][j + i] += v[i];
               }
@@ -561,32 +576,33 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
         if (!ok) break;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          if (half + 2 * c < nch) {
-            const bool last = half + 2 * c + 2 >= nch;
-            put(t, half + 2 * c, acc[c], last ? tn : t, last ? (more ? half : -1) : half + 2 * c + 2);
+          if (sub + 2 * c < nch) {
+            const bool last = sub + 2 * c + 2 >= nch;
+            put(t, sub + 2 * c, acc[c], last ? tn : t, last ? (more ? sub : -1) : sub + 2 * c + 2);
           }
       } else {
         const int buf = (int)(ch & 1);
         if (!__all_sync(0xffffffffu, wait(&acc_full[buf], (uint32_t)((ch >> 1) & 1)))) break;
         tc::fence_after();
 #pragma unroll 1
-        for (int c = half; c < nch; c += 2) {
+        for (int c = sub; c < nch; c += PER_QUARTER) {
           float v[32];
-          tc::tmem_ld32(lanes + (uint32_t)(buf * 256 + c * 32), v);
-          const bool last = c + 2 >= nch;
+          tc::tmem_ld32(lanes + (uint32_t)(buf * (FP32 ? 128 : 256) + c * 32), v);
+          const bool last = c + PER_QUARTER >= nch;
           if (last) {                                        // the last read of this accumulator
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&acc_empty[buf]);
           }
-          put(t, c, v, last ? tn : t, last ? (more ? half : -1) : c + 2);
+          put(t, c, v, last ? tn : t, last ? (more ? sub : -1) : c + PER_QUARTER);
         }
+        if (sub >= nch && lane == 0) tc::mbar_arrive(&acc_empty[buf]);   // a narrow tile has no chunk for this warp
         ++ch;
       }
     }
     if (asked && e.residual && !e.z) wait(&rbar[done % PLACES], (uint32_t)((done / PLACES) & 1));   // a load in flight (after a timeout)
     if (lane == 0) stores_read<0>();                         // the places outlive the stores' reads
-  } else if (SPLIT && warp >= 2 + EPI_WARPS) {
+  } else if (FP32 && warp >= 2 + EPI_WARPS) {
     // ---------------------------------------------------------------- split warps: group g takes stages g, g + 2, ...
     const int sw = warp - (2 + EPI_WARPS), g = sw >> 2, q = warp & 3;
     const int r = q * 32 + lane;                             // row of A (its TMEM lane) and of B
@@ -601,7 +617,6 @@ __global__ void __launch_bounds__(threads(SPLIT), 1)
         unsigned char* bhi = hl + slot * HL_BYTES;
         // first the slot (stage it - SLOTS multiplied, hence every stage before it landed), then the landing:
         // the stage before in the same place, it - LAND, has landed, so its phase's parity is unambiguous
-        static_assert(LAND >= SLOTS, "order of the two waits");
         if (it >= SLOTS && !__all_sync(0xffffffffu, wait(&sempty[slot], (uint32_t)(((it / SLOTS) - 1) & 1)))) { ok = false; break; }
         if (!__all_sync(0xffffffffu, wait(&full[s], (uint32_t)((it / LAND) & 1)))) { ok = false; break; }
         tc::fence_after();
@@ -713,23 +728,24 @@ struct Launch {
   const Maps& maps;
   unsigned grid;
   cudaStream_t st;
-  template <bool SPLIT, typename T, bool ROWS, bool SCALED>
+  template <Path PATH, typename T, bool ROWS, bool SCALED>
   int go() const {
-    auto k = k_dense_tc<SPLIT, T, ROWS, SCALED>;
+    using C = Cfg<PATH, T, ROWS, SCALED>;
+    auto k = k_dense_tc<PATH, T, ROWS, SCALED>;
     // the shared-memory limit is set once per device and kernel
     static std::atomic<unsigned long long> done{0};
     int dev = 0;
     EMP_CUDA_TRY(cudaGetDevice(&dev));
     const unsigned long long bit = 1ull << (dev & 63);
     if (dev > 63 || !(done.load() & bit)) {
-      EMP_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM));
+      EMP_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
       done.fetch_or(bit);
     }
-    k<<<grid, threads(SPLIT), SMEM, st>>>(p, e, maps);
+    k<<<grid, C::THREADS, C::SMEM, st>>>(p, e, maps);
     return cudaGetLastError() == cudaSuccess ? EMP_OK : EMP_ERR_CUDA;
   }
-  template <bool SPLIT, typename T, bool SCALED>
-  int rows(bool by_tma) const { return by_tma ? go<SPLIT, T, true, SCALED>() : go<SPLIT, T, false, SCALED>(); }
+  template <Path PATH, typename T, bool SCALED>
+  int rows(bool by_tma) const { return by_tma ? go<PATH, T, true, SCALED>() : go<PATH, T, false, SCALED>(); }
 };
 inline int launch(long long M, int N, long long K, int t, const Operand& a, const Operand& b, const dense::Epi& e, const Shape& h,
                   float* part, cudaStream_t st) {
@@ -739,7 +755,7 @@ inline int launch(long long M, int N, long long K, int t, const Operand& a, cons
   p.M = M; p.N = N; p.nk = h.nk; p.per = h.per; p.bn = h.bn; p.mtiles = h.mtiles; p.ntiles = h.ntiles; p.splits = h.splits;
   p.items = (long long)h.mtiles * h.ntiles * h.splits;
   p.a_mn = a.mn; p.b_mn = b.mn;
-  p.stages = std::min(MAX_STAGES, RING_BYTES / (A_BYTES + h.bn * 128));
+  p.stages = std::min(MAX_STAGES, Cfg<DIRECT, float, true, true>::RING_BYTES / (A_BYTES + h.bn * 128));
   const uint32_t fmt = t == EMP_F32 ? 2 : t == EMP_BF16 ? 1 : 0;
   p.idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(h.bn >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
   if (!split) p.idesc |= ((uint32_t)a.mn << 15) | ((uint32_t)b.mn << 16);
@@ -763,12 +779,12 @@ inline int launch(long long M, int N, long long K, int t, const Operand& a, cons
   p.step_m = (int)(grid / p.ntiles % p.mtiles);
   p.step_s = (int)(grid / p.ntiles / p.mtiles);
   Launch l{p, e, maps, grid, st};
-  if (split) return l.rows<true, float, false>(rows);
+  if (split) return h.per <= CHUNK_STAGES ? l.rows<SHORT, float, false>(rows) : l.rows<SPLIT, float, false>(rows);
   const bool sc = t == EMP_E4M3;
   switch (e.y_dtype) {
-    case EMP_F32: return l.rows<false, float, true>(rows);                         // of 8-bit inputs only
-    case EMP_BF16: return sc ? l.rows<false, __nv_bfloat16, true>(rows) : l.rows<false, __nv_bfloat16, false>(rows);
-    default: return sc ? l.rows<false, __half, true>(rows) : l.rows<false, __half, false>(rows);
+    case EMP_F32: return l.rows<DIRECT, float, true>(rows);                         // of 8-bit inputs only
+    case EMP_BF16: return sc ? l.rows<DIRECT, __nv_bfloat16, true>(rows) : l.rows<DIRECT, __nv_bfloat16, false>(rows);
+    default: return sc ? l.rows<DIRECT, __half, true>(rows) : l.rows<DIRECT, __half, false>(rows);
   }
 }
 

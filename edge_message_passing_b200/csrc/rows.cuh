@@ -125,6 +125,16 @@ __device__ __forceinline__ float dact_f(int act, float z) {
   return 1.0f;
 }
 
+// SiLU of two values with one reciprocal: 1 / (p q) gives 1 / p and 1 / q.  The exponentials are capped at
+// e^43 so that the product stays finite (z < -43 comes out as z e^-43, 1e-17 at most); the cap also keeps a NaN
+// from the other value.  Three special-function instructions instead of four: they bound a short-k epilogue.
+__device__ __forceinline__ void silu2(float& a, float& b) {
+  const float p = 1.0f + __expf(-fmaxf(a, -43.0f)), q = 1.0f + __expf(-fmaxf(b, -43.0f));
+  const float r = __fdividef(1.0f, p * q);
+  a *= r * q;
+  b *= r * p;
+}
+
 // ------------------------------------------------------------- join of column sums
 // out[j] = sum over b of part[b][j].  32 columns per block, JOIN_WARPS warps over the rows (warp w takes
 // rows w, w + JOIN_WARPS, ..., JOIN_BATCH loads at a time; the warps' sums are added in warp order), so the
