@@ -115,21 +115,41 @@ __global__ void __launch_bounds__(256) k_pack(long long rows, int row_bytes, con
 }
 
 // ------------------------------------------------------------------ join of the k splits, in order
-__global__ void k_join(long long M, int N, int splits, const float* __restrict__ part, const Epi e) {
+// V consecutive elements a thread (4 where N allows), JOIN_Z splits' loads in flight together.
+constexpr int JOIN_Z = 8;
+template <int V>
+__global__ void __launch_bounds__(256) k_join(long long M, int N, int splits, const float* __restrict__ part, const Epi e) {
   const size_t total = (size_t)M * N;
-  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (size_t)gridDim.x * blockDim.x) {
-    float s = 0.f;
-    for (int z = 0; z < splits; ++z) s += part[(size_t)z * total + i];
-    put_one(e, (long long)(i / N), (int)(i % N), s);
+  for (size_t i = ((size_t)blockIdx.x * blockDim.x + threadIdx.x) * V; i < total; i += (size_t)gridDim.x * blockDim.x * V) {
+    float s[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[j] = 0.f;
+    for (int z0 = 0; z0 < splits; z0 += JOIN_Z) {
+      float v[JOIN_Z][V];
+#pragma unroll
+      for (int k = 0; k < JOIN_Z; ++k) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[k][j] = 0.f;
+        if (z0 + k < splits) load_v<float, V>(part + (size_t)(z0 + k) * total + i, v[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < JOIN_Z; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[j] += v[k][j];
+    }
+    const long long m = (long long)(i / N);
+    const int n = (int)(i % N);
+#pragma unroll
+    for (int j = 0; j < V; ++j) put_one(e, m, n + j, s[j]);
   }
 }
 
 // ------------------------------------------------------------------ g act'(z) and the bias gradient
 // gz = g act'(z), rounded to the operands' type (it is an operand of both products, which take that
 // type), and part[block][n] = the block's column sums of the unrounded values (bias gradient).
-// A warp takes 32 V neighbouring columns of every 8 gridDim.x-th row, GZ_BATCH rows' loads at a time.
+// A warp takes 32 V neighbouring columns of every 8 gridDim.x-th row, a few rows' loads at a time.
 // Bound by HBM: g and z in, gz out.
-constexpr int GZ_WARPS = 8, GZ_BATCH = 4;
+constexpr int GZ_WARPS = 8;
 struct GzArgs {
   long long rows;
   int cols, act;
@@ -139,7 +159,8 @@ struct GzArgs {
   float* part;                 // null without a bias gradient
 };
 template <typename T, int V>
-__global__ void __launch_bounds__(32 * GZ_WARPS) k_dense_gz(const GzArgs p) {
+__global__ void __launch_bounds__(32 * GZ_WARPS, 3) k_dense_gz(const GzArgs p) {
+  constexpr int GZ_BATCH = V == 8 ? 2 : 4;
   __shared__ float sm[GZ_WARPS][32 * V];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = (blockIdx.y * 32 + lane) * V;

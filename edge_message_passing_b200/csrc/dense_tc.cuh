@@ -20,7 +20,7 @@
 // own over memory: A's split goes to TMEM (the MMA's A operand may live there, and a thread's TMEM
 // lane is its row, whichever way A is stored), B's to shared memory.  The tensor cores add into their
 // FP32 accumulator by truncation, which shrinks a sum by about 2e-8 of itself per MMA (measured on the
-// SO(2) products: 7e-9 K).  So an accumulator takes K_CHUNK = 64 of k only and is then added, rounded
+// SO(2) products: 7e-9 K).  So an accumulator takes K_CHUNK = 96 of k only and is then added, rounded
 // to nearest, to sums in the epilogue warps' registers, and within each stage the small products
 // lo.hi and hi.lo come before hi.hi.
 //
@@ -39,7 +39,7 @@ constexpr int SPLIT_GROUPS = 2, SPLIT_WARPS = 4 * SPLIT_GROUPS;
 constexpr int A_BYTES = BM * 128;                       // one stage of A
 constexpr int MAX_STAGES = 8, MAX_EPI = 16;
 constexpr int LAND_BYTES = 2 * A_BYTES, HL_BYTES = 2 * A_BYTES;
-constexpr int CHUNK_STAGES = 2;                         // FP32: K_CHUNK = 64
+constexpr int CHUNK_STAGES = 3;                         // FP32: K_CHUNK = 96
 constexpr int A_COL = 256;                              // FP32: TMEM columns of A's slots (64 each: hi, lo)
 
 // The kernel's forms: 16- and 8-bit operands; FP32; FP32 with k of one chunk at most (no sums to keep in registers).
@@ -181,46 +181,45 @@ __device__ __forceinline__ uint4* staged(unsigned char* place, int r, int j) {
 }
 
 // Where it cannot (rows off 16-byte boundaries), the tile is turned through the staging (16-byte chunks XORed
-// with the row) and a lane takes one column, B rows at a time so that their loads are in flight together.
-template <typename T, bool SCALED>
-__device__ __forceinline__ void put_columns(const dense::Epi& e, long long M, int N, long long m0, int n0, const float* stg, int lane) {
-  constexpr int B = 8;
-  const int n = n0 + lane, rows = (int)min((long long)32, M - m0);
-  if (n >= N) return;
-  float b = 0.f, ws = 1.f;
-  if (e.bias) b = SCALED ? static_cast<const float*>(e.bias)[n] : to_f(static_cast<const T*>(e.bias)[n]);
-  if (SCALED) ws = e.w_scale[n];
-#pragma unroll 1
-  for (int k0 = 0; k0 < rows; k0 += B) {
-    float v[B], res[B], xs[B];
-    const T* rp = static_cast<const T*>(e.residual) + (m0 + k0) * e.ldr + n;
+// with the row) and a lane takes one column, R rows at a time: their residuals are loaded together, for R = 32 a chunk
+// ahead of their use.
+template <typename T, int R>
+__device__ __forceinline__ void load_column(float (&res)[R], const dense::Epi& e, int rows, long long m0, int n, int N, int k0) {
+  if (!e.residual || n >= N) return;
+  const T* rp = static_cast<const T*>(e.residual) + (m0 + k0) * e.ldr + n;
 #pragma unroll
-    for (int k = 0; k < B; ++k, rp += e.ldr) {
-      const int r = k0 + k;
-      res[k] = e.residual && r < rows ? to_f(*rp) : 0.f;
-      xs[k] = SCALED && r < rows ? e.x_scale[m0 + r] : 0.f;
-      v[k] = stg[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)];
-    }
+  for (int k = 0; k < R; ++k, rp += e.ldr)
+    if (k0 + k < rows) res[k] = to_f(*rp);
+}
+// v: rows k0 .. k0 + R of column n, scaled sums; v becomes y
+template <typename T, int R>
+__device__ __forceinline__ void finish_column(float (&v)[R], const float (&res)[R], const dense::Epi& e, int rows, long long m0, int n,
+                                              int N, int k0) {
+  if (e.z && n < N) {
+    T* z = static_cast<T*>(e.z) + (m0 + k0) * e.ldz + n;
 #pragma unroll
-    for (int k = 0; k < B; ++k) v[k] = SCALED ? fmaf(v[k], xs[k] * ws, b) : v[k] + b;
-    if (e.z) {
-      T* z = static_cast<T*>(e.z) + (m0 + k0) * e.ldz + n;
-#pragma unroll
-      for (int k = 0; k < B; ++k, z += e.ldz)
-        if (k0 + k < rows) *z = from_f<T>(v[k]);
-    }
-    if (e.act == EMP_ACT_SILU) {
-#pragma unroll
-      for (int k = 0; k < B; k += 2) silu2(v[k], v[k + 1]);
-    } else if (e.act == EMP_ACT_GELU) {
-#pragma unroll
-      for (int k = 0; k < B; ++k) v[k] = act_f(EMP_ACT_GELU, v[k]);
-    }
-    T* y = static_cast<T*>(e.y) + (m0 + k0) * e.ldy + n;
-#pragma unroll
-    for (int k = 0; k < B; ++k, y += e.ldy)
-      if (k0 + k < rows) *y = from_f<T>(v[k] + res[k]);
+    for (int k = 0; k < R; ++k, z += e.ldz)
+      if (k0 + k < rows) *z = from_f<T>(v[k]);
   }
+  if (e.act == EMP_ACT_SILU) {
+#pragma unroll
+    for (int k = 0; k < R; k += 2) silu2(v[k], v[k + 1]);
+  } else if (e.act == EMP_ACT_GELU) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) v[k] = act_f(EMP_ACT_GELU, v[k]);
+  }
+  if (e.residual) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) v[k] += res[k];
+  }
+}
+template <typename T, int R>
+__device__ __forceinline__ void store_column(const float (&v)[R], const dense::Epi& e, int rows, long long m0, int n, int N, int k0) {
+  if (n >= N) return;
+  T* y = static_cast<T*>(e.y) + (m0 + k0) * e.ldy + n;
+#pragma unroll
+  for (int k = 0; k < R; ++k, y += e.ldy)
+    if (k0 + k < rows) *y = from_f<T>(v[k]);
 }
 
 // a row per lane (v) into the warp's staging
@@ -436,14 +435,17 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
     uint64_t* rbar = res_full + (warp - 2) * 2;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     const int nch = p.bn / 32;
-    const bool rows_out = ROWS && !p.part;
     uint32_t done = 0;                                       // chunks put through the places
     bool ok = true, asked = false;                           // asked: the next chunk's residual is on its way
     B bias_l = from_f<B>(0.f);
     float ws_l = 0.f, xs_l = 0.f;                            // of the next chunk: column lane's bias and scale, row lane's scale
     auto here = [&](const Item& t, int c) { return t.m0 + q * 32 < p.M && t.n0 + c * 32 < p.N; };
+    constexpr int R = PATH == DIRECT ? 32 : 8;               // rows of a column at a time, without TMA
+    float res[ROWS ? 2 : R];
     auto ask_residual = [&](const Item& t, int c) {          // its place must be free
-      if (lane == 0) {
+      if constexpr (!ROWS) {
+        if (R == 32) load_column<T, R>(res, e, (int)min((long long)32, p.M - t.m0 - q * 32), t.m0 + q * 32, t.n0 + c * 32 + lane, p.N, 0);
+      } else if (lane == 0) {
         const int pl = done % PLACES;
         tc::mbar_expect_tx(&rbar[pl], PLACE_BYTES);
         tc::tma_load(place + pl * PLACE_BYTES, &maps.res, &rbar[pl], t.n0 + c * 32, (int)(t.m0 + q * 32));
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
         if (SCALED) ws_l = e.w_scale[n];
       }
       if (SCALED && m < p.M) xs_l = e.x_scale[m];
-      if (e.residual && !e.z) ask_residual(t, c);
+      if (e.residual && (!ROWS || !e.z)) ask_residual(t, c);
       asked = true;
     };
     // the warp's rows, packed, into a place, and ready for a TMA store
@@ -480,11 +482,31 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
       const long long m0 = t.m0 + q * 32;
       const int n0 = t.n0 + c * 32;
       if (!here(t, c)) return;
-      if (!rows_out) {
+      if constexpr (!ROWS) {
         float* stg = reinterpret_cast<float*>(place);
         stage_rows(v, stg, lane);
-        if (p.part) store_part(p.part + (size_t)t.split * p.M * p.N, p.M, p.N, m0, n0, stg, lane);
-        else put_columns<T, SCALED>(e, p.M, p.N, m0, n0, stg, lane);
+        if (p.part) {
+          store_part(p.part + (size_t)t.split * p.M * p.N, p.M, p.N, m0, n0, stg, lane);
+        } else {
+          const int rows = (int)min((long long)32, p.M - m0), n = n0 + lane;
+          if (!asked) ask(t, c);
+          const float b = to_f(bias_l), ws = ws_l;
+          asked = false;
+#pragma unroll 1
+          for (int k0 = 0; k0 < 32; k0 += R) {
+            float u[R];
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+              const int r = k0 + k;
+              u[k] = stg[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)];
+              u[k] = SCALED ? fmaf(u[k], __shfl_sync(0xffffffffu, xs_l, r) * ws, b) : u[k] + b;
+            }
+            if (R < 32) load_column<T, R>(res, e, rows, m0, n, p.N, k0);
+            finish_column<T, R>(u, res, e, rows, m0, n, p.N, k0);
+            if (R == 32 && next >= 0 && here(tn, next)) ask(tn, next);
+            store_column<T, R>(u, e, rows, m0, n, p.N, k0);
+          }
+        }
         __syncwarp();
         return;
       }
@@ -496,7 +518,7 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
       bsm[lane] = bias_l;
       const float ws = ws_l, xs = xs_l;
       __syncwarp();
-      if (SCALED || e.bias) {
+      if (SCALED || PATH == SPLIT || e.bias) {               // (SPLIT: a branch here costs spills)
         constexpr int VB = 16 / sizeof(B);
 #pragma unroll
         for (int j = 0; j < 32; j += VB) {
@@ -538,13 +560,13 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
       ++done;
       asked = false;
       if (next >= 0 && here(tn, next)) {
-        if (lane == 0) stores_read<PLACES - 1>();
+        if (e.residual && !e.z && lane == 0) stores_read<PLACES - 1>();
         ask(tn, next);
       }
     };
     uint32_t ch = 0;
     Item t = first_item(p);
-    if (rows_out && sub < nch && here(t, sub)) ask(t, sub);
+    if (!p.part && sub < nch && here(t, sub)) ask(t, sub);
     Item tn;
     for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x, t = tn) {
       const bool more = w + gridDim.x < p.items;
@@ -600,8 +622,10 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
         ++ch;
       }
     }
-    if (asked && e.residual && !e.z) wait(&rbar[done % PLACES], (uint32_t)((done / PLACES) & 1));   // a load in flight (after a timeout)
-    if (lane == 0) stores_read<0>();                         // the places outlive the stores' reads
+    if (ROWS) {
+      if (asked && e.residual && !e.z) wait(&rbar[done % PLACES], (uint32_t)((done / PLACES) & 1));   // a load in flight (after a timeout)
+      if (lane == 0) stores_read<0>();                       // the places outlive the stores' reads
+    }
   } else if (FP32 && warp >= 2 + EPI_WARPS) {
     // ---------------------------------------------------------------- split warps: group g takes stages g, g + 2, ...
     const int sw = warp - (2 + EPI_WARPS), g = sw >> 2, q = warp & 3;
@@ -693,27 +717,46 @@ inline bool tma_ok(const void* p, long long ld, int t) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * dtype_size(t) % 16 == 0;
 }
 
-// Tile width and splits of the k axis of an M x N product with K summed.
+// Tile width and splits of the k axis of an M x N product with K summed: those of the least estimated time.  A CTA's
+// tile takes the longer of its k stages and its epilogue (which runs beside the next tile's stages), the CTAs work in
+// waves, and splits pay for their partial products.  Microseconds as measured for the 16-bit and the FP32 kernel: a
+// stage with the operands in L2, the epilogue of a tile with one stage.
 struct Shape {
   int bn, splits, per, nk, mtiles, ntiles;
 };
 inline Shape shape_for(long long M, int N, long long K, int t) {
-  Shape s;
-  const int kw = 128 / dtype_size(t);
-  s.nk = (int)((K + kw - 1) / kw);
-  s.mtiles = (int)((M + BM - 1) / BM);
-  const int sms = tc::num_sms();
-  s.bn = N <= 64 ? 64 : N <= 128 || t == EMP_F32 ? 128 : 256;
-  // too few tiles for the SMs: a short k axis gets narrower tiles, a long one is split
-  auto tiles = [&] { return (long long)s.mtiles * ((N + s.bn - 1) / s.bn); };
-  while (s.nk < 64 && s.bn > 64 && tiles() < sms) s.bn /= 2;
-  s.ntiles = (N + s.bn - 1) / s.bn;
-  // enough items for every SM, each at least eight stages long
-  long long want = tiles() >= sms ? 1 : (sms + tiles() - 1) / tiles();
-  want = std::max<long long>(1, std::min<long long>(want, s.nk / 8));
-  s.per = (int)((s.nk + want - 1) / want);
-  s.splits = (s.nk + s.per - 1) / s.per;
-  return s;
+  const int kw = 128 / dtype_size(t), sms = tc::num_sms();
+  const bool fp32 = t == EMP_F32;
+  Shape best{};
+  double best_us = 0;
+  for (int bn = 64; bn <= (fp32 ? 128 : 256); bn *= 2) {
+    if (bn > 64 && bn >= 2 * N) break;
+    const int i = bn == 64 ? 0 : bn == 128 ? 1 : 2;
+    const double stage16[3] = {0.16, 0.22, 0.36}, epi16[3] = {1.3, 1.6, 2.9}, stage32[2] = {0.40, 0.50}, epi32[2] = {1.7, 2.4};
+    const double stage = fp32 ? stage32[i] : stage16[i], epi = fp32 ? epi32[i] : epi16[i];
+    Shape s;
+    s.bn = bn;
+    s.nk = (int)((K + kw - 1) / kw);
+    s.mtiles = (int)((M + BM - 1) / BM);
+    s.ntiles = (N + bn - 1) / bn;
+    const long long tiles = (long long)s.mtiles * s.ntiles;
+    // one split, or as many as fill one to three waves of CTAs, of at least four stages each
+    for (int waves = 0; waves <= 3; ++waves) {
+      const long long want = waves == 0 ? 1 : std::min<long long>(waves * (long long)sms / tiles, s.nk / 4);
+      if (want < 1 || (waves && want < 2)) continue;
+      s.per = (int)((s.nk + want - 1) / want);
+      s.splits = (s.nk + s.per - 1) / s.per;
+      const long long items = tiles * s.splits;
+      const double work = std::max(s.per * stage, epi);
+      double us = (double)((items + sms - 1) / sms) * work + epi;
+      if (s.splits > 1) us += 4.0 + 2.0 * 4e-6 * (double)s.splits * (double)M * (double)N / 5.0;   // the join, at 5 TB/s
+      if (best_us == 0 || us < best_us) {
+        best_us = us;
+        best = s;
+      }
+    }
+  }
+  return best;
 }
 
 // A k-major: rows [M][K] with pitch lda; mn-major: [K][M].  B likewise with N.  Both TMA-readable.

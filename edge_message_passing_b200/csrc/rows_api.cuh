@@ -152,7 +152,8 @@ int dense_product(long long M, int N, long long K, int t, const dtc::Operand& a,
   { Scope sc_("dense", s); st = dtc::launch(M, N, K, t, a, b, e, h, h.splits > 1 ? part : nullptr, s); }
   if (st != EMP_OK || h.splits == 1) return st;
   Scope sc_("dense_join", s);
-  dense::k_join<<<grid_for(M * N, 256), 256, 0, s>>>(M, N, h.splits, part, e);
+  if (N % 4 == 0) dense::k_join<4><<<grid_for(M * N, 1024), 256, 0, s>>>(M, N, h.splits, part, e);
+  else dense::k_join<1><<<grid_for(M * N, 256), 256, 0, s>>>(M, N, h.splits, part, e);
   return cudaGetLastError() == cudaSuccess ? EMP_OK : EMP_ERR_CUDA;
 }
 template <typename T>
