@@ -149,7 +149,9 @@ __global__ void __launch_bounds__(256) k_join(long long M, int N, int splits, co
 // type), and part[block][n] = the block's column sums of the unrounded values (bias gradient).
 // A warp takes 32 V neighbouring columns of every 8 gridDim.x-th row, a few rows' loads at a time.
 // Bound by HBM: g and z in, gz out.
-constexpr int GZ_WARPS = 8;
+// Four blocks per SM: with 16-bit vectors one row at a time (34 us at 16384 x 1024 with two rows and three blocks, 29 so),
+// else two (102 us at 80896 x 512 in FP32 with four rows and two blocks, 86 so).
+constexpr int GZ_WARPS = 8, GZ_PER_SM = 4;
 struct GzArgs {
   long long rows;
   int cols, act;
@@ -159,8 +161,8 @@ struct GzArgs {
   float* part;                 // null without a bias gradient
 };
 template <typename T, int V>
-__global__ void __launch_bounds__(32 * GZ_WARPS, 3) k_dense_gz(const GzArgs p) {
-  constexpr int GZ_BATCH = V == 8 ? 2 : 4;
+__global__ void __launch_bounds__(32 * GZ_WARPS, GZ_PER_SM) k_dense_gz(const GzArgs p) {
+  constexpr int GZ_BATCH = V == 8 ? 1 : 2;
   __shared__ float sm[GZ_WARPS][32 * V];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = (blockIdx.y * 32 + lane) * V;
@@ -190,8 +192,16 @@ __global__ void __launch_bounds__(32 * GZ_WARPS, 3) k_dense_gz(const GzArgs p) {
         if (m >= p.rows) break;
         // a rounded product (no contraction into the sum), so that g_bias has the same bits with and without gz
         if (p.act == EMP_ACT_SILU) {
+          if constexpr (V == 1) {
+            a[k][0] = __fmul_rn(a[k][0], dsilu_fast(b[k][0]));
+          } else {
 #pragma unroll
-          for (int i = 0; i < V; ++i) a[k][i] = __fmul_rn(a[k][i], dsilu_fast(b[k][i]));
+            for (int i = 0; i < V; i += 2) {
+              dsilu2(b[k][i], b[k][i + 1]);
+              a[k][i] = __fmul_rn(a[k][i], b[k][i]);
+              a[k][i + 1] = __fmul_rn(a[k][i + 1], b[k][i + 1]);
+            }
+          }
         } else if (p.act == EMP_ACT_GELU) {
 #pragma unroll
           for (int i = 0; i < V; ++i) a[k][i] = __fmul_rn(a[k][i], dact_f(EMP_ACT_GELU, b[k][i]));

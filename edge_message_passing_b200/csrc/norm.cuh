@@ -14,6 +14,8 @@
 // and the row still needs one block-wide reduction.  The maximum is taken on the bits of |s w| as
 // unsigned integers, where a NaN is larger than every number, so a row with a NaN comes out as NaN.
 #pragma once
+#include <atomic>
+#include <type_traits>
 #include "rows.cuh"
 
 namespace emp {
@@ -62,6 +64,14 @@ __device__ __forceinline__ void row_reduce(float& a, uint32_t& b, int G, int t, 
   }
 }
 
+// a column's sums over the 2 l + 1 components of weight o = (l, c)
+__device__ __forceinline__ float degree_sum(const float* sums, int o, int C) {
+  const int l = o / C, c = o - l * C;
+  float a = 0.f;
+  for (int q = l * l; q < (l + 1) * (l + 1); ++q) a += sums[q * C + c];
+  return a;
+}
+
 template <typename T, int V, int SL, bool QUANT>
 __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm(const Args p) {
   __shared__ float red_a[32];
@@ -73,39 +83,46 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm(const Args p) {
   const T* res = p.residual ? static_cast<const T*>(p.residual) + row * p.ldr : nullptr;
   const T* w = static_cast<const T*>(p.w);
   const int C = p.cols / NCOMP;
-  float v[SL][V], wv[SL][V];
+  float v[SL][V];
   float ss = 0.f;
   uint32_t top = 0;
 #pragma unroll
   for (int k = 0; k < SL; ++k) {
     const int c = (k * G + t) * V;
-    const bool in = live && c < p.cols;
 #pragma unroll
     for (int i = 0; i < V; ++i) v[k][i] = 0.f;
-    if (in) load_v<T, V>(x + c, v[k]);
+    if (live && c < p.cols) load_v<T, V>(x + c, v[k]);
   }
   if (res) {
+    float a[SL][V];
 #pragma unroll
     for (int k = 0; k < SL; ++k) {
       const int c = (k * G + t) * V;
-      if (live && c < p.cols) {
-        float a[V];
-        load_v<T, V>(res + c, a);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[k][i] += a[i];
-      }
+      for (int i = 0; i < V; ++i) a[k][i] = 0.f;
+      if (live && c < p.cols) load_v<T, V>(res + c, a[k]);
     }
+#pragma unroll
+    for (int k = 0; k < SL; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[k][i] += a[k][i];
   }
+  // a thread's weights are read where they are used (twice for 8 bits; they stay in L1), not held: registers
+  // are what limits the rows in flight
+  auto weights = [&](int c, float (&wv)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) wv[i] = 1.f;
+    if (w && c < p.cols) load_v<T, V>(w + weight_at(c, C, p.degrees), wv);
+  };
 #pragma unroll
   for (int k = 0; k < SL; ++k) {
-    const int c = (k * G + t) * V;
 #pragma unroll
-    for (int i = 0; i < V; ++i) wv[k][i] = 1.f;
-    if (w && c < p.cols) load_v<T, V>(w + weight_at(c, C, p.degrees), wv[k]);
+    for (int i = 0; i < V; ++i) ss += v[k][i] * v[k][i];
+    if (QUANT) {
+      float wv[V];
+      weights((k * G + t) * V, wv);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      ss += v[k][i] * v[k][i];
-      if (QUANT) top = max(top, __float_as_uint(v[k][i] * wv[k][i]) & 0x7fffffffu);
+      for (int i = 0; i < V; ++i) top = max(top, __float_as_uint(v[k][i] * wv[i]) & 0x7fffffffu);
     }
   }
   const int slot = r * (G >> 5);
@@ -124,9 +141,10 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm(const Args p) {
     const int c = (k * G + t) * V;
     if (c >= p.cols) continue;
     if (p.s) store_v<T, V>(static_cast<T*>(p.s) + row * p.lds + c, v[k]);
-    float y[V];
+    float y[V], wv[V];
+    weights(c, wv);
 #pragma unroll
-    for (int i = 0; i < V; ++i) y[i] = v[k][i] * rstd * wv[k][i];
+    for (int i = 0; i < V; ++i) y[i] = v[k][i] * rstd * wv[i];
     if (QUANT) {
 #pragma unroll
       for (int i = 0; i < V; ++i) y[i] *= inv;
@@ -137,8 +155,183 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm(const Args p) {
   }
 }
 
+// ------------------------------------------------------------------ contiguous rows off 16-byte boundaries
+// Rows whose size is no multiple of 16 bytes but that follow one another without gaps: R of them are
+// (R cols sizeof(T) is), so a block moves R rows at once between memory and shared memory in 16-byte
+// vectors, and a warp takes whole rows there, a lane every 32nd element.  (Element-wise loads from memory
+// instead took 350 us for 80896 x 515 in bf16.)
+constexpr int ODD_THREADS = 256, ODD_SMEM = 110 * 1024;          // two blocks per SM at least
+
+// `bytes` from src to dst, one of them in shared memory; both 16-byte aligned
+__device__ __forceinline__ void copy_rows(void* dst, const void* src, int bytes) {
+  const int n = bytes >> 4;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n; i += ODD_THREADS) reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(src)[i];
+  for (int i = (n << 4) + threadIdx.x; i < bytes; i += ODD_THREADS)
+    reinterpret_cast<unsigned char*>(dst)[i] = reinterpret_cast<const unsigned char*>(src)[i];
+}
+
+template <typename T, bool QUANT, int RW>                         // RW rows of a warp, side by side
+__global__ void __launch_bounds__(ODD_THREADS) k_rms_norm_odd(const Args p) {
+  extern __shared__ __align__(16) unsigned char odd_sm[];
+  constexpr int WARPS = ODD_THREADS / 32, R = RW * WARPS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, C = p.cols / NCOMP;
+  const long long row0 = (long long)blockIdx.x * R;
+  const int rows = (int)min((long long)R, p.rows - row0), bytes = rows * p.cols * (int)sizeof(T);
+  const int area = (R * p.cols * (int)sizeof(T) + 15) / 16 * 16;
+  T* xs = reinterpret_cast<T*>(odd_sm);
+  T* rs = p.residual ? reinterpret_cast<T*>(odd_sm + area) : xs;
+  __nv_fp8_storage_t* qs = reinterpret_cast<__nv_fp8_storage_t*>(odd_sm + (p.residual ? 2 : 1) * area);
+  const T* w = static_cast<const T*>(p.w);
+  copy_rows(xs, static_cast<const T*>(p.x) + row0 * p.cols, bytes);
+  if (p.residual) copy_rows(rs, static_cast<const T*>(p.residual) + row0 * p.cols, bytes);
+  __syncthreads();
+  const bool two = p.residual != nullptr;
+  const int first = warp * RW;
+  float ss[RW];
+  uint32_t top[RW];
+#pragma unroll
+  for (int j = 0; j < RW; ++j) { ss[j] = 0.f; top[j] = 0; }
+#pragma unroll 4
+  for (int c = lane; c < p.cols; c += 32) {
+    const float wv = QUANT && w ? to_f(w[weight_at(c, C, p.degrees)]) : 1.f;
+#pragma unroll
+    for (int j = 0; j < RW; ++j) {
+      const int i = (first + j) * p.cols + c;
+      float v = first + j < rows ? to_f(xs[i]) : 0.f;
+      if (two && first + j < rows) v += to_f(rs[i]);
+      ss[j] += v * v;
+      if (QUANT) top[j] = max(top[j], __float_as_uint(v * wv) & 0x7fffffffu);
+    }
+  }
+  float rstd[RW], inv[RW];
+#pragma unroll
+  for (int j = 0; j < RW; ++j) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss[j] += __shfl_xor_sync(0xffffffffu, ss[j], o);
+    rstd[j] = rsqrtf(ss[j] / (float)p.cols + p.eps);
+    inv[j] = 1.f;
+    if (QUANT) {
+      const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, top[j])) * rstd[j];
+      const float scale = m < TINY ? 1.f : m / 448.f;
+      inv[j] = 1.f / scale;
+      if (lane == 0 && first + j < rows) p.scale[row0 + first + j] = scale;
+    }
+  }
+#pragma unroll 4
+  for (int c = lane; c < p.cols; c += 32) {
+    const float wv = w ? to_f(w[weight_at(c, C, p.degrees)]) : 1.f;
+#pragma unroll
+    for (int j = 0; j < RW; ++j) {
+      if (first + j >= rows) continue;
+      const int i = (first + j) * p.cols + c;
+      float v = to_f(xs[i]);
+      if (two) {
+        v += to_f(rs[i]);
+        rs[i] = from_f<T>(v);                                     // s
+      }
+      const float y = v * rstd[j] * wv;
+      if (QUANT) store_e4m3<1>(qs + i, {y * inv[j]});
+      else xs[i] = from_f<T>(y);
+    }
+  }
+  __syncthreads();
+  if (QUANT) copy_rows(static_cast<__nv_fp8_storage_t*>(p.y) + row0 * p.cols, qs, rows * p.cols);
+  else copy_rows(static_cast<T*>(p.y) + row0 * p.cols, xs, bytes);
+  if (p.s && two) copy_rows(static_cast<T*>(p.s) + row0 * p.cols, rs, bytes);
+}
+
+// The gradient of the same rows: persistent, a row per warp at a time; a lane's columns are the same in every
+// row, so its part of g_w stays in registers (NA of them: up to 32 NA columns).
+constexpr int ODD_GRAD_COLS = 1024;
+template <typename T, int NA>
+__global__ void __launch_bounds__(ODD_THREADS) k_rms_norm_grad_odd(const GradArgs p) {
+  extern __shared__ __align__(16) unsigned char odd_sm[];
+  constexpr int R = ODD_THREADS / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, C = p.cols / NCOMP;
+  const int area = R * p.cols * (int)sizeof(T);                   // a multiple of 16: R = 8
+  T* gs = reinterpret_cast<T*>(odd_sm);
+  T* ss_ = reinterpret_cast<T*>(odd_sm + area);
+  T* ts = reinterpret_cast<T*>(odd_sm + 2 * area);
+  const T* w = static_cast<const T*>(p.w);
+  float acc[NA], wv[NA];
+#pragma unroll
+  for (int k = 0; k < NA; ++k) {
+    const int c = lane + 32 * k;
+    acc[k] = 0.f;
+    wv[k] = w && c < p.cols ? to_f(w[weight_at(c, C, p.degrees)]) : 1.f;
+  }
+  const long long groups = (p.rows + R - 1) / R;
+  for (long long b = blockIdx.x; b < groups; b += gridDim.x) {
+    const long long row0 = b * R;
+    const int rows = (int)min((long long)R, p.rows - row0), bytes = rows * p.cols * (int)sizeof(T);
+    copy_rows(gs, static_cast<const T*>(p.g) + row0 * p.cols, bytes);
+    copy_rows(ss_, static_cast<const T*>(p.s) + row0 * p.cols, bytes);
+    if (p.g_s) copy_rows(ts, static_cast<const T*>(p.g_s) + row0 * p.cols, bytes);
+    __syncthreads();
+    if (warp < rows) {
+      const int base = warp * p.cols + lane;
+      float s2 = 0.f, hs = 0.f;
+#pragma unroll
+      for (int k = 0; k < NA; ++k)
+        if (lane + 32 * k < p.cols) {
+          const float s = to_f(ss_[base + 32 * k]);
+          s2 += s * s;
+          hs += to_f(gs[base + 32 * k]) * wv[k] * s;
+        }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+        hs += __shfl_xor_sync(0xffffffffu, hs, o);
+      }
+      const float rstd = rsqrtf(s2 / (float)p.cols + p.eps), q = hs * rstd * rstd / (float)p.cols;
+#pragma unroll
+      for (int k = 0; k < NA; ++k)
+        if (lane + 32 * k < p.cols) {
+          const int i = base + 32 * k;
+          const float s = to_f(ss_[i]), g = to_f(gs[i]);
+          float o = rstd * (g * wv[k] - s * q);
+          if (p.g_s) o += to_f(ts[i]);
+          acc[k] += g * (s * rstd);
+          gs[i] = from_f<T>(o);
+        }
+    }
+    __syncthreads();
+    copy_rows(static_cast<T*>(p.g_x) + row0 * p.cols, gs, bytes);
+    __syncthreads();
+  }
+  if (!p.part) return;
+  float* sum = reinterpret_cast<float*>(odd_sm);                  // [cols]; the warps in order
+  for (int q = 0; q < R; ++q) {
+    if (q) __syncthreads();
+    if (warp == q)
+#pragma unroll
+      for (int k = 0; k < NA; ++k)
+        if (lane + 32 * k < p.cols) sum[lane + 32 * k] = q ? sum[lane + 32 * k] + acc[k] : acc[k];
+  }
+  __syncthreads();
+  const int nout = p.degrees ? 4 * C : p.cols;
+  float* part = p.part + (size_t)blockIdx.x * nout;
+  for (int o = threadIdx.x; o < nout; o += ODD_THREADS) part[o] = p.degrees ? degree_sum(sum, o, C) : sum[o];
+}
+
 // Persistent: block b takes row groups b, b + gridDim.x, ...; a thread's columns are the same in
-// every row, so its part of g_w stays in registers until the end.
+// every row, so its part of g_w stays in registers until the end.  The next row's loads are issued before
+// the current row's reduction, so that some are always in flight.
+template <typename T, int V>
+struct Raw {                     // V elements as they are in memory
+  using U = std::conditional_t<V == 1, T, uint4>;
+  U u;
+  __device__ __forceinline__ void load(const T* p, bool in) {
+    if constexpr (V == 1) u = in ? *p : from_f<T>(0.f);
+    else u = in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float (&v)[V]) const {
+    if constexpr (V == 1) v[0] = to_f(u);
+    else unpack16<T, V>(u, v);
+  }
+};
+
 template <typename T, int V, int SL>
 __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm_grad(const GradArgs p) {
   extern __shared__ float acc_sm[];              // [cols] when the block has several rows or there are degrees
@@ -147,34 +340,48 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm_grad(const GradArgs p)
   const int C = p.cols / NCOMP;
   const T* w = static_cast<const T*>(p.w);
   float acc[SL][V];
+  Raw<T, V> g_[SL], s_[SL], t_[SL];
+  int at[SL];                                    // where a vector's weights are
 #pragma unroll
-  for (int k = 0; k < SL; ++k)
+  for (int k = 0; k < SL; ++k) {
+    const int c = (k * G + t) * V;
+    at[k] = c < p.cols ? weight_at(c, C, p.degrees) : 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[k][i] = 0.f;
+  }
+  auto fetch = [&](long long row) {
+    const bool live = row < p.rows;
+#pragma unroll
+    for (int k = 0; k < SL; ++k) {
+      const int c = (k * G + t) * V;
+      const bool in = live && c < p.cols;
+      g_[k].load(static_cast<const T*>(p.g) + row * p.ldg + c, in);
+      s_[k].load(static_cast<const T*>(p.s) + row * p.lds + c, in);
+      if (p.g_s) t_[k].load(static_cast<const T*>(p.g_s) + row * p.ldgs + c, in);
+    }
+  };
   const long long groups = (p.rows + R - 1) / R;
   int par = 0;
+  fetch((long long)blockIdx.x * R + r);
   for (long long b = blockIdx.x; b < groups; b += gridDim.x, par ^= 1) {
     const long long row = b * R + r;
     const bool live = row < p.rows;
     float g[SL][V], s[SL][V];
+    Raw<T, V> th[SL];
     float ss = 0.f, hs = 0.f;
 #pragma unroll
     for (int k = 0; k < SL; ++k) {
-      const int c = (k * G + t) * V;
-#pragma unroll
-      for (int i = 0; i < V; ++i) g[k][i] = s[k][i] = 0.f;
-      if (live && c < p.cols) {
-        load_v<T, V>(static_cast<const T*>(p.g) + row * p.ldg + c, g[k]);
-        load_v<T, V>(static_cast<const T*>(p.s) + row * p.lds + c, s[k]);
-      }
+      g_[k].get(g[k]);
+      s_[k].get(s[k]);
+      th[k] = t_[k];
     }
+    fetch(row + (long long)gridDim.x * R);
 #pragma unroll
     for (int k = 0; k < SL; ++k) {
-      const int c = (k * G + t) * V;
       float wv[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) wv[i] = 1.f;
-      if (w && c < p.cols) load_v<T, V>(w + weight_at(c, C, p.degrees), wv);
+      if (w) load_v<T, V>(w + at[k], wv);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         ss += s[k][i] * s[k][i];
@@ -204,8 +411,8 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm_grad(const GradArgs p)
       float wv[V], o[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) { wv[i] = 1.f; o[i] = 0.f; }
-      if (w) load_v<T, V>(w + weight_at(c, C, p.degrees), wv);
-      if (p.g_s) load_v<T, V>(static_cast<const T*>(p.g_s) + row * p.ldgs + c, o);
+      if (w) load_v<T, V>(w + at[k], wv);
+      if (p.g_s) th[k].get(o);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         o[i] += rstd * (g[k][i] * wv[i] - s[k][i] * q);
@@ -236,14 +443,7 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm_grad(const GradArgs p)
   if (direct) return;
   __syncthreads();
   for (int o = r * G + t; o < nout; o += G * R) {
-    if (!p.degrees) {
-      part[o] = acc_sm[o];
-    } else {                                     // the 2 l + 1 components of degree l
-      const int l = o / C, c = o - l * C;
-      float a = 0.f;
-      for (int q = l * l; q < (l + 1) * (l + 1); ++q) a += acc_sm[q * C + c];
-      part[o] = a;
-    }
+    part[o] = p.degrees ? degree_sum(acc_sm, o, C) : acc_sm[o];
   }
 }
 
@@ -277,23 +477,61 @@ void launch_fwd2(const Args& a, const Shape& h, bool quant, cudaStream_t st) {
   if (quant) k_rms_norm<T, V, SL, true><<<grid, block, 0, st>>>(a);
   else k_rms_norm<T, V, SL, false><<<grid, block, 0, st>>>(a);
 }
+// a kernel's dynamic shared memory above 48 KB has to be allowed, once per device
+template <auto KERNEL>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load() & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit);
+  return e;
+}
+template <typename T, bool QUANT, int RW>
+bool launch_odd3(const Args& a, int smem, cudaStream_t st) {
+  if (allow_smem<k_rms_norm_odd<T, QUANT, RW>>(ODD_SMEM) != cudaSuccess) return false;
+  const int R = RW * ODD_THREADS / 32;
+  k_rms_norm_odd<T, QUANT, RW><<<(unsigned)((a.rows + R - 1) / R), ODD_THREADS, smem, st>>>(a);
+  return true;
+}
+inline bool packed_rows(const void* p, long long ld, const Args& a) {       // contiguous, on a 16-byte boundary
+  return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld == a.cols || a.rows == 1));
+}
 template <typename T>
-void launch_fwd(const Args& a, bool quant, cudaStream_t st) {
+bool launch_odd(const Args& a, bool quant, cudaStream_t st) {
+  if (!packed_rows(a.x, a.ldx, a) || !packed_rows(a.residual, a.ldr, a) || !packed_rows(a.y, a.ldy, a) ||
+      !packed_rows(a.s, a.lds, a) || (a.s && !a.residual))
+    return false;
+  const int row = a.cols * (int)sizeof(T) * (a.residual ? 2 : 1) + (quant ? a.cols : 0);
+  const int per = ODD_THREADS / 32;                                // 8 rows, or 16 (which 8-bit rows need for 16 bytes)
+  const int s16 = 2 * per * row + 64, s8 = per * row + 64;
+  if (s16 <= ODD_SMEM && (quant || a.rows > 2 * per * 148)) return quant ? launch_odd3<T, true, 2>(a, s16, st) : launch_odd3<T, false, 2>(a, s16, st);
+  if (!quant && s8 <= ODD_SMEM) return launch_odd3<T, false, 1>(a, s8, st);
+  return false;
+}
+
+template <typename T>
+cudaError_t launch_fwd(const Args& a, bool quant, cudaStream_t st) {
   constexpr int ES = sizeof(T), V = 16 / ES;
   const bool yv = quant ? reinterpret_cast<uintptr_t>(a.y) % V == 0 && a.ldy % V == 0 : vec_ok(a.y, a.ldy, ES);
   const bool vec = a.cols % V == 0 && yv && vec_ok(a.x, a.ldx, ES) && vec_ok(a.residual, a.ldr, ES) &&
                    vec_ok(a.s, a.lds, ES) && vec_ok(a.w, 0, ES) && (!a.degrees || a.cols / NCOMP % V == 0);
-  const Shape h = shape_for(a.cols, vec ? V : 1, vec ? 16 / V : 16, a.rows);
+  if (!vec && launch_odd<T>(a, quant, st)) return cudaGetLastError();
+  const Shape h = shape_for(a.cols, vec ? V : 1, vec ? 4 : 16, a.rows);
   if (vec) {
     if (h.SL == 1) launch_fwd2<T, V, 1>(a, h, quant, st);
     else if (h.SL == 2) launch_fwd2<T, V, 2>(a, h, quant, st);
-    else launch_fwd2<T, V, 16 / V>(a, h, quant, st);
+    else launch_fwd2<T, V, 4>(a, h, quant, st);
   } else {
     if (h.SL == 1) launch_fwd2<T, 1, 1>(a, h, quant, st);
     else if (h.SL == 2) launch_fwd2<T, 1, 2>(a, h, quant, st);
     else if (h.SL == 4) launch_fwd2<T, 1, 4>(a, h, quant, st);
     else launch_fwd2<T, 1, 16>(a, h, quant, st);
   }
+  return cudaGetLastError();
 }
 
 // blocks of the gradient (each leaves one row of column sums): up to four per SM
@@ -308,7 +546,27 @@ Shape grad_shape(const GradArgs& a) {
   constexpr int ES = sizeof(T), V = 16 / ES;
   const bool vec = a.cols % V == 0 && vec_ok(a.g, a.ldg, ES) && vec_ok(a.s, a.lds, ES) && vec_ok(a.g_s, a.ldgs, ES) &&
                    vec_ok(a.g_x, a.ldgx, ES) && vec_ok(a.w, 0, ES) && (!a.degrees || a.cols / NCOMP % V == 0);
-  return shape_for(a.cols, vec ? V : 1, vec ? 16 / V : 16, a.rows);
+  return shape_for(a.cols, vec ? V : 1, !vec ? 16 : a.cols > MAX_THREADS * 2 * V ? 4 : 2, a.rows);
+}
+template <typename T, int NA>
+int launch_grad_odd3(const GradArgs& a, int smem, cudaStream_t st) {
+  if (allow_smem<k_rms_norm_grad_odd<T, NA>>(ODD_SMEM) != cudaSuccess) return 0;
+  const int blocks = grad_blocks(a.rows, ODD_THREADS / 32);
+  k_rms_norm_grad_odd<T, NA><<<blocks, ODD_THREADS, smem, st>>>(a);
+  return blocks;
+}
+template <typename T>
+int launch_grad_odd(const GradArgs& a, cudaStream_t st) {      // 0: not for these rows
+  auto packed = [&](const void* p, long long ld) {
+    return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld == a.cols || a.rows == 1));
+  };
+  const int smem = std::max(ODD_THREADS / 32 * a.cols * (int)sizeof(T) * (a.g_s ? 3 : 2), a.cols * 4);
+  if (a.cols > ODD_GRAD_COLS || smem > ODD_SMEM || !packed(a.g, a.ldg) || !packed(a.s, a.lds) || !packed(a.g_s, a.ldgs) ||
+      !packed(a.g_x, a.ldgx))
+    return 0;
+  if (a.cols <= 128) return launch_grad_odd3<T, 4>(a, smem, st);
+  if (a.cols <= 512) return launch_grad_odd3<T, 16>(a, smem, st);
+  return launch_grad_odd3<T, 32>(a, smem, st);
 }
 template <typename T>
 int launch_grad(const GradArgs& a, cudaStream_t st) {          // returns the rows of a.part
@@ -317,7 +575,9 @@ int launch_grad(const GradArgs& a, cudaStream_t st) {          // returns the ro
   if (h.V == V) {
     if (h.SL == 1) launch_grad2<T, V, 1>(a, h, st);
     else if (h.SL == 2) launch_grad2<T, V, 2>(a, h, st);
-    else launch_grad2<T, V, 16 / V>(a, h, st);
+    else if constexpr (V == 4) launch_grad2<T, V, 4>(a, h, st);      // 16-bit rows of the most columns take two
+  } else if (const int blocks = launch_grad_odd<T>(a, st)) {
+    return blocks;
   } else {
     if (h.SL == 1) launch_grad2<T, 1, 1>(a, h, st);
     else if (h.SL == 2) launch_grad2<T, 1, 2>(a, h, st);

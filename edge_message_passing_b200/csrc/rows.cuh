@@ -135,6 +135,15 @@ __device__ __forceinline__ void silu2(float& a, float& b) {
   b *= r * p;
 }
 
+// the derivatives of two values, s (1 + z (1 - s)) each, likewise
+__device__ __forceinline__ void dsilu2(float& a, float& b) {
+  const float p = 1.0f + __expf(-fmaxf(a, -43.0f)), q = 1.0f + __expf(-fmaxf(b, -43.0f));
+  const float r = __fdividef(1.0f, p * q);
+  const float sa = r * q, sb = r * p;
+  a = sa * (1.0f + a * (1.0f - sa));
+  b = sb * (1.0f + b * (1.0f - sb));
+}
+
 // ------------------------------------------------------------- join of column sums
 // out[j] = sum over b of part[b][j].  32 columns per block, JOIN_WARPS warps over the rows (warp w takes
 // rows w, w + JOIN_WARPS, ..., JOIN_BATCH loads at a time; the warps' sums are added in warp order), so the

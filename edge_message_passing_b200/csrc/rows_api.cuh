@@ -105,8 +105,8 @@ DenseGradLayout dense_grad_layout(const emp_dense_grad& a) {
   L.gz = take(L.prep ? (size_t)a.rows * L.ldgz * es : 0);
   if (!L.prep && a.rows > 1) L.ldgz = a.ldg;
   L.gz_vec = gz_vec(a, L);
-  const int per = 32 * (L.gz_vec ? 16 / es : 1);             // columns of a block; about four blocks per SM
-  L.gz_blocks = (int)std::max<long long>(1, std::min<long long>((a.rows + 31) / 32, 592 / ((a.fan_out + per - 1) / per)));
+  const int V = L.gz_vec ? 16 / es : 1, per = 32 * V;        // columns of a block; one wave of blocks
+  L.gz_blocks = (int)std::max<long long>(1, std::min<long long>((a.rows + 31) / 32, std::max(1, tc::num_sms() * dense::GZ_PER_SM / ((a.fan_out + per - 1) / per))));
   L.colsum = take(a.g_bias ? (size_t)L.gz_blocks * a.fan_out * 4 : 0);
   if (a.g_x) {
     L.w = packed(a.weight, a.ldw, a.fan_out, a.fan_in, a.dtype, take);
@@ -190,10 +190,10 @@ int mp_rms_norm(const emp_rms_norm* a, cudaStream_t stream) {
   if (st != EMP_OK) return st;
   norm::Args p{a->rows, a->cols, a->degrees, a->eps, a->x, a->residual, a->weight, a->y, a->s, a->scale, a->ldx, a->ldr, a->ldy, a->lds};
   Scope sc_("rms_norm", stream);
-  if (a->dtype == EMP_F32) norm::launch_fwd<float>(p, quant, stream);
-  else if (a->dtype == EMP_BF16) norm::launch_fwd<__nv_bfloat16>(p, quant, stream);
-  else norm::launch_fwd<__half>(p, quant, stream);
-  return cudaGetLastError() == cudaSuccess ? EMP_OK : EMP_ERR_CUDA;
+  const cudaError_t e = a->dtype == EMP_F32 ? norm::launch_fwd<float>(p, quant, stream)
+                      : a->dtype == EMP_BF16 ? norm::launch_fwd<__nv_bfloat16>(p, quant, stream)
+                                             : norm::launch_fwd<__half>(p, quant, stream);
+  return e == cudaSuccess ? EMP_OK : EMP_ERR_CUDA;
 }
 
 size_t mp_rms_norm_grad_workspace_bytes(const emp_rms_norm_grad* a) {
