@@ -11,8 +11,7 @@
 //
 // y in 8 bits: scale = max_j |y_j| / 448 per row, q = RN_e4m3(y / scale).  max |y| = rstd max |s w|
 // (rstd is one positive factor of the row), so the maximum is taken together with the sum of squares
-// and the row still needs one block-wide reduction.  The maximum is taken on the bits of |s w| as
-// unsigned integers, where a NaN is larger than every number, so a row with a NaN comes out as NaN.
+// and the row still needs one block-wide reduction.  The maximum keeps a NaN, so a row with one comes out as NaN.
 #pragma once
 #include <atomic>
 #include <type_traits>
@@ -50,17 +49,30 @@ __device__ __forceinline__ int weight_at(int col, int C, int degrees) {
   return degree_of(lm) * C + (col - lm * C);
 }
 
-// sum of a and maximum (as unsigned) of b over the G threads of a row; red: 32 float2-sized slots per row
-__device__ __forceinline__ void row_reduce(float& a, uint32_t& b, int G, int t, float* red_a, uint32_t* red_b) {
+// max(a, |b|), a NaN if either is one
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(fabsf(b)));
+  return m;
+}
+
+// sum of a and max_abs of b over the G threads of a row; red_a, red_b: a slot per warp of the row
+template <bool MAX>
+__device__ __forceinline__ void row_reduce(float& a, float& b, int G, int t, float* red_a, float* red_b) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-  b = __reduce_max_sync(0xffffffffu, b);
+  for (int o = 16; o; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    if (MAX) b = max_abs(b, __shfl_xor_sync(0xffffffffu, b, o));
+  }
   if (G > 32) {
     const int nw = G >> 5, w = t >> 5;
     if ((t & 31) == 0) { red_a[w] = a; red_b[w] = b; }
     __syncthreads();
     a = 0.f;
-    for (int i = 0; i < nw; ++i) { a += red_a[i]; b = max(b, red_b[i]); }
+    for (int i = 0; i < nw; ++i) {
+      a += red_a[i];
+      if (MAX) b = max_abs(b, red_b[i]);
+    }
   }
 }
 
@@ -74,8 +86,7 @@ __device__ __forceinline__ float degree_sum(const float* sums, int o, int C) {
 
 template <typename T, int V, int SL, bool QUANT>
 __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm(const Args p) {
-  __shared__ float red_a[32];
-  __shared__ uint32_t red_b[32];
+  __shared__ float red_a[32], red_b[32];
   const int G = blockDim.x, t = threadIdx.x, r = threadIdx.y;
   const long long row = (long long)blockIdx.x * blockDim.y + r;
   const bool live = row < p.rows;
@@ -84,8 +95,7 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm(const Args p) {
   const T* w = static_cast<const T*>(p.w);
   const int C = p.cols / NCOMP;
   float v[SL][V];
-  float ss = 0.f;
-  uint32_t top = 0;
+  float ss = 0.f, top = 0.f;
 #pragma unroll
   for (int k = 0; k < SL; ++k) {
     const int c = (k * G + t) * V;
@@ -107,31 +117,31 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm(const Args p) {
 #pragma unroll
       for (int i = 0; i < V; ++i) v[k][i] += a[k][i];
   }
-  // a thread's weights are read where they are used (twice for 8 bits; they stay in L1), not held: registers
-  // are what limits the rows in flight
-  auto weights = [&](int c, float (&wv)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) wv[i] = 1.f;
-    if (w && c < p.cols) load_v<T, V>(w + weight_at(c, C, p.degrees), wv);
-  };
+  // s needs no reduction: it is written now, and only the products s w are kept
 #pragma unroll
   for (int k = 0; k < SL; ++k) {
+    const int c = (k * G + t) * V;
+    if (p.s && live && c < p.cols) store_v<T, V>(static_cast<T*>(p.s) + row * p.lds + c, v[k]);
 #pragma unroll
     for (int i = 0; i < V; ++i) ss += v[k][i] * v[k][i];
-    if (QUANT) {
+    if (w && c < p.cols) {
       float wv[V];
-      weights((k * G + t) * V, wv);
+      load_v<T, V>(w + weight_at(c, C, p.degrees), wv);
 #pragma unroll
-      for (int i = 0; i < V; ++i) top = max(top, __float_as_uint(v[k][i] * wv[i]) & 0x7fffffffu);
+      for (int i = 0; i < V; ++i) v[k][i] *= wv[i];
+    }
+    if (QUANT) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) top = max_abs(top, v[k][i]);
     }
   }
   const int slot = r * (G >> 5);
-  row_reduce(ss, top, G, t, red_a + slot, red_b + slot);
+  row_reduce<QUANT>(ss, top, G, t, red_a + slot, red_b + slot);
   if (!live) return;
   const float rstd = rsqrtf(ss / (float)p.cols + p.eps);
   float inv = 1.f;
   if (QUANT) {
-    const float m = __uint_as_float(top) * rstd;
+    const float m = top * rstd;
     const float scale = m < TINY ? 1.f : m / 448.f;     // a NaN stays one
     inv = 1.f / scale;
     if (t == 0) p.scale[row] = scale;
@@ -140,11 +150,9 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm(const Args p) {
   for (int k = 0; k < SL; ++k) {
     const int c = (k * G + t) * V;
     if (c >= p.cols) continue;
-    if (p.s) store_v<T, V>(static_cast<T*>(p.s) + row * p.lds + c, v[k]);
-    float y[V], wv[V];
-    weights(c, wv);
+    float y[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) y[i] = v[k][i] * rstd * wv[i];
+    for (int i = 0; i < V; ++i) y[i] = v[k][i] * rstd;
     if (QUANT) {
 #pragma unroll
       for (int i = 0; i < V; ++i) y[i] *= inv;
@@ -188,10 +196,9 @@ __global__ void __launch_bounds__(ODD_THREADS) k_rms_norm_odd(const Args p) {
   __syncthreads();
   const bool two = p.residual != nullptr;
   const int first = warp * RW;
-  float ss[RW];
-  uint32_t top[RW];
+  float ss[RW], top[RW];
 #pragma unroll
-  for (int j = 0; j < RW; ++j) { ss[j] = 0.f; top[j] = 0; }
+  for (int j = 0; j < RW; ++j) ss[j] = top[j] = 0.f;
 #pragma unroll 4
   for (int c = lane; c < p.cols; c += 32) {
     const float wv = QUANT && w ? to_f(w[weight_at(c, C, p.degrees)]) : 1.f;
@@ -201,18 +208,21 @@ __global__ void __launch_bounds__(ODD_THREADS) k_rms_norm_odd(const Args p) {
       float v = first + j < rows ? to_f(xs[i]) : 0.f;
       if (two && first + j < rows) v += to_f(rs[i]);
       ss[j] += v * v;
-      if (QUANT) top[j] = max(top[j], __float_as_uint(v * wv) & 0x7fffffffu);
+      if (QUANT) top[j] = max_abs(top[j], v * wv);
     }
   }
   float rstd[RW], inv[RW];
 #pragma unroll
   for (int j = 0; j < RW; ++j) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) ss[j] += __shfl_xor_sync(0xffffffffu, ss[j], o);
+    for (int o = 16; o; o >>= 1) {
+      ss[j] += __shfl_xor_sync(0xffffffffu, ss[j], o);
+      if (QUANT) top[j] = max_abs(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+    }
     rstd[j] = rsqrtf(ss[j] / (float)p.cols + p.eps);
     inv[j] = 1.f;
     if (QUANT) {
-      const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, top[j])) * rstd[j];
+      const float m = top[j] * rstd[j];
       const float scale = m < TINY ? 1.f : m / 448.f;
       inv[j] = 1.f / scale;
       if (lane == 0 && first + j < rows) p.scale[row0 + first + j] = scale;
@@ -520,11 +530,12 @@ cudaError_t launch_fwd(const Args& a, bool quant, cudaStream_t st) {
   const bool vec = a.cols % V == 0 && yv && vec_ok(a.x, a.ldx, ES) && vec_ok(a.residual, a.ldr, ES) &&
                    vec_ok(a.s, a.lds, ES) && vec_ok(a.w, 0, ES) && (!a.degrees || a.cols / NCOMP % V == 0);
   if (!vec && launch_odd<T>(a, quant, st)) return cudaGetLastError();
-  const Shape h = shape_for(a.cols, vec ? V : 1, vec ? 4 : 16, a.rows);
+    // 16-bit rows: at most two vectors a thread (16384 x 2048 bf16 to e4m3: 59 us with one, 50 with two, 68 with four)
+  const Shape h = shape_for(a.cols, vec ? V : 1, vec ? 16 / V : 16, a.rows);
   if (vec) {
     if (h.SL == 1) launch_fwd2<T, V, 1>(a, h, quant, st);
     else if (h.SL == 2) launch_fwd2<T, V, 2>(a, h, quant, st);
-    else launch_fwd2<T, V, 4>(a, h, quant, st);
+    else if constexpr (V == 4) launch_fwd2<T, V, 4>(a, h, quant, st);
   } else {
     if (h.SL == 1) launch_fwd2<T, 1, 1>(a, h, quant, st);
     else if (h.SL == 2) launch_fwd2<T, 1, 2>(a, h, quant, st);

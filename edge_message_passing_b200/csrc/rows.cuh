@@ -32,10 +32,12 @@ template <> __device__ __forceinline__ void unpack2<__half>(uint32_t w, float& a
 }
 template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
 template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
-  return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(a)) | (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(b)) << 16;
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);      // one conversion for both
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
-  return (uint32_t)__half_as_ushort(__float2half_rn(a)) | (uint32_t)__half_as_ushort(__float2half_rn(b)) << 16;
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 // 16 bytes as floats: four of fp32 or eight of a 16-bit type
 template <typename T, int V>
