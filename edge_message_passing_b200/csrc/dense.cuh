@@ -162,7 +162,7 @@ struct GzArgs {
 };
 template <typename T, int V>
 __global__ void __launch_bounds__(32 * GZ_WARPS, GZ_PER_SM) k_dense_gz(const GzArgs p) {
-  constexpr int GZ_BATCH = V == 8 ? 1 : 2;
+  constexpr int GZ_BATCH = V == 8 ? 1 : V == 4 ? 2 : V == 2 ? 4 : 8;
   __shared__ float sm[GZ_WARPS][32 * V];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = (blockIdx.y * 32 + lane) * V;

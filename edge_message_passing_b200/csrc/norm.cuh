@@ -325,21 +325,274 @@ __global__ void __launch_bounds__(ODD_THREADS) k_rms_norm_grad_odd(const GradArg
   for (int o = threadIdx.x; o < nout; o += ODD_THREADS) part[o] = p.degrees ? degree_sum(sum, o, C) : sum[o];
 }
 
+// ------------------------------------------------------------------ any rows
+// The rest (pitches or starts off 16 bytes, or contiguous rows too long for the form above) is staged in
+// shared memory at the offset from a 16-byte boundary that a row has in memory, so that all but its first and
+// last bytes still move in 16-byte vectors.  Persistent teams of tw warps (1 to 8, so that a thread has at most 16 of a
+// row's columns, 32 beyond 4096), each with its own rows and no barrier but its own: while a row is
+// computed the next one is on its way (cp.async) into the team's other input slots.  A thread's columns are the
+// same in every row, so its weights, and its part of g_w, stay in registers.  Bound by instructions: some hundreds a row
+// and warp beside its elements.
+constexpr int ST_THREADS = 256, ST_WARPS = ST_THREADS / 32;
+
+__host__ __device__ constexpr int slot_bytes(int row_bytes) { return (row_bytes + 15) / 16 * 16 + 16; }
+__device__ __forceinline__ int phase_of(const void* p) { return (int)(reinterpret_cast<uintptr_t>(p) & 15); }
+
+struct Team {
+  int tw, n, r, t;                 // warps, threads, the team's number in the block, the thread's in the team
+  __device__ __forceinline__ explicit Team(int tw_) : tw(tw_), n(32 * tw_), r(threadIdx.x / (32 * tw_)), t(threadIdx.x % (32 * tw_)) {}
+  __device__ __forceinline__ void sync() const {
+    if (tw == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(r + 1), "r"(n) : "memory");
+  }
+};
+
+// A row's copy into its slot: 16-byte bodies by cp.async, the up to 15 bytes before and behind them as at most one
+// element each per thread, kept in registers until they are written.
+template <typename T>
+struct RowIn {
+  T head, tail;
+  __device__ __forceinline__ void issue(unsigned char* slot, const T* row, int cols, const Team& m) {
+    const int ph = phase_of(row), end = ph + cols * (int)sizeof(T);
+    const unsigned char* base = reinterpret_cast<const unsigned char*>(row) - ph;
+    const int first = ph ? 1 : 0, last = end >> 4;                     // whole chunks: first .. last - 1
+    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(slot);
+    for (int i = first + m.t; i < last; i += m.n)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 16), "l"(base + i * 16) : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const int h = head_at(ph, end, m.t), l = tail_at(ph, end, m.t);
+    if (h >= 0) head = *reinterpret_cast<const T*>(base + h);
+    if (l >= 0) tail = *reinterpret_cast<const T*>(base + l);
+  }
+  __device__ __forceinline__ void finish(unsigned char* slot, const T* row, int cols, const Team& m) const {
+    const int ph = phase_of(row), end = ph + cols * (int)sizeof(T);
+    const int h = head_at(ph, end, m.t), l = tail_at(ph, end, m.t);
+    if (h >= 0) *reinterpret_cast<T*>(slot + h) = head;
+    if (l >= 0) *reinterpret_cast<T*>(slot + l) = tail;
+  }
+  // byte offset of thread t's element before the first whole chunk and behind the last, or -1
+  static __device__ __forceinline__ int head_at(int ph, int end, int t) {
+    const int at = ph + t * (int)sizeof(T);
+    return ph && at < 16 && at < end ? at : -1;
+  }
+  static __device__ __forceinline__ int tail_at(int ph, int end, int t) {
+    const int from = end & ~15, at = from + t * (int)sizeof(T);
+    return at < end && !(from == 0 && ph) ? at : -1;                   // a row inside one chunk is all head
+  }
+};
+template <typename U>
+__device__ __forceinline__ void row_out(const unsigned char* slot, U* row, int cols, const Team& m) {
+  const int ph = phase_of(row), end = ph + cols * (int)sizeof(U);
+  unsigned char* base = reinterpret_cast<unsigned char*>(row) - ph;
+  for (int i = (ph ? 1 : 0) + m.t; i < (end >> 4); i += m.n) *reinterpret_cast<uint4*>(base + i * 16) = *reinterpret_cast<const uint4*>(slot + i * 16);
+  const int h = RowIn<U>::head_at(ph, end, m.t), l = RowIn<U>::tail_at(ph, end, m.t);
+  if (h >= 0) *reinterpret_cast<U*>(base + h) = *reinterpret_cast<const U*>(slot + h);
+  if (l >= 0) *reinterpret_cast<U*>(base + l) = *reinterpret_cast<const U*>(slot + l);
+}
+__device__ __forceinline__ void rows_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// sums (MAX: the second is max_abs) over a team
+template <bool MAX>
+__device__ __forceinline__ void team_reduce(float& a, float& b, const Team& m, float (*red)[2]) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    const float c = __shfl_xor_sync(0xffffffffu, b, o);
+    b = MAX ? max_abs(b, c) : b + c;
+  }
+  if (m.tw == 1) return;
+  const int w0 = m.r * m.tw;
+  if ((m.t & 31) == 0) { red[w0 + (m.t >> 5)][0] = a; red[w0 + (m.t >> 5)][1] = b; }
+  m.sync();
+  a = red[w0][0];
+  b = red[w0][1];
+  for (int i = 1; i < m.tw; ++i) {
+    a += red[w0 + i][0];
+    b = MAX ? max_abs(b, red[w0 + i][1]) : b + red[w0 + i][1];
+  }
+}
+
+// Shared memory of a team: `stages` sets of input slots (two where they fit), then the output slots.
+template <typename T, bool QUANT, int NA>
+__global__ void __launch_bounds__(ST_THREADS, NA > 16 ? 2 : 4) k_rms_norm_staged(const Args p, int tw, int stages) {
+  extern __shared__ __align__(16) unsigned char st_sm[];
+  __shared__ float red[ST_WARPS][2];
+  const Team m(tw);
+  const int C = p.cols / NCOMP, R = ST_WARPS / tw, slot = slot_bytes(p.cols * (int)sizeof(T)), ni = p.residual ? 2 : 1;
+  unsigned char* in = st_sm + m.r * slot * (stages * ni + (p.s ? 2 : 1));
+  unsigned char* ys = in + stages * ni * slot;
+  unsigned char* ss_ = ys + slot;
+  const T* w = static_cast<const T*>(p.w);
+  float wv[NA];
+#pragma unroll
+  for (int k = 0; k < NA; ++k) {
+    const int c = m.t + m.n * k;
+    wv[k] = w && c < p.cols ? to_f(w[weight_at(c, C, p.degrees)]) : 1.f;
+  }
+  auto x_row = [&](long long row) { return static_cast<const T*>(p.x) + row * p.ldx; };
+  auto r_row = [&](long long row) { return static_cast<const T*>(p.residual) + row * p.ldr; };
+  RowIn<T> xi, ri;
+  auto issue = [&](long long row, int st) {
+    if (row >= p.rows) return;
+    xi.issue(in + st * ni * slot, x_row(row), p.cols, m);
+    if (p.residual) ri.issue(in + (st * ni + 1) * slot, r_row(row), p.cols, m);
+  };
+  const long long step = (long long)gridDim.x * R;
+  long long row = (long long)blockIdx.x * R + m.r;
+  int st = 0;
+  issue(row, 0);
+  for (; row < p.rows; row += step) {
+    unsigned char* xs = in + st * ni * slot;
+    unsigned char* rs = xs + slot;
+    xi.finish(xs, x_row(row), p.cols, m);
+    if (p.residual) ri.finish(rs, r_row(row), p.cols, m);
+    rows_landed();
+    m.sync();
+    if (stages == 2) issue(row + step, st ^ 1);
+    const T* xv = reinterpret_cast<const T*>(xs + phase_of(x_row(row)));
+    const T* rv = reinterpret_cast<const T*>(rs + phase_of(r_row(row)));
+    T* srow = static_cast<T*>(p.s) + row * p.lds;
+    T* sv = reinterpret_cast<T*>(ss_ + phase_of(srow));
+    float v[NA], ss = 0.f, top = 0.f;
+#pragma unroll
+    for (int k = 0; k < NA; ++k) {
+      const int c = m.t + m.n * k;
+      v[k] = 0.f;
+      if (c < p.cols) {
+        v[k] = to_f(xv[c]);
+        if (p.residual) v[k] += to_f(rv[c]);
+        if (p.s) sv[c] = from_f<T>(v[k]);
+      }
+      ss += v[k] * v[k];
+      v[k] *= wv[k];
+      if (QUANT) top = max_abs(top, v[k]);
+    }
+    team_reduce<true>(ss, top, m, red);
+    const float rstd = rsqrtf(ss / (float)p.cols + p.eps);
+    float inv = 1.f;
+    if (QUANT) {
+      const float big = top * rstd;
+      const float scale = big < TINY ? 1.f : big / 448.f;
+      inv = 1.f / scale;
+      if (m.t == 0) p.scale[row] = scale;
+    }
+    T* yrow = static_cast<T*>(p.y) + row * p.ldy;
+    __nv_fp8_storage_t* qrow = static_cast<__nv_fp8_storage_t*>(p.y) + row * p.ldy;
+    T* yv = reinterpret_cast<T*>(ys + phase_of(yrow));
+    __nv_fp8_storage_t* qv = ys + phase_of(qrow);
+#pragma unroll
+    for (int k = 0; k < NA; ++k) {
+      const int c = m.t + m.n * k;
+      if (c >= p.cols) continue;
+      if (QUANT) qv[c] = __nv_cvt_float_to_fp8(v[k] * rstd * inv, __NV_SATFINITE, __NV_E4M3);
+      else yv[c] = from_f<T>(v[k] * rstd);
+    }
+    m.sync();
+    if (stages == 1) issue(row + step, 0);
+    if (QUANT) row_out<__nv_fp8_storage_t>(ys, qrow, p.cols, m);
+    else row_out<T>(ys, yrow, p.cols, m);
+    if (p.s) row_out<T>(ss_, srow, p.cols, m);
+    if (stages == 2) st ^= 1;
+  }
+}
+
+template <typename T, int NA>
+__global__ void __launch_bounds__(ST_THREADS, NA > 16 ? 2 : 3) k_rms_norm_grad_staged(const GradArgs p, int tw, int stages) {
+  extern __shared__ __align__(16) unsigned char st_sm[];
+  __shared__ float red[ST_WARPS][2];
+  const Team m(tw);
+  const int C = p.cols / NCOMP, R = ST_WARPS / tw, slot = slot_bytes(p.cols * (int)sizeof(T)), ni = p.g_s ? 3 : 2;
+  unsigned char* in = st_sm + m.r * slot * (stages * ni + 1);
+  unsigned char* os = in + stages * ni * slot;
+  const T* w = static_cast<const T*>(p.w);
+  float acc[NA], wv[NA];
+#pragma unroll
+  for (int k = 0; k < NA; ++k) {
+    const int c = m.t + m.n * k;
+    acc[k] = 0.f;
+    wv[k] = w && c < p.cols ? to_f(w[weight_at(c, C, p.degrees)]) : 1.f;
+  }
+  auto g_row = [&](long long row) { return static_cast<const T*>(p.g) + row * p.ldg; };
+  auto s_row = [&](long long row) { return static_cast<const T*>(p.s) + row * p.lds; };
+  auto t_row = [&](long long row) { return static_cast<const T*>(p.g_s) + row * p.ldgs; };
+  RowIn<T> gi, si, ti;
+  auto issue = [&](long long row, int st) {
+    if (row >= p.rows) return;
+    unsigned char* a = in + st * ni * slot;
+    gi.issue(a, g_row(row), p.cols, m);
+    si.issue(a + slot, s_row(row), p.cols, m);
+    if (p.g_s) ti.issue(a + 2 * slot, t_row(row), p.cols, m);
+  };
+  const long long step = (long long)gridDim.x * R;
+  long long row = (long long)blockIdx.x * R + m.r;
+  int st = 0;
+  issue(row, 0);
+  for (; row < p.rows; row += step) {
+    unsigned char* a = in + st * ni * slot;
+    gi.finish(a, g_row(row), p.cols, m);
+    si.finish(a + slot, s_row(row), p.cols, m);
+    if (p.g_s) ti.finish(a + 2 * slot, t_row(row), p.cols, m);
+    rows_landed();
+    m.sync();
+    if (stages == 2) issue(row + step, st ^ 1);
+    const T* gv = reinterpret_cast<const T*>(a + phase_of(g_row(row)));
+    const T* sv = reinterpret_cast<const T*>(a + slot + phase_of(s_row(row)));
+    const T* tv = reinterpret_cast<const T*>(a + 2 * slot + phase_of(t_row(row)));
+    float s2 = 0.f, hs = 0.f;
+#pragma unroll
+    for (int k = 0; k < NA; ++k) {
+      const int c = m.t + m.n * k;
+      if (c >= p.cols) continue;
+      const float v = to_f(sv[c]);
+      s2 += v * v;
+      hs += to_f(gv[c]) * wv[k] * v;
+    }
+    team_reduce<false>(s2, hs, m, red);
+    const float rstd = rsqrtf(s2 / (float)p.cols + p.eps), q = hs * rstd * rstd / (float)p.cols;
+    T* out = static_cast<T*>(p.g_x) + row * p.ldgx;
+    T* ov = reinterpret_cast<T*>(os + phase_of(out));
+#pragma unroll
+    for (int k = 0; k < NA; ++k) {
+      const int c = m.t + m.n * k;
+      if (c >= p.cols) continue;
+      const float v = to_f(sv[c]), g = to_f(gv[c]);
+      float o = rstd * (g * wv[k] - v * q);
+      if (p.g_s) o += to_f(tv[c]);
+      acc[k] += g * (v * rstd);
+      ov[c] = from_f<T>(o);
+    }
+    m.sync();
+    if (stages == 1) issue(row + step, 0);
+    row_out<T>(os, out, p.cols, m);
+    if (stages == 2) st ^= 1;
+  }
+  if (!p.part) return;
+  __syncthreads();
+  float* sum = reinterpret_cast<float*>(st_sm);                // [cols]; the block's teams in order
+  for (int q = 0; q < R; ++q) {
+    if (q) __syncthreads();
+    if (m.r == q) {
+#pragma unroll
+      for (int k = 0; k < NA; ++k) {
+        const int c = m.t + m.n * k;
+        if (c < p.cols) sum[c] = q ? sum[c] + acc[k] : acc[k];
+      }
+    }
+  }
+  __syncthreads();
+  const int nout = p.degrees ? 4 * C : p.cols;
+  float* part = p.part + (size_t)blockIdx.x * nout;
+  for (int o = threadIdx.x; o < nout; o += ST_THREADS) part[o] = p.degrees ? degree_sum(sum, o, C) : sum[o];
+}
+
 // Persistent: block b takes row groups b, b + gridDim.x, ...; a thread's columns are the same in
 // every row, so its part of g_w stays in registers until the end.  The next row's loads are issued before
 // the current row's reduction, so that some are always in flight.
 template <typename T, int V>
 struct Raw {                     // V elements as they are in memory
-  using U = std::conditional_t<V == 1, T, uint4>;
-  U u;
-  __device__ __forceinline__ void load(const T* p, bool in) {
-    if constexpr (V == 1) u = in ? *p : from_f<T>(0.f);
-    else u = in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ void get(float (&v)[V]) const {
-    if constexpr (V == 1) v[0] = to_f(u);
-    else unpack16<T, V>(u, v);
-  }
+  uint4 u;
+  __device__ __forceinline__ void load(const T* p, bool in) { u = in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&v)[V]) const { unpack16<T, V>(u, v); }
 };
 
 template <typename T, int V, int SL>
@@ -457,35 +710,25 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm_grad(const GradArgs p)
   }
 }
 
-// Launch shape: a row's V-element vectors fill a warp first, then each thread takes up to `most` of
+// Launch shape of the vector kernels: a row's vectors fill a warp first, then each thread takes up to `most` of
 // them, then the row gets more warps; short rows share a block of up to 256 threads, fewer when there
 // are not enough rows for two blocks on every SM.
 struct Shape {
-  int V, SL, G, R;
+  int SL, G, R;
 };
 inline Shape shape_for(int cols, int V, int most, long long rows) {
   Shape s;
-  s.V = V;
   const int n = (cols + V - 1) / V;
   s.SL = 1;
   while (s.SL < most && n > 32 * s.SL) s.SL *= 2;
-  if (s.SL == 8) s.SL = 16;                          // the element-wise form has 1, 2, 4 or 16
   s.G = (n + 32 * s.SL - 1) / (32 * s.SL) * 32;
   s.R = (int)std::max<long long>(1, std::min<long long>(256 / s.G, rows / 296));
   return s;
 }
 
 // 16-byte vectors need every pointer and row pitch in use to allow them
-inline bool vec_ok(const void* p, long long ld, int es) {
-  return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0);
-}
-
-template <typename T, int V, int SL>
-void launch_fwd2(const Args& a, const Shape& h, bool quant, cudaStream_t st) {
-  const dim3 block(h.G, h.R);
-  const unsigned grid = (unsigned)((a.rows + h.R - 1) / h.R);
-  if (quant) k_rms_norm<T, V, SL, true><<<grid, block, 0, st>>>(a);
-  else k_rms_norm<T, V, SL, false><<<grid, block, 0, st>>>(a);
+inline bool vec_ok(const void* p, long long ld, long long rows, int es) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows == 1 || ld * es % 16 == 0));
 }
 // a kernel's dynamic shared memory above 48 KB has to be allowed, once per device
 template <auto KERNEL>
@@ -499,6 +742,47 @@ cudaError_t allow_smem(int bytes) {
   e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) done.fetch_or(bit);
   return e;
+}
+constexpr int ST_SMEM = 220 * 1024;                            // one row of the most columns, its inputs and outputs, fits
+
+template <typename T, int V, int SL>
+void launch_fwd2(const Args& a, const Shape& h, bool quant, cudaStream_t st) {
+  const dim3 block(h.G, h.R);
+  const unsigned grid = (unsigned)((a.rows + h.R - 1) / h.R);
+  if (quant) k_rms_norm<T, V, SL, true><<<grid, block, 0, st>>>(a);
+  else k_rms_norm<T, V, SL, false><<<grid, block, 0, st>>>(a);
+}
+// blocks of the persistent kernels (the gradient's each leave one row of column sums): up to four per SM
+inline int grad_blocks(long long rows, int R) { return (int)std::min<long long>((rows + R - 1) / R, 4 * 148); }
+
+struct Staged {
+  int tw, R, stages, smem, NA;
+};
+inline Staged staged_for(int cols, int es, int ins, int outs) {
+  Staged h;
+  h.tw = 1;
+  while (h.tw < ST_WARPS && cols > 32 * 16 * h.tw) h.tw *= 2;
+  h.R = ST_WARPS / h.tw;
+  const int per = h.R * slot_bytes(cols * es);
+  h.stages = per * (2 * ins + outs) <= ST_SMEM / 2 ? 2 : 1;            // two where two blocks fit on an SM
+  h.smem = std::max(per * (h.stages * ins + outs), cols * 4);
+  h.NA = cols <= 128 ? 4 : cols <= 32 * 16 * h.tw ? 16 : 32;
+  return h;
+}
+template <auto KERNEL, typename A>
+cudaError_t launch_staged(const A& a, const Staged& h, int blocks, cudaStream_t st) {
+  const cudaError_t e = allow_smem<KERNEL>(ST_SMEM);
+  if (e != cudaSuccess) return e;
+  KERNEL<<<blocks, ST_THREADS, h.smem, st>>>(a, h.tw, h.stages);
+  return cudaGetLastError();
+}
+template <typename T, bool QUANT>
+cudaError_t launch_fwd_staged(const Args& a, cudaStream_t st) {
+  const Staged h = staged_for(a.cols, sizeof(T), a.residual ? 2 : 1, a.s ? 2 : 1);
+  const int blocks = grad_blocks(a.rows, h.R);
+  if (h.NA == 4) return launch_staged<k_rms_norm_staged<T, QUANT, 4>>(a, h, blocks, st);
+  if (h.NA == 16) return launch_staged<k_rms_norm_staged<T, QUANT, 16>>(a, h, blocks, st);
+  return launch_staged<k_rms_norm_staged<T, QUANT, 32>>(a, h, blocks, st);
 }
 template <typename T, bool QUANT, int RW>
 bool launch_odd3(const Args& a, int smem, cudaStream_t st) {
@@ -526,38 +810,22 @@ bool launch_odd(const Args& a, bool quant, cudaStream_t st) {
 template <typename T>
 cudaError_t launch_fwd(const Args& a, bool quant, cudaStream_t st) {
   constexpr int ES = sizeof(T), V = 16 / ES;
-  const bool yv = quant ? reinterpret_cast<uintptr_t>(a.y) % V == 0 && a.ldy % V == 0 : vec_ok(a.y, a.ldy, ES);
-  const bool vec = a.cols % V == 0 && yv && vec_ok(a.x, a.ldx, ES) && vec_ok(a.residual, a.ldr, ES) &&
-                   vec_ok(a.s, a.lds, ES) && vec_ok(a.w, 0, ES) && (!a.degrees || a.cols / NCOMP % V == 0);
+  const bool yv = quant ? reinterpret_cast<uintptr_t>(a.y) % V == 0 && (a.rows == 1 || a.ldy % V == 0) : vec_ok(a.y, a.ldy, a.rows, ES);
+  const bool vec = a.cols % V == 0 && yv && vec_ok(a.x, a.ldx, a.rows, ES) && vec_ok(a.residual, a.ldr, a.rows, ES) &&
+                   vec_ok(a.s, a.lds, a.rows, ES) && vec_ok(a.w, 0, 1, ES) && (!a.degrees || a.cols / NCOMP % V == 0);
   if (!vec && launch_odd<T>(a, quant, st)) return cudaGetLastError();
-    // 16-bit rows: at most two vectors a thread (16384 x 2048 bf16 to e4m3: 59 us with one, 50 with two, 68 with four)
-  const Shape h = shape_for(a.cols, vec ? V : 1, vec ? 16 / V : 16, a.rows);
-  if (vec) {
-    if (h.SL == 1) launch_fwd2<T, V, 1>(a, h, quant, st);
-    else if (h.SL == 2) launch_fwd2<T, V, 2>(a, h, quant, st);
-    else if constexpr (V == 4) launch_fwd2<T, V, 4>(a, h, quant, st);
-  } else {
-    if (h.SL == 1) launch_fwd2<T, 1, 1>(a, h, quant, st);
-    else if (h.SL == 2) launch_fwd2<T, 1, 2>(a, h, quant, st);
-    else if (h.SL == 4) launch_fwd2<T, 1, 4>(a, h, quant, st);
-    else launch_fwd2<T, 1, 16>(a, h, quant, st);
-  }
+  if (!vec) return quant ? launch_fwd_staged<T, true>(a, st) : launch_fwd_staged<T, false>(a, st);
+  // at most 16 elements a thread (16384 x 2048 bf16 to e4m3: 59 us with 8, 50 with 16, 68 with 32)
+  const Shape h = shape_for(a.cols, V, 16 / V, a.rows);
+  if (h.SL == 1) launch_fwd2<T, V, 1>(a, h, quant, st);
+  else if (h.SL == 2) launch_fwd2<T, V, 2>(a, h, quant, st);
+  else if constexpr (V == 4) launch_fwd2<T, V, 4>(a, h, quant, st);
   return cudaGetLastError();
 }
-
-// blocks of the gradient (each leaves one row of column sums): up to four per SM
-inline int grad_blocks(long long rows, int R) { return (int)std::min<long long>((rows + R - 1) / R, 4 * 148); }
 
 template <typename T, int V, int SL>
 void launch_grad2(const GradArgs& a, const Shape& h, cudaStream_t st) {
   k_rms_norm_grad<T, V, SL><<<grad_blocks(a.rows, h.R), dim3(h.G, h.R), h.R > 1 || a.degrees ? a.cols * 4 : 0, st>>>(a);
-}
-template <typename T>
-Shape grad_shape(const GradArgs& a) {
-  constexpr int ES = sizeof(T), V = 16 / ES;
-  const bool vec = a.cols % V == 0 && vec_ok(a.g, a.ldg, ES) && vec_ok(a.s, a.lds, ES) && vec_ok(a.g_s, a.ldgs, ES) &&
-                   vec_ok(a.g_x, a.ldgx, ES) && vec_ok(a.w, 0, ES) && (!a.degrees || a.cols / NCOMP % V == 0);
-  return shape_for(a.cols, vec ? V : 1, !vec ? 16 : a.cols > MAX_THREADS * 2 * V ? 4 : 2, a.rows);
 }
 template <typename T, int NA>
 int launch_grad_odd3(const GradArgs& a, int smem, cudaStream_t st) {
@@ -580,22 +848,25 @@ int launch_grad_odd(const GradArgs& a, cudaStream_t st) {      // 0: not for the
   return launch_grad_odd3<T, 32>(a, smem, st);
 }
 template <typename T>
-int launch_grad(const GradArgs& a, cudaStream_t st) {          // returns the rows of a.part
-  constexpr int V = 16 / sizeof(T);
-  const Shape h = grad_shape<T>(a);
-  if (h.V == V) {
-    if (h.SL == 1) launch_grad2<T, V, 1>(a, h, st);
-    else if (h.SL == 2) launch_grad2<T, V, 2>(a, h, st);
-    else if constexpr (V == 4) launch_grad2<T, V, 4>(a, h, st);      // 16-bit rows of the most columns take two
-  } else if (const int blocks = launch_grad_odd<T>(a, st)) {
-    return blocks;
-  } else {
-    if (h.SL == 1) launch_grad2<T, 1, 1>(a, h, st);
-    else if (h.SL == 2) launch_grad2<T, 1, 2>(a, h, st);
-    else if (h.SL == 4) launch_grad2<T, 1, 4>(a, h, st);
-    else launch_grad2<T, 1, 16>(a, h, st);
+cudaError_t launch_grad(const GradArgs& a, int* blocks, cudaStream_t st) {          // *blocks: the rows of a.part
+  constexpr int ES = sizeof(T), V = 16 / ES;
+  const bool vec = a.cols % V == 0 && vec_ok(a.g, a.ldg, a.rows, ES) && vec_ok(a.s, a.lds, a.rows, ES) &&
+                   vec_ok(a.g_s, a.ldgs, a.rows, ES) && vec_ok(a.g_x, a.ldgx, a.rows, ES) && vec_ok(a.w, 0, 1, ES) &&
+                   (!a.degrees || a.cols / NCOMP % V == 0);
+  if (!vec) {
+    if ((*blocks = launch_grad_odd<T>(a, st)) > 0) return cudaGetLastError();
+    const Staged h = staged_for(a.cols, ES, a.g_s ? 3 : 2, 1);
+    *blocks = grad_blocks(a.rows, h.R);
+    if (h.NA == 4) return launch_staged<k_rms_norm_grad_staged<T, 4>>(a, h, *blocks, st);
+    if (h.NA == 16) return launch_staged<k_rms_norm_grad_staged<T, 16>>(a, h, *blocks, st);
+    return launch_staged<k_rms_norm_grad_staged<T, 32>>(a, h, *blocks, st);
   }
-  return grad_blocks(a.rows, h.R);
+  const Shape h = shape_for(a.cols, V, a.cols > MAX_THREADS * 2 * V ? 4 : 2, a.rows);
+  *blocks = grad_blocks(a.rows, h.R);
+  if (h.SL == 1) launch_grad2<T, V, 1>(a, h, st);
+  else if (h.SL == 2) launch_grad2<T, V, 2>(a, h, st);
+  else if constexpr (V == 4) launch_grad2<T, V, 4>(a, h, st);      // 16-bit rows of the most columns take two
+  return cudaGetLastError();
 }
 
 }  // namespace norm

@@ -48,7 +48,7 @@ __device__ __forceinline__ void unpack16(const uint4& u, float (&v)[V]) {
     unpack2<T>(u.x, v[0], v[1]); unpack2<T>(u.y, v[2], v[3]); unpack2<T>(u.z, v[4], v[5]); unpack2<T>(u.w, v[6], v[7]);
   }
 }
-// V consecutive elements as floats; V > 1: 16 bytes (8 of e4m3), p aligned to them
+// V consecutive elements as floats; V > 1: 16 bytes (4 for V = 2, 8 of e4m3), p aligned to them
 template <typename T, int V>
 __device__ __forceinline__ void load_v(const T* p, float (&v)[V]) {
   if constexpr (V == 1) {
@@ -62,6 +62,8 @@ __device__ __forceinline__ void load_v(const T* p, float (&v)[V]) {
       e.__x = (unsigned char)((i < 4 ? u.x : u.y) >> (8 * (i & 3)));
       v[i] = (float)e;
     }
+  } else if constexpr (V == 2) {
+    unpack2<T>(*reinterpret_cast<const uint32_t*>(p), v[0], v[1]);
   } else {
     static_assert(V * sizeof(T) == 16, "vector bytes");
     unpack16<T, V>(*reinterpret_cast<const uint4*>(p), v);
@@ -71,6 +73,8 @@ template <typename T, int V>
 __device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
   if constexpr (V == 1) {
     *p = from_f<T>(v[0]);
+  } else if constexpr (V == 2) {
+    *reinterpret_cast<uint32_t*>(p) = pack2<T>(v[0], v[1]);
   } else if constexpr (V == 4) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   } else {
@@ -114,19 +118,38 @@ __device__ __forceinline__ void store_any(void* p, size_t i, int t, float v) {
 __device__ __forceinline__ int degree_of(int lm) { return (lm > 0) + (lm > 3) + (lm > 8); }
 
 // ------------------------------------------------------------- activations
-// SiLU z/(1+exp(-z)) and GELU z Phi(z) (Phi by erf, no tanh form), and their derivatives
+// SiLU z / (1 + exp(-z)) and GELU z Phi(z), and their derivatives.  Phi, the normal distribution function, is
+// 1/2 erfc(-z / sqrt 2) with the rational approximation 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical
+// Functions (1964): erfc(x) = t (a1 + t (a2 + ...)) exp(-x^2), t = 1 / (1 + p x), within 1.5e-7 for x >= 0; erff costs
+// twice as much and bounds a short-k epilogue.  The error of GELU is below 1e-7 |z|, one and a half FP32 steps of z.
+__device__ __forceinline__ float phi_from(float z, float t, float e) {      // t = 1 / (1 + p x), e = exp(-x^2), x = |z| / sqrt 2
+  float q = fmaf(t, 1.061405429f, -1.453152027f);
+  q = fmaf(t, q, 1.421413741f);
+  q = fmaf(t, q, -0.284496736f);
+  q = fmaf(t, q, 0.254829592f);
+  const float h = 0.5f * t * q * e;                       // Phi(-|z|)
+  return z < 0.f ? h : 1.f - h;
+}
+constexpr float GELU_P = 0.3275911f * 0.70710678f;        // p / sqrt 2
+__device__ __forceinline__ float phi_f(float z, float* gauss) {             // Phi(z); *gauss = exp(-z^2 / 2)
+  *gauss = __expf(-0.5f * z * z);
+  return phi_from(z, __fdividef(1.f, fmaf(GELU_P, fabsf(z), 1.f)), *gauss);
+}
 __device__ __forceinline__ float act_f(int act, float z) {
   if (act == EMP_ACT_SILU) return silu_f(z);
-  if (act == EMP_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  float g;
+  if (act == EMP_ACT_GELU) return z * phi_f(z, &g);
   return z;
 }
 __device__ __forceinline__ float dact_f(int act, float z) {
   if (act == EMP_ACT_SILU) return dsilu_f(z);
-  if (act == EMP_ACT_GELU)
-    return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+  if (act == EMP_ACT_GELU) {
+    float g;
+    const float phi = phi_f(z, &g);
+    return phi + z * 0.39894228040143268f * g;
+  }
   return 1.0f;
 }
-
 // SiLU of two values with one reciprocal: 1 / (p q) gives 1 / p and 1 / q.  The exponentials are capped at
 // e^43 so that the product stays finite (z < -43 comes out as z e^-43, 1e-17 at most); the cap also keeps a NaN
 // from the other value.  Three special-function instructions instead of four: they bound a short-k epilogue.

@@ -75,25 +75,35 @@ DenseLayout dense_layout(const emp_dense& a) {
 struct DenseGradLayout {
   size_t gz = 0, colsum = 0, part_x = 0, part_w = 0, total = 0;
   long long ldgz = 0;
-  bool gz_vec = false;           // g and z (and gz) in 16-byte vectors
+  int gz_v = 1;                  // elements of g and z (and gz) read at once
   bool prep = false;             // gz is written (an activation, or g that TMA cannot read)
   int gz_blocks = 0;
   Packed x, w;
   dtc::Shape hx{}, hw{};
 };
-bool gz_vec(const emp_dense_grad& a, const DenseGradLayout& L) {
+// elements that g and z allow to be read at once: 16 bytes, a 32-bit word, or one
+int gz_vec(const emp_dense_grad& a) {
   const int es = dtype_size(a.dtype);
-  auto ok = [&](const void* p, long long ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (a.rows == 1 || ld * es % 16 == 0); };
-  return a.fan_out * es % 16 == 0 && ok(a.g, a.ldg) && ok(a.z, a.ldz);
+  for (int bytes = 16; bytes > es; bytes = 4) {
+    auto ok = [&](const void* p, long long ld) { return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (a.rows == 1 || ld * es % bytes == 0); };
+    if (a.fan_out * es % bytes == 0 && ok(a.g, a.ldg) && ok(a.z, a.ldz)) return bytes / es;
+    if (bytes == 4) break;
+  }
+  return 1;
+}
+template <typename T, int V>
+void dense_gz_v(const dense::GzArgs& z, int blocks, cudaStream_t s) {
+  const dim3 grid(blocks, (z.cols + 32 * V - 1) / (32 * V));
+  Scope sc_("dense_gz", s);
+  dense::k_dense_gz<T, V><<<grid, 32 * dense::GZ_WARPS, 0, s>>>(z);
 }
 template <typename T>
-void dense_gz(const dense::GzArgs& z, int blocks, bool vec, cudaStream_t s) {
-  constexpr int V = 16 / sizeof(T);
-  const int per = 32 * (vec ? V : 1);
-  const dim3 grid(blocks, (z.cols + per - 1) / per);
-  Scope sc_("dense_gz", s);
-  if (vec) dense::k_dense_gz<T, V><<<grid, 32 * dense::GZ_WARPS, 0, s>>>(z);
-  else dense::k_dense_gz<T, 1><<<grid, 32 * dense::GZ_WARPS, 0, s>>>(z);
+void dense_gz(const dense::GzArgs& z, int blocks, int V, cudaStream_t s) {
+  if (V == 1) return dense_gz_v<T, 1>(z, blocks, s);
+  if constexpr (sizeof(T) == 2) {
+    if (V == 2) return dense_gz_v<T, 2>(z, blocks, s);
+  }
+  dense_gz_v<T, 16 / sizeof(T)>(z, blocks, s);
 }
 DenseGradLayout dense_grad_layout(const emp_dense_grad& a) {
   DenseGradLayout L{};
@@ -104,8 +114,8 @@ DenseGradLayout dense_grad_layout(const emp_dense_grad& a) {
   L.prep = products && (a.activation != EMP_ACT_NONE || !dtc::tma_ok(a.g, a.rows == 1 ? 0 : a.ldg, a.dtype));
   L.gz = take(L.prep ? (size_t)a.rows * L.ldgz * es : 0);
   if (!L.prep && a.rows > 1) L.ldgz = a.ldg;
-  L.gz_vec = gz_vec(a, L);
-  const int V = L.gz_vec ? 16 / es : 1, per = 32 * V;        // columns of a block; one wave of blocks
+  L.gz_v = gz_vec(a);
+  const int per = 32 * L.gz_v;        // columns of a block; one wave of blocks
   L.gz_blocks = (int)std::max<long long>(1, std::min<long long>((a.rows + 31) / 32, std::max(1, tc::num_sms() * dense::GZ_PER_SM / ((a.fan_out + per - 1) / per))));
   L.colsum = take(a.g_bias ? (size_t)L.gz_blocks * a.fan_out * 4 : 0);
   if (a.g_x) {
@@ -152,7 +162,10 @@ int dense_product(long long M, int N, long long K, int t, const dtc::Operand& a,
   { Scope sc_("dense", s); st = dtc::launch(M, N, K, t, a, b, e, h, h.splits > 1 ? part : nullptr, s); }
   if (st != EMP_OK || h.splits == 1) return st;
   Scope sc_("dense_join", s);
-  if (N % 4 == 0) dense::k_join<4><<<grid_for(M * N, 1024), 256, 0, s>>>(M, N, h.splits, part, e);
+  if (h.splits > JOIN_WARPS && M * N <= (1 << 14) && e.ldy == N && !e.z && !e.bias && !e.residual && e.act == EMP_ACT_NONE)
+    // few outputs of many splits (a weight gradient): warps share an output's splits
+    k_col_join<<<(unsigned)((M * N + 31) / 32), 32 * JOIN_WARPS, 0, s>>>(h.splits, (int)(M * N), part, e.y, e.y_dtype);
+  else if (N % 4 == 0) dense::k_join<4><<<grid_for(M * N, 1024), 256, 0, s>>>(M, N, h.splits, part, e);
   else dense::k_join<1><<<grid_for(M * N, 256), 256, 0, s>>>(M, N, h.splits, part, e);
   return cudaGetLastError() == cudaSuccess ? EMP_OK : EMP_ERR_CUDA;
 }
@@ -219,13 +232,15 @@ int mp_rms_norm_grad(const emp_rms_norm_grad* a, void* ws, size_t ws_bytes, cuda
   if (st != EMP_OK) return st;
   norm::GradArgs p{a->rows, a->cols, a->degrees, a->eps, a->g, a->s, a->g_s, a->weight, a->g_x,
                    a->g_weight ? static_cast<float*>(ws) : nullptr, a->ldg, a->lds, a->ldgs, a->ldgx};
-  int blocks;
+  int blocks = 0;
+  cudaError_t e;
   {
     Scope sc_("rms_norm_grad", stream);
-    if (a->dtype == EMP_F32) blocks = norm::launch_grad<float>(p, stream);
-    else if (a->dtype == EMP_BF16) blocks = norm::launch_grad<__nv_bfloat16>(p, stream);
-    else blocks = norm::launch_grad<__half>(p, stream);
+    e = a->dtype == EMP_F32 ? norm::launch_grad<float>(p, &blocks, stream)
+      : a->dtype == EMP_BF16 ? norm::launch_grad<__nv_bfloat16>(p, &blocks, stream)
+                             : norm::launch_grad<__half>(p, &blocks, stream);
   }
+  if (e != cudaSuccess) return EMP_ERR_CUDA;
   if (a->g_weight) {
     Scope sc_("col_join", stream);
     k_col_join<<<(nout + 31) / 32, 32 * JOIN_WARPS, 0, stream>>>(blocks, nout, p.part, a->g_weight, a->dtype);
@@ -281,9 +296,9 @@ int mp_dense_grad(const emp_dense_grad* a, void* ws, size_t ws_bytes, cudaStream
   if (L.prep || a->g_bias) {
     const dense::GzArgs z{a->rows, a->fan_out, a->activation, a->g, a->z, a->ldg, a->ldz, L.ldgz,
                           L.prep ? at<char>(ws, L.gz) : nullptr, a->g_bias ? at<float>(ws, L.colsum) : nullptr};
-    if (a->dtype == EMP_F32) dense_gz<float>(z, L.gz_blocks, L.gz_vec, stream);
-    else if (a->dtype == EMP_BF16) dense_gz<__nv_bfloat16>(z, L.gz_blocks, L.gz_vec, stream);
-    else dense_gz<__half>(z, L.gz_blocks, L.gz_vec, stream);
+    if (a->dtype == EMP_F32) dense_gz<float>(z, L.gz_blocks, L.gz_v, stream);
+    else if (a->dtype == EMP_BF16) dense_gz<__nv_bfloat16>(z, L.gz_blocks, L.gz_v, stream);
+    else dense_gz<__half>(z, L.gz_blocks, L.gz_v, stream);
     if (a->g_bias) {
       Scope sc_("col_join", stream);
       k_col_join<<<(a->fan_out + 31) / 32, 32 * JOIN_WARPS, 0, stream>>>(L.gz_blocks, a->fan_out, z.part, a->g_bias, a->dtype);
