@@ -16,15 +16,22 @@ struct Epi {
   long long ldy, ldz;
 };
 
-__device__ __forceinline__ void put_one(const Epi& e, long long m, int n, float acc) {
-  float v = acc;
-  if (e.x_scale) v *= e.x_scale[m] * e.w_scale[n];
-  if (e.bias) v += load_any(e.bias, n, e.bias_dtype);
-  if (e.z) store_any(e.z, (size_t)m * e.ldz + n, e.y_dtype, v);
-  v = act_f(e.act, v);
-  if (e.residual) v += load_any(e.residual, (size_t)m * e.ldr + n, e.y_dtype);
-  store_any(e.y, (size_t)m * e.ldy + n, e.y_dtype, v);
+struct EpiIn {                 // what the epilogue of one output reads
+  float scale, bias, residual;
+};
+__device__ __forceinline__ EpiIn epi_in(const Epi& e, long long m, int n) {
+  EpiIn i;
+  i.scale = e.x_scale ? e.x_scale[m] * e.w_scale[n] : 1.f;
+  i.bias = e.bias ? load_any(e.bias, n, e.bias_dtype) : 0.f;
+  i.residual = e.residual ? load_any(e.residual, (size_t)m * e.ldr + n, e.y_dtype) : 0.f;
+  return i;
 }
+__device__ __forceinline__ void put_one(const Epi& e, long long m, int n, float acc, const EpiIn& in) {
+  float v = acc * in.scale + in.bias;
+  if (e.z) store_any(e.z, (size_t)m * e.ldz + n, e.y_dtype, v);
+  store_any(e.y, (size_t)m * e.ldy + n, e.y_dtype, act_f(e.act, v) + in.residual);
+}
+__device__ __forceinline__ void put_one(const Epi& e, long long m, int n, float acc) { put_one(e, m, n, acc, epi_in(e, m, n)); }
 
 // ------------------------------------------------------------------ few rows
 // Up to FEW_ROWS rows: the product reads W once and little else, so it runs on SIMT with a warp on
@@ -43,28 +50,36 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) k_dense_few(const Few p, const
   __shared__ __align__(16) float xs[FEW_M][K_PART];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n0 = (blockIdx.x * FEW_WARPS + warp) * FEW_COLS, m0 = blockIdx.y * FEW_M;
+  // lane c FEW_M + r finishes output (r, c); what its epilogue reads, and the first of W, is on its way before x is staged
+  const int m = m0 + lane % FEW_M, n = n0 + lane / FEW_M;
+  const bool mine = lane < FEW_COLS * FEW_M && m < p.M && n < p.N;
+  EpiIn in{};
+  if (mine) in = epi_in(e, m, n);
+  float w[FEW_COLS][V];
+  auto load_w = [&](int k) {
+#pragma unroll
+    for (int c = 0; c < FEW_COLS; ++c) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) w[c][j] = 0.f;
+      if (n0 + c < p.N && k < p.K) load_v<T, V>(static_cast<const T*>(p.w) + (n0 + c) * p.ldw + k, w[c]);
+    }
+  };
+  load_w(lane * V);
   float acc[FEW_COLS][FEW_M] = {};
   for (int k0 = 0; k0 < p.K; k0 += K_PART) {
-    const int kn = min(K_PART, p.K - k0);
+    const int kn = min(K_PART, p.K - k0), kq = kn / V;          // V divides K (or is 1)
     if (k0) __syncthreads();
-    for (int i = threadIdx.x * V; i < FEW_M * K_PART; i += 32 * FEW_WARPS * V) {
-      const int r = i / K_PART, k = i % K_PART;
+    for (int i = threadIdx.x; i < FEW_M * kq; i += 32 * FEW_WARPS) {
+      const int r = i / kq, k = (i - r * kq) * V;
       float v[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) v[j] = 0.f;
-      if (m0 + r < p.M && k < kn) load_v<T, V>(static_cast<const T*>(p.x) + (m0 + r) * p.ldx + k0 + k, v);
+      if (m0 + r < p.M) load_v<T, V>(static_cast<const T*>(p.x) + (m0 + r) * p.ldx + k0 + k, v);
 #pragma unroll
       for (int j = 0; j < V; ++j) xs[r][k + j] = v[j];
     }
     __syncthreads();
     for (int k = lane * V; k < kn; k += 32 * V) {
-      float w[FEW_COLS][V];
-#pragma unroll
-      for (int c = 0; c < FEW_COLS; ++c) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) w[c][j] = 0.f;
-        if (n0 + c < p.N) load_v<T, V>(static_cast<const T*>(p.w) + (n0 + c) * p.ldw + k0 + k, w[c]);
-      }
 #pragma unroll
       for (int r = 0; r < FEW_M; ++r)
 #pragma unroll
@@ -73,9 +88,10 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) k_dense_few(const Few p, const
 #pragma unroll
           for (int c = 0; c < FEW_COLS; ++c) acc[c][r] += w[c][j] * x;
         }
+      load_w(k0 + k + 32 * V < k0 + kn ? k0 + k + 32 * V : k0 + K_PART + lane * V);       // the next of this part, or of the next part
     }
   }
-  float mine = 0.f;                       // lane c FEW_M + r keeps output (r, c)
+  float sum = 0.f;
 #pragma unroll
   for (int c = 0; c < FEW_COLS; ++c)
 #pragma unroll
@@ -83,10 +99,9 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) k_dense_few(const Few p, const
       float a = acc[c][r];
 #pragma unroll
       for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-      if (lane == c * FEW_M + r) mine = a;
+      if (lane == c * FEW_M + r) sum = a;
     }
-  const int m = m0 + lane % FEW_M, n = n0 + lane / FEW_M;
-  if (lane < FEW_COLS * FEW_M && m < p.M && n < p.N) put_one(e, m, n, mine);
+  if (mine) put_one(e, m, n, sum, in);
 }
 
 // ------------------------------------------------------------------ operands TMA cannot read

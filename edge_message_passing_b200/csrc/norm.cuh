@@ -588,6 +588,9 @@ __global__ void __launch_bounds__(ST_THREADS, NA > 16 ? 2 : 3) k_rms_norm_grad_s
 // Persistent: block b takes row groups b, b + gridDim.x, ...; a thread's columns are the same in
 // every row, so its part of g_w stays in registers until the end.  The next row's loads are issued before
 // the current row's reduction, so that some are always in flight.
+// Two blocks of 256 threads per SM and two vectors a thread: 4096 x 2048 FP32 takes 28 us; three blocks spill (33 us),
+// one vector with four blocks 40 us.
+constexpr int GRAD_PER_SM = 2;
 template <typename T, int V>
 struct Raw {                     // V elements as they are in memory
   uint4 u;
@@ -595,8 +598,8 @@ struct Raw {                     // V elements as they are in memory
   __device__ __forceinline__ void get(float (&v)[V]) const { unpack16<T, V>(u, v); }
 };
 
-template <typename T, int V, int SL>
-__global__ void __launch_bounds__(MAX_THREADS) k_rms_norm_grad(const GradArgs p) {
+template <typename T, int V, int SL, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? GRAD_PER_SM : 1) k_rms_norm_grad(const GradArgs p) {
   extern __shared__ float acc_sm[];              // [cols] when the block has several rows or there are degrees
   __shared__ float red[2][2][32];
   const int G = blockDim.x, t = threadIdx.x, r = threadIdx.y, R = blockDim.y;
@@ -629,26 +632,27 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm_grad(const GradArgs p)
   for (long long b = blockIdx.x; b < groups; b += gridDim.x, par ^= 1) {
     const long long row = b * R + r;
     const bool live = row < p.rows;
-    float g[SL][V], s[SL][V];
-    Raw<T, V> th[SL];
+    Raw<T, V> gh[SL], sh[SL], th[SL];            // this row as it is in memory: unpacked for each use
     float ss = 0.f, hs = 0.f;
 #pragma unroll
     for (int k = 0; k < SL; ++k) {
-      g_[k].get(g[k]);
-      s_[k].get(s[k]);
+      gh[k] = g_[k];
+      sh[k] = s_[k];
       th[k] = t_[k];
     }
     fetch(row + (long long)gridDim.x * R);
 #pragma unroll
     for (int k = 0; k < SL; ++k) {
-      float wv[V];
+      float wv[V], g[V], s[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) wv[i] = 1.f;
       if (w) load_v<T, V>(w + at[k], wv);
+      gh[k].get(g);
+      sh[k].get(s);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        ss += s[k][i] * s[k][i];
-        hs += g[k][i] * wv[i] * s[k][i];
+        ss += s[i] * s[i];
+        hs += g[i] * wv[i] * s[i];
       }
     }
 #pragma unroll
@@ -671,15 +675,17 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm_grad(const GradArgs p)
     for (int k = 0; k < SL; ++k) {
       const int c = (k * G + t) * V;
       if (c >= p.cols) continue;
-      float wv[V], o[V];
+      float wv[V], o[V], g[V], s[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) { wv[i] = 1.f; o[i] = 0.f; }
       if (w) load_v<T, V>(w + at[k], wv);
       if (p.g_s) th[k].get(o);
+      gh[k].get(g);
+      sh[k].get(s);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        o[i] += rstd * (g[k][i] * wv[i] - s[k][i] * q);
-        acc[k][i] += g[k][i] * (s[k][i] * rstd);
+        o[i] += rstd * (g[i] * wv[i] - s[i] * q);
+        acc[k][i] += g[i] * (s[i] * rstd);
       }
       store_v<T, V>(static_cast<T*>(p.g_x) + row * p.ldgx + c, o);
     }
@@ -802,7 +808,8 @@ bool launch_odd(const Args& a, bool quant, cudaStream_t st) {
   const int row = a.cols * (int)sizeof(T) * (a.residual ? 2 : 1) + (quant ? a.cols : 0);
   const int per = ODD_THREADS / 32;                                // 8 rows, or 16 (which 8-bit rows need for 16 bytes)
   const int s16 = 2 * per * row + 64, s8 = per * row + 64;
-  if (s16 <= ODD_SMEM && (quant || a.rows > 2 * per * 148)) return quant ? launch_odd3<T, true, 2>(a, s16, st) : launch_odd3<T, false, 2>(a, s16, st);
+  // two rows a warp where that leaves four blocks on an SM
+  if (s16 <= (quant ? ODD_SMEM : 56 * 1024) && (quant || a.rows > 2 * per * 148)) return quant ? launch_odd3<T, true, 2>(a, s16, st) : launch_odd3<T, false, 2>(a, s16, st);
   if (!quant && s8 <= ODD_SMEM) return launch_odd3<T, false, 1>(a, s8, st);
   return false;
 }
@@ -824,8 +831,10 @@ cudaError_t launch_fwd(const Args& a, bool quant, cudaStream_t st) {
 }
 
 template <typename T, int V, int SL>
-void launch_grad2(const GradArgs& a, const Shape& h, cudaStream_t st) {
-  k_rms_norm_grad<T, V, SL><<<grad_blocks(a.rows, h.R), dim3(h.G, h.R), h.R > 1 || a.degrees ? a.cols * 4 : 0, st>>>(a);
+void launch_grad2(const GradArgs& a, const Shape& h, int blocks, cudaStream_t st) {
+  const int smem = h.R > 1 || a.degrees ? a.cols * 4 : 0;
+  if (h.G * h.R <= 256) k_rms_norm_grad<T, V, SL, 256><<<blocks, dim3(h.G, h.R), smem, st>>>(a);
+  else k_rms_norm_grad<T, V, SL, MAX_THREADS><<<blocks, dim3(h.G, h.R), smem, st>>>(a);
 }
 template <typename T, int NA>
 int launch_grad_odd3(const GradArgs& a, int smem, cudaStream_t st) {
@@ -863,9 +872,9 @@ cudaError_t launch_grad(const GradArgs& a, int* blocks, cudaStream_t st) {      
   }
   const Shape h = shape_for(a.cols, V, a.cols > MAX_THREADS * 2 * V ? 4 : 2, a.rows);
   *blocks = grad_blocks(a.rows, h.R);
-  if (h.SL == 1) launch_grad2<T, V, 1>(a, h, st);
-  else if (h.SL == 2) launch_grad2<T, V, 2>(a, h, st);
-  else if constexpr (V == 4) launch_grad2<T, V, 4>(a, h, st);      // 16-bit rows of the most columns take two
+  if (h.SL == 1) launch_grad2<T, V, 1>(a, h, *blocks, st);
+  else if (h.SL == 2) launch_grad2<T, V, 2>(a, h, *blocks, st);
+  else if constexpr (V == 4) launch_grad2<T, V, 4>(a, h, *blocks, st);      // 16-bit rows of the most columns take two
   return cudaGetLastError();
 }
 

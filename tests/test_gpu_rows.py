@@ -520,3 +520,65 @@ def test_refusals():
     need = emp.lib().mp_dense_grad_workspace_bytes(ctypes.byref(a))
     assert need > 0
     assert emp.lib().mp_dense_grad(ctypes.byref(a), x.data_ptr() // 256 * 256, need - 1, None) == -6
+
+
+# ------------------------------------------------------------------ alignments
+@pytest.mark.parametrize("type", list(TYPES))
+@pytest.mark.parametrize("rows,cols", [(1, 5), (3000, 31), (70, 77), (40, 515), (9, 1453), (4, 4097), (3, 8191), (700, 64)])
+@pytest.mark.parametrize("off,pad", [(0, 0), (1, 0), (0, 3), (3, 5)])
+def test_norm_of_any_alignment(rows, cols, off, pad, type):
+    """Rows `off` elements past a 16-byte boundary and `pad` elements apart; the residual aligned otherwise."""
+    t, rng = TYPES[type], np.random.default_rng(rows + cols + off)
+
+    def view(a, off, pad):
+        full = torch.zeros(rows * (cols + pad) + off, dtype=t, device="cuda")
+        v = torch.as_strided(full, (rows, cols), (cols + pad, 1), off)
+        v.copy_(dev(a, t))
+        return v
+
+    x, r, g = (view(normal(rng, rows, cols), o, p) for o, p in ((off, pad), (pad, off), (off, 0)))
+    w = dev(1 + 0.3 * normal(rng, cols), t)
+    y, s = emp.mp_rms_norm(x, w, residual=r, eps=EPS)
+    ry, rs = orow.rms_norm(host(x), host(w), host(r), EPS)
+    near(y, ry, (half_step(t) + 32 * U) * np.abs(ry) + floor_of(t), "y")
+    near(s, rs, (half_step(t) + U) * np.abs(rs) + floor_of(t), "s")
+    q, scale, s2 = emp.mp_rms_norm(x, w, residual=r, eps=EPS, quantize=True)
+    assert torch.equal(s, s2)
+    rscale = orow.scale_of(ry)
+    near(scale, rscale, 40 * U * rscale, "scale")
+    value = host(q) * host(scale)[:, None]
+    assert np.all(np.abs(value - ry) <= np.maximum(2.0 ** -4 * np.abs(ry), 2.0 ** -10 * rscale[:, None]) + 64 * U * np.abs(ry))
+    S, G, W = host(x), host(g), host(w)
+    g_x, g_w = emp.mp_rms_norm_grad(g, x, w, g_s=r, eps=EPS)
+    rx, rw = orow.rms_norm_grad(G, S, W, host(r), EPS)
+    rstd = 1 / np.sqrt((S * S).mean(1, keepdims=True) + EPS)
+    n, h = S * rstd, G * W
+    size = rstd * (np.abs(h) + np.abs(n) * np.abs(h * n).mean(1, keepdims=True)) + np.abs(host(r))
+    near(g_x, rx, half_step(t) * np.abs(rx) + 64 * U * size + floor_of(t), "g_x")
+    near(g_w, rw, half_step(t) * np.abs(rw) + (rows / 592 + 400) * U * np.abs(G * n).sum(0) + floor_of(t), "g_w")
+
+
+@pytest.mark.parametrize("type", list(TYPES))
+@pytest.mark.parametrize("rows", [3, 150])
+@pytest.mark.parametrize("off,pad", [(1, 0), (0, 3), (2, 2)])
+def test_dense_of_any_alignment(rows, off, pad, type):
+    """x, W, the residual and g off 16-byte boundaries, outputs of rows that are off them too."""
+    t, rng = TYPES[type], np.random.default_rng(rows + off)
+    K, N = 70, 45
+
+    def view(a):
+        full = torch.zeros(a.shape[0] * (a.shape[1] + pad) + off, dtype=t, device="cuda")
+        v = torch.as_strided(full, a.shape, (a.shape[1] + pad, 1), off)
+        v.copy_(dev(a, t))
+        return v
+
+    x, w, r, g, z0 = (view(a) for a in (normal(rng, rows, K), normal(rng, N, K) / 8, normal(rng, rows, N), normal(rng, rows, N),
+                                        normal(rng, rows, N)))
+    y, z = emp.mp_dense(x, w, activation="gelu", residual=r, keep_z=True)
+    ry, rz, ty, tz = dense_tol(host(x), host(w), None, host(r), "gelu", t, K)
+    near(z, rz, tz, "z")
+    near(y, ry, ty, "y")
+    got = emp.mp_dense_grad(g, x, w, z=z0, activation="silu")
+    ref = emp.mp_dense_grad(*(a.contiguous().clone() for a in (g, x, w)), z=z0.contiguous().clone(), activation="silu")
+    for a, b in zip(got, ref):
+        assert (a.double() - b.double()).abs().max() <= (4 * half_step(t) + 1e-5) * b.double().abs().max()
