@@ -510,8 +510,10 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
         __syncwarp();
         return;
       }
-      if (lane == 0) stores_read<PLACES - 1>();              // this chunk's place is free
-      __syncwarp();
+      // the place's last store has to have read it before it is written: before a residual comes (here or in the
+      // prefetch below), else only before the finished rows go in
+      const bool res_now = e.residual && !e.z;
+      if (res_now && !asked && lane == 0) stores_read<PLACES - 1>();
       if (!asked) ask(t, c);
       const int pl = done % PLACES;
       unsigned char* pp = place + pl * PLACE_BYTES;
@@ -529,6 +531,8 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
         }
       }
       if (e.z) {                                             // z takes the place first, the residual after it
+        if (lane == 0) stores_read<PLACES - 1>();
+        __syncwarp();
         stage(pp, v);
         if (lane == 0) {
           tma_store(&maps.z, pp, n0, (int)m0);
@@ -554,6 +558,10 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < V; ++i) v[j * V + i] += a[i];
         }
+      }
+      if (!res_now && !e.z) {
+        if (lane == 0) stores_read<PLACES - 1>();
+        __syncwarp();
       }
       stage(pp, v);
       if (lane == 0) tma_store(&maps.y, pp, n0, (int)m0);
