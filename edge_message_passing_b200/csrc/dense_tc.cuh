@@ -38,11 +38,12 @@ constexpr int BM = 128;
 constexpr int SPLIT_GROUPS = 2, SPLIT_WARPS = 4 * SPLIT_GROUPS;
 constexpr int A_BYTES = BM * 128;                       // one stage of A
 constexpr int MAX_STAGES = 8, MAX_EPI = 16;
-constexpr int LAND_BYTES = 2 * A_BYTES, HL_BYTES = 2 * A_BYTES;
+constexpr int HL_BYTES = 2 * A_BYTES;                   // hi and lo of a stage of B
 constexpr int CHUNK_STAGES = 3;                         // FP32: K_CHUNK = 96
 constexpr int A_COL = 256;                              // FP32: TMEM columns of A's slots (64 each: hi, lo)
 
-// The kernel's forms: 16- and 8-bit operands; FP32; FP32 with k of one chunk at most (no sums to keep in registers).
+// The kernel's forms: 16- and 8-bit operands; FP32; FP32 with k of one chunk at most.  SHORT keeps no sums in
+// registers, and each of its CTAs stays on one column of tiles, whose B is split once and kept.
 enum Path { DIRECT, SPLIT, SHORT };
 
 // T: the type of y, z and residual; ROWS: their rows by TMA; SCALED: 8-bit operands with scales.
@@ -52,14 +53,15 @@ template <Path PATH, typename T, bool ROWS, bool SCALED>
 struct Cfg {
   static constexpr bool FP32 = PATH != DIRECT;
   static constexpr int EPI = PATH == SHORT || (PATH == DIRECT && sizeof(T) == 2 && ROWS && !SCALED) ? 16 : 8;
-  static constexpr int LAND = PATH == SHORT ? 2 : 3;    // FP32: stages as they land ...
-  static constexpr int SLOTS = LAND;                    // ... and split (A in TMEM, B's hi and lo in shared memory)
-  static constexpr int RING_BYTES = FP32 ? LAND * LAND_BYTES + SLOTS * HL_BYTES : 4 * (A_BYTES + 256 * 128);
+  static constexpr int LAND = 3, SLOTS = 3;             // FP32: stages as they land (A and B; A alone in SHORT) and split
+  static constexpr int LAND_BYTES = PATH == SHORT ? A_BYTES : 2 * A_BYTES;
+  // A's split is in TMEM, B's hi and lo in shared memory: a place per slot, or per stage of the whole k in SHORT
+  static constexpr int RING_BYTES = FP32 ? LAND * LAND_BYTES + (PATH == SHORT ? CHUNK_STAGES : SLOTS) * HL_BYTES : 4 * (A_BYTES + 256 * 128);
   static constexpr int PLACE_BYTES = ROWS ? 32 * 32 * (int)sizeof(T) : 4096;
   static constexpr int PLACES = EPI == 8 && PLACE_BYTES == 2048 ? 2 : 1;      // of a warp
   static constexpr int STAGING = EPI * PLACES * PLACE_BYTES;
   static constexpr int BIAS = EPI * 32 * (SCALED ? 4 : (int)sizeof(T));
-  static constexpr int BARS = 512;
+  static constexpr int BARS = 640;
   static constexpr int SMEM = 1024 + RING_BYTES + STAGING + BIAS + BARS;
   static constexpr int THREADS = 32 * (2 + EPI + (FP32 ? SPLIT_WARPS : 0));
   static_assert(SMEM <= 232448, "shared memory of a CTA");
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
     k_dense_tc(const Plan p, const dense::Epi e, const __grid_constant__ Maps maps) {
   using C = Cfg<PATH, T, ROWS, SCALED>;
   constexpr bool FP32 = C::FP32;
-  constexpr int EPI_WARPS = C::EPI, PER_QUARTER = EPI_WARPS / 4, LAND = C::LAND, SLOTS = C::SLOTS;
+  constexpr int EPI_WARPS = C::EPI, PER_QUARTER = EPI_WARPS / 4, LAND = C::LAND, SLOTS = C::SLOTS, LAND_BYTES = C::LAND_BYTES;
   extern __shared__ __align__(1024) unsigned char dtc_raw[];
   unsigned char* sm = dtc_raw + (1024 - (tc::smem_u32(dtc_raw) & 1023)) % 1024;
   unsigned char* hl = sm + LAND * LAND_BYTES;                           // FP32: B's hi and lo
@@ -298,7 +300,9 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
   uint64_t* acc_full = sempty + SLOTS;                                  // [2]
   uint64_t* acc_empty = acc_full + 2;                                   // [2]
   uint64_t* res_full = acc_empty + 2;                                   // [MAX_EPI][2] residual chunks landed
-  uint64_t* drain = res_full + 2 * MAX_EPI;
+  uint64_t* b_full = res_full + 2 * MAX_EPI;                             // [CHUNK_STAGES] SHORT: B landed ...
+  uint64_t* b_split = b_full + CHUNK_STAGES;                            // [CHUNK_STAGES] ... and split
+  uint64_t* drain = b_split + CHUNK_STAGES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int stages = FP32 ? LAND : p.stages;
@@ -313,6 +317,10 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
     for (int s = 0; s < SLOTS; ++s) {
       tc::mbar_init(&sfull[s], 4);
       tc::mbar_init(&sempty[s], 1);
+    }
+    for (int k = 0; k < CHUNK_STAGES; ++k) {
+      tc::mbar_init(&b_full[k], 1);
+      tc::mbar_init(&b_split[k], 4);
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&acc_full[b], 1);
@@ -336,8 +344,15 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
     uint32_t it = 0;
     bool ok = true;
     const int kw = FP32 ? 32 : SCALED ? 128 : 64;                       // k of a stage
-    const uint32_t bytes = A_BYTES + p.bn * 128;
+    const uint32_t bytes = A_BYTES + (PATH == SHORT ? 0 : p.bn * 128);
     Item t = first_item(p);
+    if (PATH == SHORT && elect_one()) {
+      for (int k = 0; k < p.nk; ++k) {                                   // B of this CTA's column of tiles
+        tc::mbar_expect_tx(&b_full[k], p.bn * 128);
+        tc::tma_load(hl + k * HL_BYTES, &maps.b, &b_full[k], p.b_mn ? t.n0 : k * kw, p.b_mn ? k * kw : t.n0);
+      }
+    }
+    __syncwarp();
     for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x, t = t.next(p)) {
       int k0 = t.k_first * kw;
       const int m0 = (int)t.m0, n0 = t.n0;
@@ -355,7 +370,8 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
             tc::tma_load(a, &maps.a, bar, m0, k0);
             if (!FP32) tc::tma_load(a + 8192, &maps.a, bar, m0 + 64, k0);
           }
-          if (!p.b_mn) {
+          if (PATH == SHORT) {
+          } else if (!p.b_mn) {
             tc::tma_load(b, &maps.b, bar, k0, n0);
           } else if (FP32) {
             tc::tma_load(b, &maps.b, bar, n0, k0);
@@ -366,6 +382,8 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
         __syncwarp();
       }
     }
+    if (PATH == SHORT)
+      for (int k = 0; k < p.nk; ++k) wait(&b_full[k], 0);
     // copies in flight can only be among the last `stages`
     for (uint32_t j = it > (uint32_t)stages ? it - stages : 0; j < it; ++j) wait(&full[j % stages], (j / stages) & 1);
   } else if (warp == 1) {
@@ -393,9 +411,10 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
         }
         const int s = ring.at;
         if (!__all_sync(0xffffffffu, wait(&in[s], ring.phase))) { ok = false; break; }
+        if (PATH == SHORT && w == blockIdx.x && !__all_sync(0xffffffffu, wait(&b_split[k], 0))) { ok = false; break; }
         tc::fence_after();
         if (elect_one()) {
-          const uint32_t b = b0 + s * step16;
+          const uint32_t b = b0 + (PATH == SHORT ? k : s) * step16;
           if (FP32) {
             const uint32_t hi = a0 + s * 64, lo = hi + 32, bl = b + (A_BYTES >> 4);
 #pragma unroll
@@ -641,12 +660,39 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
     uint32_t it = 0;
     bool ok = true;
     Item t = first_item(p);
+    // x (32 k of B's row r) as hi and lo, k-major, 128-byte swizzle
+    auto split_b = [&](unsigned char* bhi, const float (&x)[32]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float4 hi, lo;
+        hi.x = tf32_rna(x[4 * j]);     lo.x = tf32_rna(x[4 * j] - hi.x);
+        hi.y = tf32_rna(x[4 * j + 1]); lo.y = tf32_rna(x[4 * j + 1] - hi.y);
+        hi.z = tf32_rna(x[4 * j + 2]); lo.z = tf32_rna(x[4 * j + 2] - hi.z);
+        hi.w = tf32_rna(x[4 * j + 3]); lo.w = tf32_rna(x[4 * j + 3] - hi.w);
+        const int o = r * 128 + ((j ^ (r & 7)) << 4);
+        *reinterpret_cast<float4*>(bhi + o) = hi;
+        *reinterpret_cast<float4*>(bhi + A_BYTES + o) = lo;
+      }
+    };
+    if constexpr (PATH == SHORT) {
+      for (int k = g; k < p.nk; k += SPLIT_GROUPS) {        // B, in place: the whole stage is read before hi is written over it
+        const bool landed = __all_sync(0xffffffffu, wait(&b_full[k], 0));
+        unsigned char* bhi = hl + k * HL_BYTES;
+        float x[32];
+        if (r < p.bn) read_row(bhi, r, p.b_mn, p.bn, x);
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");       // reached by all four warps, landed or not
+        if (!landed) { ok = false; break; }
+        if (r < p.bn) split_b(bhi, x);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&b_split[k]);
+      }
+    }
     for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x, t = t.next(p)) {
       for (int k = 0; k < t.k_n; ++k, ++it) {
         if (it % SPLIT_GROUPS != g) continue;
         const int s = (int)(it % LAND), slot = (int)(it % SLOTS);
         const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + A_COL + slot * 64;
-        unsigned char* bhi = hl + slot * HL_BYTES;
         // first the slot (stage it - SLOTS multiplied, hence every stage before it landed), then the landing:
         // the stage before in the same place, it - LAND, has landed, so its phase's parity is unambiguous
         if (it >= SLOTS && !__all_sync(0xffffffffu, wait(&sempty[slot], (uint32_t)(((it / SLOTS) - 1) & 1)))) { ok = false; break; }
@@ -665,23 +711,13 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
           for (int i = 0; i < 16; ++i) h[i] = tf32_rna(v[j + i] - h[i]);
           tmem_st16(ta + 32 + j, h);
         }
-        if (r < p.bn) {
+        if (PATH == SPLIT && r < p.bn) {
           float x[32];
           read_row(land + A_BYTES, r, p.b_mn, p.bn, x);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float4 hi, lo;
-            hi.x = tf32_rna(x[4 * j]);     lo.x = tf32_rna(x[4 * j] - hi.x);
-            hi.y = tf32_rna(x[4 * j + 1]); lo.y = tf32_rna(x[4 * j + 1] - hi.y);
-            hi.z = tf32_rna(x[4 * j + 2]); lo.z = tf32_rna(x[4 * j + 2] - hi.z);
-            hi.w = tf32_rna(x[4 * j + 3]); lo.w = tf32_rna(x[4 * j + 3] - hi.w);
-            const int o = r * 128 + ((j ^ (r & 7)) << 4);
-            *reinterpret_cast<float4*>(bhi + o) = hi;
-            *reinterpret_cast<float4*>(bhi + A_BYTES + o) = lo;
-          }
+          split_b(hl + slot * HL_BYTES, x);
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (PATH == SPLIT) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc::fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -825,12 +861,15 @@ inline int launch(long long M, int N, long long K, int t, const Operand& a, cons
     };
     if (!map(&maps.y, e.y, e.ldy) || !map(&maps.z, e.z, e.ldz) || !map(&maps.res, e.residual, e.ldr)) return EMP_ERR_CUDA;
   }
-  const unsigned grid = (unsigned)std::min<long long>(p.items, tc::num_sms());
+  // SHORT: a whole number of CTAs per column of tiles, so that a CTA's column does not change
+  const bool one_chunk = split && h.splits == 1 && h.nk <= CHUNK_STAGES && h.ntiles <= tc::num_sms();
+  const int sms = tc::num_sms();
+  const unsigned grid = (unsigned)std::min<long long>(p.items, one_chunk ? sms / h.ntiles * h.ntiles : sms);
   p.step_n = (int)(grid % p.ntiles);
   p.step_m = (int)(grid / p.ntiles % p.mtiles);
   p.step_s = (int)(grid / p.ntiles / p.mtiles);
   Launch l{p, e, maps, grid, st};
-  if (split) return h.per <= CHUNK_STAGES ? l.rows<SHORT, float, false>(rows) : l.rows<SPLIT, float, false>(rows);
+  if (split) return one_chunk ? l.rows<SHORT, float, false>(rows) : l.rows<SPLIT, float, false>(rows);
   const bool sc = t == EMP_E4M3;
   switch (e.y_dtype) {
     case EMP_F32: return l.rows<DIRECT, float, true>(rows);                         // of 8-bit inputs only
