@@ -620,6 +620,7 @@ def mp_radial_chain(chain: Chain, x, g_kc=None, g_y0=None, out=None):
 # ------------------------------------------------------------------ row-wise operators
 # These calls are short (a few microseconds on the device for a few hundred rows), so the host's part is
 # kept short too: torch is looked up once, and contiguous tensors take no reshape.
+EMP_ERR_WORKSPACE = -6
 _ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
 _T = None                  # torch
 _CODES: Dict[object, int] = {}
@@ -675,11 +676,15 @@ def _launch(fn, args, dev: int, workspace=None):
         with torch.cuda.device(dev):
             return _launch(fn, args, dev, workspace)
     stream = torch.cuda.current_stream(dev).cuda_stream
+    ref = ctypes.byref(args)
     if workspace is None:
-        return fn(ctypes.byref(args), stream)
-    nbytes = workspace(ctypes.byref(args))
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}") if nbytes else None
-    return fn(ctypes.byref(args), _ptr(ws), nbytes, stream)
+        return fn(ref, stream)
+    st = fn(ref, None, 0, stream)              # many shapes need no workspace
+    if st != EMP_ERR_WORKSPACE:
+        return st
+    nbytes = workspace(ref)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+    return fn(ref, ws.data_ptr(), nbytes, stream)
 
 
 def _norm_rows(x, weight, code: int, dev: int, what: str):

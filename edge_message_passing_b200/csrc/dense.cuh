@@ -108,24 +108,48 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) k_dense_few(const Few p, const
 // Rows whose start or pitch is not a multiple of 16 bytes are copied once to rows that are.  A thread
 // writes 16 bytes, put together by funnel shifts from the (up to five) aligned words that hold them; words
 // past the row's last byte are not read.  x: 16-byte chunks of a row, y: rows.
-__global__ void __launch_bounds__(256) k_pack(long long rows, int row_bytes, const unsigned char* __restrict__ src, long long pitch,
-                                              unsigned char* __restrict__ dst, long long pitch_d) {
-  const int chunk = blockIdx.x * 32 + threadIdx.x;
-  if (chunk * 16 >= row_bytes) return;
-  for (long long r = (long long)blockIdx.y * 8 + threadIdx.y; r < rows; r += (long long)gridDim.y * 8) {
-    const unsigned char* s = src + r * pitch + chunk * 16;
-    const unsigned char* end = src + r * pitch + row_bytes;
-    const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(s) & 3);
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(s - off);
-    uint32_t v[5];
+struct Pack {                  // up to two matrices (blockIdx.z)
+  int n = 0;
+  long long rows[2], pitch[2], pitch_d[2];
+  int row_bytes[2];
+  const unsigned char* src[2];
+  unsigned char* dst[2];
+};
+constexpr int PACK_ROWS = 4;   // rows of a thread whose loads are in flight together
+__global__ void __launch_bounds__(256) k_pack(const Pack p) {
+  // (chosen by value: an index into the parameters would put them into local memory)
+  const bool second = blockIdx.z != 0;
+  const long long rows = second ? p.rows[1] : p.rows[0], pitch = second ? p.pitch[1] : p.pitch[0];
+  const long long pitch_d = second ? p.pitch_d[1] : p.pitch_d[0];
+  const int row_bytes = second ? p.row_bytes[1] : p.row_bytes[0], at = (blockIdx.x * blockDim.x + threadIdx.x) * 16;
+  const unsigned char* __restrict__ src = second ? p.src[1] : p.src[0];
+  unsigned char* __restrict__ dst = second ? p.dst[1] : p.dst[0];
+  if (at >= row_bytes) return;
+  const long long step = (long long)gridDim.y * blockDim.y;
+  for (long long r0 = (long long)blockIdx.y * blockDim.y + threadIdx.y; r0 < rows; r0 += PACK_ROWS * step) {
+    uint32_t v[PACK_ROWS][5];
+    unsigned off[PACK_ROWS];
 #pragma unroll
-    for (int i = 0; i < 5; ++i) v[i] = reinterpret_cast<const unsigned char*>(w + i) < end ? w[i] : 0u;
-    uint4 o;
-    o.x = __funnelshift_r(v[0], v[1], off * 8);
-    o.y = __funnelshift_r(v[1], v[2], off * 8);
-    o.z = __funnelshift_r(v[2], v[3], off * 8);
-    o.w = __funnelshift_r(v[3], v[4], off * 8);
-    *reinterpret_cast<uint4*>(dst + r * pitch_d + chunk * 16) = o;
+    for (int k = 0; k < PACK_ROWS; ++k) {
+      const long long r = r0 + k * step;
+      const unsigned char* s = src + r * pitch + at;
+      const unsigned char* end = src + r * pitch + row_bytes;
+      off[k] = (unsigned)(reinterpret_cast<uintptr_t>(s) & 3);
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(s - off[k]);
+#pragma unroll
+      for (int i = 0; i < 5; ++i) v[k][i] = r < rows && reinterpret_cast<const unsigned char*>(w + i) < end ? w[i] : 0u;
+    }
+#pragma unroll
+    for (int k = 0; k < PACK_ROWS; ++k) {
+      const long long r = r0 + k * step;
+      if (r >= rows) break;
+      uint4 o;
+      o.x = __funnelshift_r(v[k][0], v[k][1], off[k] * 8);
+      o.y = __funnelshift_r(v[k][1], v[k][2], off[k] * 8);
+      o.z = __funnelshift_r(v[k][2], v[k][3], off[k] * 8);
+      o.w = __funnelshift_r(v[k][3], v[k][4], off[k] * 8);
+      *reinterpret_cast<uint4*>(dst + r * pitch_d + at) = o;
+    }
   }
 }
 

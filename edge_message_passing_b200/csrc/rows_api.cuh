@@ -43,15 +43,31 @@ Packed packed(const void* p, long long ld, long long rows, int cols, int t, Take
   k.off = take((size_t)rows * k.ld * es);
   return k;
 }
-const void* pack(const Packed& k, const void* p, long long ld, long long rows, int cols, int t, void* ws, cudaStream_t s) {
+// where an operand is read, and its copy noted in `all` if it takes one
+const void* pack(dense::Pack& all, const Packed& k, const void* p, long long ld, long long rows, int cols, int t, void* ws) {
   if (!k.copy) return p;
-  void* d = at<char>(ws, k.off);
+  const int es = dtype_size(t), q = all.n++;
+  all.rows[q] = rows;
+  all.row_bytes[q] = cols * es;
+  all.src[q] = static_cast<const unsigned char*>(p);
+  all.pitch[q] = ld * es;
+  all.dst[q] = at<unsigned char>(ws, k.off);
+  all.pitch_d[q] = k.ld * es;
+  return all.dst[q];
+}
+void pack_all(const dense::Pack& all, cudaStream_t s) {
+  if (!all.n) return;
+  long long rows = all.rows[0];
+  int bytes = all.row_bytes[0];
+  for (int q = 1; q < all.n; ++q) {
+    rows = std::max(rows, all.rows[q]);
+    bytes = std::max(bytes, all.row_bytes[q]);
+  }
+  const int chunks = (bytes + 15) / 16, bx = std::min(256, chunks), by = 256 / bx;
+  const long long blocks = (rows + by * dense::PACK_ROWS - 1) / (by * dense::PACK_ROWS);
+  const dim3 grid((chunks + bx - 1) / bx, (unsigned)std::min<long long>(blocks, 32 * tc::num_sms()), all.n);
   Scope sc_("dense_pack", s);
-  const int es = dtype_size(t);
-  const dim3 grid((cols * es + 511) / 512, (unsigned)std::min<long long>((rows + 7) / 8, 4736));
-  dense::k_pack<<<grid, dim3(32, 8), 0, s>>>(rows, cols * es, static_cast<const unsigned char*>(p), ld * es,
-                                             static_cast<unsigned char*>(d), k.ld * es);
-  return d;
+  dense::k_pack<<<grid, dim3(bx, by), 0, s>>>(all);
 }
 
 struct DenseLayout {
@@ -226,8 +242,8 @@ int mp_rms_norm_grad(const emp_rms_norm_grad* a, void* ws, size_t ws_bytes, cuda
       !rows_ok_or_null(a->g_s, a->ldgs, a->cols, a->rows, a->dtype) || !rows_ok(a->g_x, a->ldgx, a->cols, a->rows, a->dtype))
     return EMP_ERR_ARG;
   const size_t need = norm_grad_bytes(*a);
-  if (need && (!ws || reinterpret_cast<uintptr_t>(ws) % 16)) return EMP_ERR_ARG;
   if (ws_bytes < need) return EMP_ERR_WORKSPACE;
+  if (need && (!ws || reinterpret_cast<uintptr_t>(ws) % 256)) return EMP_ERR_ARG;
   int st = check_device();
   if (st != EMP_OK) return st;
   norm::GradArgs p{a->rows, a->cols, a->degrees, a->eps, a->g, a->s, a->g_s, a->weight, a->g_x,
@@ -257,8 +273,8 @@ int mp_dense(const emp_dense* a, void* ws, size_t ws_bytes, cudaStream_t stream)
   if (!a || !dense_args_ok(*a)) return EMP_ERR_ARG;
   if (a->rows == 0) return EMP_OK;
   const DenseLayout L = dense_layout(*a);
-  if (L.total && (!ws || reinterpret_cast<uintptr_t>(ws) % 256)) return EMP_ERR_ARG;
   if (ws_bytes < L.total) return EMP_ERR_WORKSPACE;
+  if (L.total && (!ws || reinterpret_cast<uintptr_t>(ws) % 256)) return EMP_ERR_ARG;
   int st = check_device();
   if (st != EMP_OK) return st;
   const int bt = a->dtype == EMP_E4M3 ? EMP_F32 : a->dtype;
@@ -270,8 +286,10 @@ int mp_dense(const emp_dense* a, void* ws, size_t ws_bytes, cudaStream_t stream)
     else dense_few<__nv_fp8_e4m3>(*a, e, stream);
     return cudaGetLastError() == cudaSuccess ? EMP_OK : EMP_ERR_CUDA;
   }
-  const dtc::Operand x{pack(L.x, a->x, a->ldx, a->rows, a->fan_in, a->dtype, ws, stream), L.x.ld, 0};
-  const dtc::Operand w{pack(L.w, a->weight, a->ldw, a->fan_out, a->fan_in, a->dtype, ws, stream), L.w.ld, 0};
+  dense::Pack copies;
+  const dtc::Operand x{pack(copies, L.x, a->x, a->ldx, a->rows, a->fan_in, a->dtype, ws), L.x.ld, 0};
+  const dtc::Operand w{pack(copies, L.w, a->weight, a->ldw, a->fan_out, a->fan_in, a->dtype, ws), L.w.ld, 0};
+  pack_all(copies, stream);
   return dense_product(a->rows, a->fan_out, a->fan_in, a->dtype, x, w, e, L.h, at<float>(ws, L.part), stream);
 }
 
@@ -289,8 +307,8 @@ int mp_dense_grad(const emp_dense_grad* a, void* ws, size_t ws_bytes, cudaStream
     return EMP_OK;
   }
   const DenseGradLayout L = dense_grad_layout(*a);
-  if (L.total && (!ws || reinterpret_cast<uintptr_t>(ws) % 256)) return EMP_ERR_ARG;
   if (ws_bytes < L.total) return EMP_ERR_WORKSPACE;
+  if (L.total && (!ws || reinterpret_cast<uintptr_t>(ws) % 256)) return EMP_ERR_ARG;
   int st = check_device();
   if (st != EMP_OK) return st;
   if (L.prep || a->g_bias) {
@@ -305,15 +323,17 @@ int mp_dense_grad(const emp_dense_grad* a, void* ws, size_t ws_bytes, cudaStream
     }
   }
   const void* gz = L.prep ? at<char>(ws, L.gz) : static_cast<const char*>(a->g);
+  dense::Pack copies;
+  const dtc::Operand w{a->g_x ? pack(copies, L.w, a->weight, a->ldw, a->fan_out, a->fan_in, a->dtype, ws) : nullptr, L.w.ld, 1};
+  const dtc::Operand x{a->g_weight ? pack(copies, L.x, a->x, a->ldx, a->rows, a->fan_in, a->dtype, ws) : nullptr, L.x.ld, 1};
+  pack_all(copies, stream);
   if (a->g_x) {
     const dense::Epi e{EMP_ACT_NONE, a->dtype, 0, nullptr, nullptr, nullptr, nullptr, 0, a->g_x, nullptr, a->ldgx, 0};
-    const dtc::Operand w{pack(L.w, a->weight, a->ldw, a->fan_out, a->fan_in, a->dtype, ws, stream), L.w.ld, 1};
     st = dense_product(a->rows, a->fan_in, a->fan_out, a->dtype, {gz, L.ldgz, 0}, w, e, L.hx, at<float>(ws, L.part_x), stream);
     if (st != EMP_OK) return st;
   }
   if (a->g_weight) {
     const dense::Epi e{EMP_ACT_NONE, a->dtype, 0, nullptr, nullptr, nullptr, nullptr, 0, a->g_weight, nullptr, a->fan_in, 0};
-    const dtc::Operand x{pack(L.x, a->x, a->ldx, a->rows, a->fan_in, a->dtype, ws, stream), L.x.ld, 1};
     st = dense_product(a->fan_out, a->fan_in, a->rows, a->dtype, {gz, L.ldgz, 1}, x, e, L.hw, at<float>(ws, L.part_w), stream);
   }
   return st != EMP_OK ? st : cudaGetLastError() == cudaSuccess ? EMP_OK : EMP_ERR_CUDA;

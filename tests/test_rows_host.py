@@ -43,7 +43,7 @@ def test_norm(kw):
 
 
 @pytest.mark.parametrize("kw", [dict(rows=-1), dict(cols=0), dict(dtype=3), dict(eps=0.0), dict(g=None), dict(s=None),
-                                dict(g_x=None), dict(ldg=1), dict(g_s=P, ldgs=1), dict(weight=P + 2), dict(g_weight=P)])
+                                dict(g_x=None), dict(ldg=1), dict(g_s=P, ldgs=1), dict(weight=P + 2)])
 def test_norm_gradient(kw):
     assert norm_grad(**kw) == ARG
 
@@ -68,6 +68,19 @@ def test_dense(kw):
                                 dict(ldgx=63), dict(g_weight=P, x=None), dict(g_weight=P + 1), dict(g_bias=P + 3)])
 def test_dense_gradient(kw):
     assert dense_grad(**kw) == ARG
+
+
+def test_workspace():
+    """Too small a workspace is refused before its pointer is looked at; then a null or misaligned one."""
+    assert norm_grad(g_weight=P) == -6
+    a = emp.DenseGradC(rows=4, fan_in=64, fan_out=32, dtype=0, g=P, ldg=32, x=P, ldx=64, weight=P, ldw=64, g_x=P, ldgx=64,
+                       g_bias=P)
+    L = emp.lib()
+    need = L.mp_dense_grad_workspace_bytes(ctypes.byref(a))
+    assert need > 0
+    assert L.mp_dense_grad(ctypes.byref(a), P, need - 1, None) == -6
+    assert L.mp_dense_grad(ctypes.byref(a), None, need, None) == ARG
+    assert L.mp_dense_grad(ctypes.byref(a), P + 16, need, None) == ARG
 
 
 def test_zero_rows_and_null():
