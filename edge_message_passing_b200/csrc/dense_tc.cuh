@@ -5,7 +5,7 @@
 // with A and B each stored with k contiguous ("k-major": x, W, and g in g_x = gz W) or with the other
 // index contiguous ("mn-major": W in g_x, both operands of g_W = gz^T x), and the dense layer's epilogue.
 //
-// Persistent kernel, one CTA per SM, 128 x bn tiles (bn = 64, 128 or 256) taken round-robin with n
+// Persistent kernel, one CTA per SM, 128 x bn tiles (bn a multiple of 32, up to 256 or in FP32 128) taken round-robin with n
 // fastest, so that neighbouring CTAs share an A tile in L2.  A long k axis with few tiles is split:
 // each split leaves a partial product, and k_join adds them in order.  Warps: one issues TMA loads, one
 // the MMAs, eight drain the accumulators (two per TMEM lane quarter, every other 32 columns each) and
@@ -761,23 +761,23 @@ inline bool tma_ok(const void* p, long long ld, int t) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * dtype_size(t) % 16 == 0;
 }
 
-// Tile width and splits of the k axis of an M x N product with K summed: those of the least estimated time.  A CTA's
+// Tile width and splits of the k axis of an M x N product with K summed: those of the least estimated time (a width
+// that divides N well against one that uses each operand byte more often).  A CTA's
 // tile takes the longer of its k stages and its epilogue (which runs beside the next tile's stages), the CTAs work in
 // waves, and splits pay for their partial products.  Microseconds as measured for the 16-bit and the FP32 kernel: a
 // stage with the operands in L2, the epilogue of a tile with one stage.
 struct Shape {
   int bn, splits, per, nk, mtiles, ntiles;
 };
-inline Shape shape_for(long long M, int N, long long K, int t) {
+inline Shape shape_for(long long M, int N, long long K, int t, int b_mn) {
   const int kw = 128 / dtype_size(t), sms = tc::num_sms();
   const bool fp32 = t == EMP_F32;
   Shape best{};
   double best_us = 0;
-  for (int bn = 64; bn <= (fp32 ? 128 : 256); bn *= 2) {
-    if (bn > 64 && bn >= 2 * N) break;
-    const int i = bn == 64 ? 0 : bn == 128 ? 1 : 2;
-    const double stage16[3] = {0.16, 0.22, 0.36}, epi16[3] = {1.3, 1.6, 2.9}, stage32[2] = {0.40, 0.50}, epi32[2] = {1.7, 2.4};
-    const double stage = fp32 ? stage32[i] : stage16[i], epi = fp32 ? epi32[i] : epi16[i];
+  const int unit = b_mn && !fp32 ? 64 : 32;              // columns come in chunks of 32, in mn-major runs of 64
+  for (int bn = unit; bn <= (fp32 ? 128 : 256); bn += unit) {
+    if (bn > unit && bn >= N + unit) break;
+    const double stage = fp32 ? 0.30 + 0.0016 * bn : 0.095 + 0.00104 * bn, epi = fp32 ? 0.3 + 0.015 * bn : 0.7 + 0.0045 * bn;
     Shape s;
     s.bn = bn;
     s.nk = (int)((K + kw - 1) / kw);

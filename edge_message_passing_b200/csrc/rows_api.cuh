@@ -83,7 +83,7 @@ DenseLayout dense_layout(const emp_dense& a) {
   auto take = [&](size_t bytes) { size_t r = L.total; L.total = align_up(L.total + bytes); return r; };
   L.x = packed(a.x, a.ldx, a.rows, a.fan_in, a.dtype, take);
   L.w = packed(a.weight, a.ldw, a.fan_out, a.fan_in, a.dtype, take);
-  L.h = dtc::shape_for(a.rows, a.fan_out, a.fan_in, a.dtype);
+  L.h = dtc::shape_for(a.rows, a.fan_out, a.fan_in, a.dtype, 0);
   L.part = take(L.h.splits > 1 ? (size_t)L.h.splits * a.rows * a.fan_out * 4 : 0);
   return L;
 }
@@ -136,12 +136,12 @@ DenseGradLayout dense_grad_layout(const emp_dense_grad& a) {
   L.colsum = take(a.g_bias ? (size_t)L.gz_blocks * a.fan_out * 4 : 0);
   if (a.g_x) {
     L.w = packed(a.weight, a.ldw, a.fan_out, a.fan_in, a.dtype, take);
-    L.hx = dtc::shape_for(a.rows, a.fan_in, a.fan_out, a.dtype);
+    L.hx = dtc::shape_for(a.rows, a.fan_in, a.fan_out, a.dtype, 1);
     L.part_x = take(L.hx.splits > 1 ? (size_t)L.hx.splits * a.rows * a.fan_in * 4 : 0);
   }
   if (a.g_weight) {
     L.x = packed(a.x, a.ldx, a.rows, a.fan_in, a.dtype, take);
-    L.hw = dtc::shape_for(a.fan_out, a.fan_in, a.rows, a.dtype);
+    L.hw = dtc::shape_for(a.fan_out, a.fan_in, a.rows, a.dtype, 1);
     L.part_w = take(L.hw.splits > 1 ? (size_t)L.hw.splits * a.fan_out * a.fan_in * 4 : 0);
   }
   return L;
