@@ -52,15 +52,16 @@ enum Path { DIRECT, SPLIT, SHORT };
 template <Path PATH, typename T, bool ROWS, bool SCALED>
 struct Cfg {
   static constexpr bool FP32 = PATH != DIRECT;
-  static constexpr int EPI = PATH == SHORT || (PATH == DIRECT && sizeof(T) == 2 && ROWS && !SCALED) ? 16 : 8;
+  static constexpr int EPI = PATH == SHORT || (ROWS && !SCALED) ? 16 : 8;
+  static constexpr int W = PATH == SPLIT && ROWS ? 16 : 32;                   // columns put out at once (staging)
   static constexpr int LAND = 3, SLOTS = 3;             // FP32: stages as they land (A and B; A alone in SHORT) and split
   static constexpr int LAND_BYTES = PATH == SHORT ? A_BYTES : 2 * A_BYTES;
   // A's split is in TMEM, B's hi and lo in shared memory: a place per slot, or per stage of the whole k in SHORT
   static constexpr int RING_BYTES = FP32 ? LAND * LAND_BYTES + (PATH == SHORT ? CHUNK_STAGES : SLOTS) * HL_BYTES : 4 * (A_BYTES + 256 * 128);
-  static constexpr int PLACE_BYTES = ROWS ? 32 * 32 * (int)sizeof(T) : 4096;
+  static constexpr int PLACE_BYTES = ROWS ? 32 * W * (int)sizeof(T) : 4096;
   static constexpr int PLACES = EPI == 8 && PLACE_BYTES == 2048 ? 2 : 1;      // of a warp
   static constexpr int STAGING = EPI * PLACES * PLACE_BYTES;
-  static constexpr int BIAS = EPI * 32 * (SCALED ? 4 : (int)sizeof(T));
+  static constexpr int BIAS = EPI * W * (SCALED ? 4 : (int)sizeof(T));
   static constexpr int BARS = 640;
   static constexpr int SMEM = 1024 + RING_BYTES + STAGING + BIAS + BARS;
   static constexpr int THREADS = 32 * (2 + EPI + (FP32 ? SPLIT_WARPS : 0));
@@ -176,10 +177,10 @@ __device__ __forceinline__ void stores_read() {            // all but the N late
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
-// 16-byte chunk j of row r of a staged tile: rows of 64 bytes (16-bit types; 64-byte swizzle) or 128 (128-byte)
-template <typename T>
+// 16-byte chunk j of row r of a staged tile: rows of 64 or 128 bytes, with the swizzle of that width
+template <int ROW_BYTES>
 __device__ __forceinline__ uint4* staged(unsigned char* place, int r, int j) {
-  return reinterpret_cast<uint4*>(sizeof(T) == 4 ? place + r * 128 + ((j ^ (r & 7)) << 4) : place + r * 64 + (((j ^ (r >> 1)) & 3) << 4));
+  return reinterpret_cast<uint4*>(ROW_BYTES == 128 ? place + r * 128 + ((j ^ (r & 7)) << 4) : place + r * 64 + (((j ^ (r >> 1)) & 3) << 4));
 }
 
 // Where it cannot (rows off 16-byte boundaries), the tile is turned through the staging (16-byte chunks XORed
@@ -446,28 +447,28 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
     wait(drain, 0);
   } else if (warp >= 2 && warp < 2 + EPI_WARPS) {
     // ---------------------------------------------------------------- epilogue
-    constexpr int V = 16 / sizeof(T), PLACE_BYTES = C::PLACE_BYTES, PLACES = C::PLACES;
+    constexpr int V = 16 / sizeof(T), W = C::W, ROW_BYTES = W * sizeof(T), PLACE_BYTES = C::PLACE_BYTES, PLACES = C::PLACES;
     using B = std::conditional_t<SCALED, float, T>;          // the bias's type
     const int q = warp & 3, sub = (warp - 2) >> 2;           // TMEM lanes q * 32 ..; chunks sub, sub + PER_QUARTER, ...
     unsigned char* place = sm + C::RING_BYTES + (warp - 2) * PLACES * PLACE_BYTES;
-    B* bsm = reinterpret_cast<B*>(sm + C::RING_BYTES + C::STAGING) + (warp - 2) * 32;
+    B* bsm = reinterpret_cast<B*>(sm + C::RING_BYTES + C::STAGING) + (warp - 2) * W;
     uint64_t* rbar = res_full + (warp - 2) * 2;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     const int nch = p.bn / 32;
-    uint32_t done = 0;                                       // chunks put through the places
+    uint32_t done = 0;                                       // pieces of W columns put through the places
     bool ok = true, asked = false;                           // asked: the next chunk's residual is on its way
     B bias_l = from_f<B>(0.f);
     float ws_l = 0.f, xs_l = 0.f;                            // of the next chunk: column lane's bias and scale, row lane's scale
     auto here = [&](const Item& t, int c) { return t.m0 + q * 32 < p.M && t.n0 + c * 32 < p.N; };
     constexpr int R = PATH == DIRECT ? 32 : 8;               // rows of a column at a time, without TMA
     float res[ROWS ? 2 : R];
-    auto ask_residual = [&](const Item& t, int c) {          // its place must be free
+    auto ask_residual = [&](const Item& t, int c, int h) {   // of piece h of the chunk; its place must be free
       if constexpr (!ROWS) {
         if (R == 32) load_column<T, R>(res, e, (int)min((long long)32, p.M - t.m0 - q * 32), t.m0 + q * 32, t.n0 + c * 32 + lane, p.N, 0);
       } else if (lane == 0) {
         const int pl = done % PLACES;
         tc::mbar_expect_tx(&rbar[pl], PLACE_BYTES);
-        tc::tma_load(place + pl * PLACE_BYTES, &maps.res, &rbar[pl], t.n0 + c * 32, (int)(t.m0 + q * 32));
+        tc::tma_load(place + pl * PLACE_BYTES, &maps.res, &rbar[pl], t.n0 + c * 32 + h * W, (int)(t.m0 + q * 32));
       }
     };
     // ask for what chunk c of an item needs
@@ -481,17 +482,17 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
         if (SCALED) ws_l = e.w_scale[n];
       }
       if (SCALED && m < p.M) xs_l = e.x_scale[m];
-      if (e.residual && (!ROWS || !e.z)) ask_residual(t, c);
+      if (e.residual && (!ROWS || !e.z)) ask_residual(t, c, 0);
       asked = true;
     };
-    // the warp's rows, packed, into a place, and ready for a TMA store
-    auto stage = [&](unsigned char* pp, const float (&v)[32]) {
+    // piece h of the warp's rows, packed, into a place, and ready for a TMA store
+    auto stage = [&](unsigned char* pp, const float (&v)[32], int h) {
 #pragma unroll
-      for (int j = 0; j < 32 / V; ++j) {
+      for (int j = 0; j < W / V; ++j) {
         float y[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) y[i] = v[j * V + i];
-        store_v<T, V>(reinterpret_cast<T*>(staged<T>(pp, lane, j)), y);
+        for (int i = 0; i < V; ++i) y[i] = v[h * W + j * V + i];
+        store_v<T, V>(reinterpret_cast<T*>(staged<ROW_BYTES>(pp, lane, j)), y);
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
@@ -534,57 +535,70 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
       const bool res_now = e.residual && !e.z;
       if (res_now && !asked && lane == 0) stores_read<PLACES - 1>();
       if (!asked) ask(t, c);
-      const int pl = done % PLACES;
-      unsigned char* pp = place + pl * PLACE_BYTES;
-      bsm[lane] = bias_l;
+      const B bias = bias_l;
       const float ws = ws_l, xs = xs_l;
-      __syncwarp();
-      if (SCALED || PATH == SPLIT || e.bias) {               // (SPLIT: a branch here costs spills)
-        constexpr int VB = 16 / sizeof(B);
 #pragma unroll
-        for (int j = 0; j < 32; j += VB) {
-          float b[VB];
-          unpack16<B, VB>(*reinterpret_cast<const uint4*>(bsm + j), b);
-#pragma unroll
-          for (int i = 0; i < VB; ++i) v[j + i] = SCALED ? fmaf(v[j + i], xs * __shfl_sync(0xffffffffu, ws, j + i), b[i]) : v[j + i] + b[i];
+      for (int h = 0; h < 32 / W; ++h) {
+        const int nh = n0 + h * W;
+        if (h && nh >= p.N) break;
+        const int pl = done % PLACES;
+        unsigned char* pp = place + pl * PLACE_BYTES;
+        if (h && res_now) {
+          if (lane == 0) stores_read<PLACES - 1>();
+          ask_residual(t, c, h);
         }
-      }
-      if (e.z) {                                             // z takes the place first, the residual after it
-        if (lane == 0) stores_read<PLACES - 1>();
-        __syncwarp();
-        stage(pp, v);
-        if (lane == 0) {
-          tma_store(&maps.z, pp, n0, (int)m0);
-          stores_read<0>();
+        if (SCALED || PATH == SPLIT || e.bias) {             // (SPLIT: a branch here costs spills)
+          constexpr int VB = 16 / sizeof(B);
+          if (W == 32 || lane / W == h) bsm[lane % W] = bias;
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < W; j += VB) {
+            float b[VB];
+            unpack16<B, VB>(*reinterpret_cast<const uint4*>(bsm + j), b);
+#pragma unroll
+            for (int i = 0; i < VB; ++i) {
+              float& u = v[h * W + j + i];
+              u = SCALED ? fmaf(u, xs * __shfl_sync(0xffffffffu, ws, h * W + j + i), b[i]) : u + b[i];
+            }
+          }
         }
-        __syncwarp();
-        if (e.residual) ask_residual(t, c);
-      }
-      // each step for the whole chunk: a branch per element would jump over the other activations' code every time
-      if (e.act == EMP_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) silu2(v[i], v[i + 1]);
-      } else if (e.act == EMP_ACT_GELU) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = act_f(EMP_ACT_GELU, v[i]);
-      }
-      if (e.residual) {
-        if (!__all_sync(0xffffffffu, wait(&rbar[pl], (uint32_t)((done / PLACES) & 1)))) { ok = false; return; }
-#pragma unroll
-        for (int j = 0; j < 32 / V; ++j) {
-          float a[V];
-          unpack16<T, V>(*staged<T>(pp, lane, j), a);
-#pragma unroll
-          for (int i = 0; i < V; ++i) v[j * V + i] += a[i];
+        if (e.z) {                                           // z takes the place first, the residual after it
+          if (lane == 0) stores_read<PLACES - 1>();
+          __syncwarp();
+          stage(pp, v, h);
+          if (lane == 0) {
+            tma_store(&maps.z, pp, nh, (int)m0);
+            stores_read<0>();
+          }
+          __syncwarp();
+          if (e.residual) ask_residual(t, c, h);
         }
+        // each step for the whole piece: a branch per element would jump over the other activations' code every time
+        if (e.act == EMP_ACT_SILU) {
+#pragma unroll
+          for (int i = 0; i < W; i += 2) silu2(v[h * W + i], v[h * W + i + 1]);
+        } else if (e.act == EMP_ACT_GELU) {
+#pragma unroll
+          for (int i = 0; i < W; ++i) v[h * W + i] = act_f(EMP_ACT_GELU, v[h * W + i]);
+        }
+        if (e.residual) {
+          if (!__all_sync(0xffffffffu, wait(&rbar[pl], (uint32_t)((done / PLACES) & 1)))) { ok = false; return; }
+#pragma unroll
+          for (int j = 0; j < W / V; ++j) {
+            float a[V];
+            unpack16<T, V>(*staged<ROW_BYTES>(pp, lane, j), a);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[h * W + j * V + i] += a[i];
+          }
+        }
+        if (!res_now && !e.z) {
+          if (lane == 0) stores_read<PLACES - 1>();
+          __syncwarp();
+        }
+        stage(pp, v, h);
+        if (lane == 0) tma_store(&maps.y, pp, nh, (int)m0);
+        ++done;
       }
-      if (!res_now && !e.z) {
-        if (lane == 0) stores_read<PLACES - 1>();
-        __syncwarp();
-      }
-      stage(pp, v);
-      if (lane == 0) tma_store(&maps.y, pp, n0, (int)m0);
-      ++done;
       asked = false;
       if (next >= 0 && here(tn, next)) {
         if (e.residual && !e.z && lane == 0) stores_read<PLACES - 1>();
@@ -599,20 +613,23 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
       const bool more = w + gridDim.x < p.items;
       tn = t.next(p);
       if constexpr (PATH == SPLIT) {
-        float acc[2][32];
+        constexpr int HELD = 4 / PER_QUARTER;                // chunks of a warp (bn is 128 at most)
+        float acc[HELD][32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) acc[0][i] = acc[1][i] = 0.f;
+        for (int c = 0; c < HELD; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[c][i] = 0.f;
         for (int k = 0; k < t.k_n; k += CHUNK_STAGES, ++ch) {
           const int buf = (int)(ch & 1);
           if (!__all_sync(0xffffffffu, wait(&acc_full[buf], (uint32_t)((ch >> 1) & 1)))) { ok = false; break; }
           tc::fence_after();
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            if (sub + 2 * c < nch) {
+          for (int c = 0; c < HELD; ++c) {
+            if (sub + PER_QUARTER * c < nch) {
 #pragma unroll
               for (int j = 0; j < 32; j += 16) {
                 float v[16];
-                tmem_ld16(lanes + (uint32_t)(buf * 128 + (sub + 2 * c) * 32 + j), v);
+                tmem_ld16(lanes + (uint32_t)(buf * 128 + (sub + PER_QUARTER * c) * 32 + j), v);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[c][j + i] += v[i];
               }
@@ -624,11 +641,13 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
         }
         if (!ok) break;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (sub + 2 * c < nch) {
-            const bool last = sub + 2 * c + 2 >= nch;
-            put(t, sub + 2 * c, acc[c], last ? tn : t, last ? (more ? sub : -1) : sub + 2 * c + 2);
+        for (int c = 0; c < HELD; ++c) {
+          const int at = sub + PER_QUARTER * c;
+          if (at < nch) {
+            const bool last = at + PER_QUARTER >= nch;
+            put(t, at, acc[c], last ? tn : t, last ? (more ? sub : -1) : at + PER_QUARTER);
           }
+        }
       } else {
         const int buf = (int)(ch & 1);
         if (!__all_sync(0xffffffffu, wait(&acc_full[buf], (uint32_t)((ch >> 1) & 1)))) break;
@@ -851,18 +870,19 @@ inline int launch(long long M, int N, long long K, int t, const Operand& a, cons
   const bool ok_a = a.mn ? make_map(&maps.a, a.p, t, M, K, a.ld, split ? BM : 64, kw, 128 * !split) : make_map(&maps.a, a.p, t, K, M, a.ld, kw, BM, 128);
   const bool ok_b = b.mn ? make_map(&maps.b, b.p, t, N, K, b.ld, split ? h.bn : 64, kw, 128 * !split) : make_map(&maps.b, b.p, t, K, N, b.ld, kw, h.bn, 128);
   if (!ok_a || !ok_b) return EMP_ERR_CUDA;
-  // rows of y, z and residual in 32 x 32 boxes
+  // SHORT: a whole number of CTAs per column of tiles, so that a CTA's column does not change
+  const bool one_chunk = split && h.splits == 1 && h.nk <= CHUNK_STAGES && h.ntiles <= tc::num_sms();
+  // rows of y, z and residual in boxes of 32 rows
+  const int cols = split && !one_chunk ? Cfg<SPLIT, float, true, false>::W : 32;
   const int ys = dtype_size(e.y_dtype), one = (N * ys + 15) / 16 * 16 / ys;       // a single row: any pitch will do
   auto fits = [&](const void* q, long long ld) { return !q || tma_ok(q, M == 1 ? one : ld, e.y_dtype); };
   const bool rows = !part && fits(e.y, e.ldy) && fits(e.z, e.ldz) && fits(e.residual, e.ldr);
   if (rows) {
     auto map = [&](CUtensorMap* m, const void* q, long long ld) {
-      return !q || make_map(m, q, e.y_dtype, N, M, M == 1 ? one : ld, 32, 32, 32 * ys);
+      return !q || make_map(m, q, e.y_dtype, N, M, M == 1 ? one : ld, cols, 32, cols * ys);
     };
     if (!map(&maps.y, e.y, e.ldy) || !map(&maps.z, e.z, e.ldz) || !map(&maps.res, e.residual, e.ldr)) return EMP_ERR_CUDA;
   }
-  // SHORT: a whole number of CTAs per column of tiles, so that a CTA's column does not change
-  const bool one_chunk = split && h.splits == 1 && h.nk <= CHUNK_STAGES && h.ntiles <= tc::num_sms();
   const int sms = tc::num_sms();
   const unsigned grid = (unsigned)std::min<long long>(p.items, one_chunk ? sms / h.ntiles * h.ntiles : sms);
   p.step_n = (int)(grid % p.ntiles);
