@@ -804,7 +804,7 @@ inline Shape shape_for(long long M, int N, long long K, int t, int b_mn) {
     s.ntiles = (N + bn - 1) / bn;
     const long long tiles = (long long)s.mtiles * s.ntiles;
     // one split, or as many as fill one to three waves of CTAs, of at least four stages each
-    for (int waves = 0; waves <= 3; ++waves) {
+    for (int waves = 0; waves <= (tiles < 3 * sms ? 3 : 0); ++waves) {
       const long long want = waves == 0 ? 1 : std::min<long long>(waves * (long long)sms / tiles, s.nk / 4);
       if (want < 1 || (waves && want < 2)) continue;
       s.per = (int)((s.nk + want - 1) / want);

@@ -632,27 +632,26 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? GRAD_PER_SM : 1) k_rms_nor
   for (long long b = blockIdx.x; b < groups; b += gridDim.x, par ^= 1) {
     const long long row = b * R + r;
     const bool live = row < p.rows;
-    Raw<T, V> gh[SL], sh[SL], th[SL];            // this row as it is in memory: unpacked for each use
+    float g[SL][V], s[SL][V];
+    Raw<T, V> th[SL];
     float ss = 0.f, hs = 0.f;
 #pragma unroll
     for (int k = 0; k < SL; ++k) {
-      gh[k] = g_[k];
-      sh[k] = s_[k];
+      g_[k].get(g[k]);
+      s_[k].get(s[k]);
       th[k] = t_[k];
     }
     fetch(row + (long long)gridDim.x * R);
 #pragma unroll
     for (int k = 0; k < SL; ++k) {
-      float wv[V], g[V], s[V];
+      float wv[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) wv[i] = 1.f;
       if (w) load_v<T, V>(w + at[k], wv);
-      gh[k].get(g);
-      sh[k].get(s);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        ss += s[i] * s[i];
-        hs += g[i] * wv[i] * s[i];
+        ss += s[k][i] * s[k][i];
+        hs += g[k][i] * wv[i] * s[k][i];
       }
     }
 #pragma unroll
@@ -675,17 +674,15 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? GRAD_PER_SM : 1) k_rms_nor
     for (int k = 0; k < SL; ++k) {
       const int c = (k * G + t) * V;
       if (c >= p.cols) continue;
-      float wv[V], o[V], g[V], s[V];
+      float wv[V], o[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) { wv[i] = 1.f; o[i] = 0.f; }
       if (w) load_v<T, V>(w + at[k], wv);
       if (p.g_s) th[k].get(o);
-      gh[k].get(g);
-      sh[k].get(s);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        o[i] += rstd * (g[i] * wv[i] - s[i] * q);
-        acc[k][i] += g[i] * (s[i] * rstd);
+        o[i] += rstd * (g[k][i] * wv[i] - s[k][i] * q);
+        acc[k][i] += g[k][i] * (s[k][i] * rstd);
       }
       store_v<T, V>(static_cast<T*>(p.g_x) + row * p.ldgx + c, o);
     }
