@@ -785,6 +785,7 @@ inline bool tma_ok(const void* p, long long ld, int t) {
 // tile takes the longer of its k stages and its epilogue (which runs beside the next tile's stages), the CTAs work in
 // waves, and splits pay for their partial products.  Microseconds as measured for the 16-bit and the FP32 kernel: a
 // stage with the operands in L2, the epilogue of a tile with one stage.
+constexpr int MAX_CHAIN = 1024;   // 4096 MMAs: a sum shrinks by 8e-5 of itself at most, a fiftieth of a bf16 step
 struct Shape {
   int bn, splits, per, nk, mtiles, ntiles;
 };
@@ -803,10 +804,12 @@ inline Shape shape_for(long long M, int N, long long K, int t, int b_mn) {
     s.mtiles = (int)((M + BM - 1) / BM);
     s.ntiles = (N + bn - 1) / bn;
     const long long tiles = (long long)s.mtiles * s.ntiles;
-    // one split, or as many as fill one to three waves of CTAs, of at least four stages each
+    // one split, or as many as fill one to three waves of CTAs, of at least four stages each; in any case so many that
+    // the 16-bit kernel's sums, which stay in the truncating accumulator, end after MAX_CHAIN stages
+    const int least = fp32 ? 1 : (s.nk + MAX_CHAIN - 1) / MAX_CHAIN;
     for (int waves = 0; waves <= (tiles < 3 * sms ? 3 : 0); ++waves) {
-      const long long want = waves == 0 ? 1 : std::min<long long>(waves * (long long)sms / tiles, s.nk / 4);
-      if (want < 1 || (waves && want < 2)) continue;
+      const long long want = waves == 0 ? least : std::min<long long>(waves * (long long)sms / tiles, s.nk / 4);
+      if (want < least || (waves && want < 2)) continue;
       s.per = (int)((s.nk + want - 1) / want);
       s.splits = (s.nk + s.per - 1) / s.per;
       const long long items = tiles * s.splits;

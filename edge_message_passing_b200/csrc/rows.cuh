@@ -121,7 +121,7 @@ __device__ __forceinline__ int degree_of(int lm) { return (lm > 0) + (lm > 3) + 
 // SiLU z / (1 + exp(-z)) and GELU z Phi(z), and their derivatives.  Phi, the normal distribution function, is
 // 1/2 erfc(-z / sqrt 2) with the rational approximation 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical
 // Functions (1964): erfc(x) = t (a1 + t (a2 + ...)) exp(-x^2), t = 1 / (1 + p x), within 1.5e-7 for x >= 0; erff costs
-// twice as much and bounds a short-k epilogue.  The error of GELU is below 1e-7 |z|, one and a half FP32 steps of z.
+// twice as much and bounds a short-k epilogue.  With the FP32 arithmetic the error of GELU is about 2e-7 |z|.
 __device__ __forceinline__ float phi_from(float z, float t, float e) {      // t = 1 / (1 + p x), e = exp(-x^2), x = |z| / sqrt 2
   float q = fmaf(t, 1.061405429f, -1.453152027f);
   q = fmaf(t, q, 1.421413741f);
@@ -150,21 +150,25 @@ __device__ __forceinline__ float dact_f(int act, float z) {
   }
   return 1.0f;
 }
-// SiLU of two values with one reciprocal: 1 / (p q) gives 1 / p and 1 / q.  The exponentials are capped at
-// e^43 so that the product stays finite (z < -43 comes out as z e^-43, 1e-17 at most); the cap also keeps a NaN
-// from the other value.  Three special-function instructions instead of four: they bound a short-k epilogue.
-__device__ __forceinline__ void silu2(float& a, float& b) {
+// The sigmoids of two values with one reciprocal: 1 / (p q) gives 1 / p and 1 / q (three special-function
+// instructions instead of four: they bound a short-k epilogue).  The exponentials are capped at e^43 so that the
+// product stays finite, which also keeps a NaN from the other value; below -43 the sigmoid (2e-19) is zero.
+__device__ __forceinline__ void sigmoid2(float a, float b, float& sa, float& sb) {
   const float p = 1.0f + __expf(-fmaxf(a, -43.0f)), q = 1.0f + __expf(-fmaxf(b, -43.0f));
   const float r = __fdividef(1.0f, p * q);
-  a *= r * q;
-  b *= r * p;
+  sa = a < -43.0f ? 0.0f : r * q;
+  sb = b < -43.0f ? 0.0f : r * p;
 }
-
-// the derivatives of two values, s (1 + z (1 - s)) each, likewise
+__device__ __forceinline__ void silu2(float& a, float& b) {
+  float sa, sb;
+  sigmoid2(a, b, sa, sb);
+  a *= sa;
+  b *= sb;
+}
+// the derivatives, s (1 + z (1 - s)) each
 __device__ __forceinline__ void dsilu2(float& a, float& b) {
-  const float p = 1.0f + __expf(-fmaxf(a, -43.0f)), q = 1.0f + __expf(-fmaxf(b, -43.0f));
-  const float r = __fdividef(1.0f, p * q);
-  const float sa = r * q, sb = r * p;
+  float sa, sb;
+  sigmoid2(a, b, sa, sb);
   a = sa * (1.0f + a * (1.0f - sa));
   b = sb * (1.0f + b * (1.0f - sb));
 }

@@ -582,3 +582,86 @@ def test_dense_of_any_alignment(rows, off, pad, type):
     ref = emp.mp_dense_grad(*(a.contiguous().clone() for a in (g, x, w)), z=z0.contiguous().clone(), activation="silu")
     for a, b in zip(got, ref):
         assert (a.double() - b.double()).abs().max() <= (4 * half_step(t) + 1e-5) * b.double().abs().max()
+
+
+# ------------------------------------------------------------------ the ends of the range
+EXTREME = [0.0, -0.0, 1e-30, -1e-30, 0.5, -0.5, 3.0, -3.0, 8.0, -8.0, 20.0, -20.0, 42.9, -42.9, 43.1, -43.1, 88.0, -88.0, 95.0, -95.0,
+           1e4, -1e4, 1e10, -1e10, 1e30, -1e30]
+
+
+@pytest.mark.parametrize("rows", [16, 160])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activations_over_the_whole_range(act, rows):
+    """y and dE/dx of a one-to-one layer (x 1, weights 1): z is x to 2^-20.  SiLU and GELU with 32 u |z| (the exponential's
+    argument and the approximation of the normal distribution, 1.5e-7 / 2, included) and 2^-20 |z| times a slope below
+    1.13; their slopes likewise with 64 u (1 + |z|) below |z| = 20, and exact limits beyond."""
+    z = np.array((EXTREME * 7)[:rows]).reshape(rows, 1)
+    x, w = dev(z, torch.float32), torch.ones((20, 1), device="cuda")
+    z = host(x)
+    y = host(emp.mp_dense(x, w, activation=act))
+    with np.errstate(over="ignore"):
+        ref, slope = orow.activation(z, act), orow.slope(z, act)
+    assert np.all(np.isfinite(y)) and np.all(np.abs(y - ref) <= (32 * U + 1.13 * 2.0 ** -20) * np.abs(z) + 1e-37)
+    assert np.all(y[z[:, 0] < -100] == 0)
+    g = torch.ones((rows, 20), device="cuda")
+    g_x, _, g_b = emp.mp_dense_grad(g, x, w, z=x.expand(rows, 20).contiguous(), activation=act)
+    near = np.abs(z[:, 0]) <= 20
+    d = np.abs(host(g_x) / 20 - slope)[:, 0]
+    assert np.all(d[near] <= 64 * U * (1 + np.abs(z[near, 0])) + 2.0 ** -20 * 20) and np.all(d[~near] <= 2.0 ** -19)
+    assert torch.isfinite(g_b).all()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_non_finite_values_through_an_activation(act):
+    """+inf stays, -inf and NaN give NaN as z sigma(z) and z Phi(z) do, and the neighbouring columns are not touched."""
+    x = torch.tensor([[float("inf")], [float("-inf")], [float("nan")], [1.0]], device="cuda").repeat(10, 1)
+    w = torch.zeros((40, 1), device="cuda", dtype=torch.float32)
+    w[7], w[20] = 1.0, 1.0
+    for rows in (8, 40):
+        for t in (torch.bfloat16, torch.float16):
+            y = emp.mp_dense(x[:rows].to(t), w.to(t), residual=torch.ones((rows, 40), device="cuda", dtype=t), activation=act)
+            col = y[:, 7].float()
+            assert torch.isinf(col[0::4]).all() and torch.isnan(col[1::4]).all() and torch.isnan(col[2::4]).all()
+            assert torch.isfinite(col[3::4]).all() and torch.equal(y[3::4, 0], torch.ones_like(y[3::4, 0]))
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements: the last rows come out as they do alone."""
+    rows, n = 1_100_000, 300
+    t = torch.bfloat16
+    w, wn = torch.randn((2048, 32), device="cuda").to(t), torch.ones(2048, device="cuda", dtype=t)
+    x = torch.randn((rows, 32), device="cuda").to(t)
+    y, z = emp.mp_dense(x, w, activation="silu", keep_z=True)
+    ys, zs = emp.mp_dense(x[-n:], w, activation="silu", keep_z=True)
+    assert torch.equal(y[-n:], ys) and torch.equal(z[-n:], zs)
+    # the 300 rows alone split their 2048 products (too few tiles for the SMs), the many rows do not: the two sums are each
+    # within 2 (n + 8) u sum|terms| of the exact one before they are rounded by at most half a step each
+    g_x, _, _ = emp.mp_dense_grad(y, x, w, z=z, activation="silu", need_weight=False, need_bias=False)
+    alone = emp.mp_dense_grad(ys, x[-n:], w, z=zs, activation="silu")[0]
+    size = (ys.double() * 1.13).abs() @ w.double().abs()
+    top = torch.maximum(g_x[-n:].double().abs(), alone.double().abs())
+    assert torch.all((g_x[-n:].double() - alone.double()).abs() <= 2 * half_step(t) * top + 4 * (2048 + 8) * U * size)
+    v, s = emp.mp_rms_norm(y, wn, residual=z)
+    vs, ss = emp.mp_rms_norm(ys, wn, residual=zs)
+    assert torch.equal(v[-n:], vs) and torch.equal(s[-n:], ss)
+    q, scale, _ = emp.mp_rms_norm(y, wn, quantize=True)
+    qs, scales, _ = emp.mp_rms_norm(ys, wn, quantize=True)
+    assert torch.equal(q[-n:].view(torch.uint8), qs.view(torch.uint8)) and torch.equal(scale[-n:], scales)
+    g_x, _ = emp.mp_rms_norm_grad(v, s, wn, g_s=z)
+    assert torch.equal(g_x[-n:], emp.mp_rms_norm_grad(vs, ss, wn, g_s=zs)[0])
+    del y, z, v, s, q, g_x
+    odd = torch.randn((rows, 1999), device="cuda", dtype=t)
+    v, _ = emp.mp_rms_norm(odd, wn[:1999])
+    vs, _ = emp.mp_rms_norm(odd[-n:].clone(), wn[:1999])
+    assert (v[-n:].float() - vs.float()).abs().max() <= 2.0 ** -7 * vs.float().abs().max()
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+def test_a_weight_gradient_over_many_rows(type):
+    """300000 rows: the sum of 300000 products keeps 2^-17 of its scale in FP32 and half a step in bf16 (2-norm)."""
+    t, rng = TYPES[type], np.random.default_rng(23)
+    x, g = dev(normal(rng, 300000, 64), t), dev(normal(rng, 300000, 48), t)
+    _, g_w, g_b = emp.mp_dense_grad(g, x, torch.zeros((48, 64), device="cuda", dtype=t), need_x=False)
+    ref = g.double().t() @ x.double()
+    assert ((g_w.double() - ref).norm() / ref.norm()).item() <= (2.0 ** -17 if t == torch.float32 else half_step(t))
+    assert ((g_b.double() - g.double().sum(0)).norm() / g.double().sum(0).norm()).item() <= (2.0 ** -17 if t == torch.float32 else half_step(t))
