@@ -78,7 +78,7 @@ struct DenseLayout {
 };
 DenseLayout dense_layout(const emp_dense& a) {
   DenseLayout L;
-  L.few = a.rows <= dense::FEW_ROWS;
+  L.few = dense::few_rows(a.rows, a.fan_out, a.fan_in);
   if (L.few) return L;
   auto take = [&](size_t bytes) { size_t r = L.total; L.total = align_up(L.total + bytes); return r; };
   L.x = packed(a.x, a.ldx, a.rows, a.fan_in, a.dtype, take);

@@ -195,7 +195,7 @@ def dense_tol(x, w, b, r, act, t, K, extra=0.0):
     return y, z, ty, tz
 
 
-DENSE_SHAPES = [(1, 1, 1), (1, 64, 128), (3, 7, 5), (8, 256, 1024), (9, 100, 33), (17, 515, 250), (64, 64, 64),
+DENSE_SHAPES = [(1, 1, 1), (1, 64, 128), (1, 2500, 40), (16, 2000, 1500), (5, 70, 9000), (3, 7, 5), (8, 256, 1024), (9, 100, 33), (17, 515, 250), (64, 64, 64),
                 (127, 32, 8), (128, 128, 128), (129, 130, 131), (257, 96, 512), (1000, 48, 25), (300, 2048, 72),
                 (2, 1100, 1000), (640, 64, 700)]
 
