@@ -631,7 +631,14 @@ def _row_torch():
     if _T is None:
         _T = _torch()
         _CODES.update({_T.float32: 0, _T.bfloat16: 1, _T.float16: 2, _T.float8_e4m3fn: 3})
+        # the stream's handle without a Stream object, where this torch has it
+        global _stream_of
+        _stream_of = getattr(_T._C, "_cuda_getCurrentRawStream", _stream_of)
     return _T
+
+
+def _stream_of(dev: int):
+    return _T.cuda.current_stream(dev).cuda_stream
 
 
 def _row_input(x, name: str):
@@ -675,7 +682,7 @@ def _launch(fn, args, dev: int, workspace=None):
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _launch(fn, args, dev, workspace)
-    stream = torch.cuda.current_stream(dev).cuda_stream
+    stream = _stream_of(dev)
     ref = ctypes.byref(args)
     if workspace is None:
         return fn(ref, stream)
@@ -805,7 +812,7 @@ def mp_dense(x, weight, bias=None, activation: str = "none", residual=None, x_sc
     if residual is not None:
         _same(residual, shape, out, dev, "residual")
         rr, ldr = _as_rows(residual, rows, N)
-    y = torch.empty(shape, dtype=out, device=x.device)
+    y = x.new_empty(shape, dtype=out)
     z = torch.empty_like(y) if keep_z else None
     a = DenseC(rows, K, N, code, ycode, act, xr.data_ptr(), ldx, _ptr(x_scale), wr.data_ptr(), ldw, _ptr(w_scale), _ptr(bias),
                _ptr(rr), ldr, y.data_ptr(), N, _ptr(z), N)
@@ -836,7 +843,7 @@ def mp_dense_grad(g, x, weight, z=None, activation: str = "none", need_x: bool =
     wr, ldw = _as_rows(weight, N, K)
     g_x = torch.empty_like(x, memory_format=torch.contiguous_format) if need_x else None
     g_w = torch.empty_like(weight, memory_format=torch.contiguous_format) if need_weight else None
-    g_b = torch.empty(N, dtype=x.dtype, device=x.device) if need_bias else None
+    g_b = x.new_empty(N) if need_bias else None
     a = DenseGradC(rows, K, N, code, act, gr.data_ptr(), ldg, _ptr(zr), ldz, xr.data_ptr(), ldx, wr.data_ptr(), ldw,
                    _ptr(g_x), K, _ptr(g_w), _ptr(g_b))
     _check(_launch(L.mp_dense_grad, a, dev, L.mp_dense_grad_workspace_bytes), "mp_dense_grad")

@@ -202,7 +202,8 @@ struct GzArgs {
   const void *g, *z;
   long long ldg, ldz, ldo;
   void* gz;                    // null: the bias gradient alone
-  float* part;                 // null without a bias gradient
+  float* part;                 // null without a bias gradient ...
+  void* g_b;                   // ... which a single block per column writes itself
 };
 template <typename T, int V>
 __global__ void __launch_bounds__(32 * GZ_WARPS, GZ_PER_SM) k_dense_gz(const GzArgs p) {
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(32 * GZ_WARPS, GZ_PER_SM) k_dense_gz(const GzA
       }
     }
   }
-  if (!p.part) return;
+  if (!p.g_b) return;
 #pragma unroll
   for (int i = 0; i < V; ++i) sm[w][i * 32 + lane] = s[i];
   __syncthreads();
@@ -265,7 +266,9 @@ __global__ void __launch_bounds__(32 * GZ_WARPS, GZ_PER_SM) k_dense_gz(const GzA
 #pragma unroll
     for (int i = 0; i < GZ_WARPS; ++i) t += sm[i][j];
     const int col = (blockIdx.y * 32 + (j & 31)) * V + (j >> 5);
-    if (col < p.cols) p.part[(size_t)blockIdx.x * p.cols + col] = t;
+    if (col >= p.cols) continue;
+    if (gridDim.x == 1) static_cast<T*>(p.g_b)[col] = from_f<T>(t);
+    else p.part[(size_t)blockIdx.x * p.cols + col] = t;
   }
 }
 

@@ -132,8 +132,9 @@ DenseGradLayout dense_grad_layout(const emp_dense_grad& a) {
   if (!L.prep && a.rows > 1) L.ldgz = a.ldg;
   L.gz_v = gz_vec(a);
   const int per = 32 * L.gz_v;        // columns of a block; one wave of blocks
-  L.gz_blocks = (int)std::max<long long>(1, std::min<long long>((a.rows + 31) / 32, std::max(1, tc::num_sms() * dense::GZ_PER_SM / ((a.fan_out + per - 1) / per))));
-  L.colsum = take(a.g_bias ? (size_t)L.gz_blocks * a.fan_out * 4 : 0);
+  // up to 256 rows one block per columns' block, which then needs no join (a launch less)
+  L.gz_blocks = a.rows <= 256 ? 1 : (int)std::max<long long>(1, std::min<long long>((a.rows + 31) / 32, std::max(1, tc::num_sms() * dense::GZ_PER_SM / ((a.fan_out + per - 1) / per))));
+  L.colsum = take(a.g_bias && L.gz_blocks > 1 ? (size_t)L.gz_blocks * a.fan_out * 4 : 0);
   if (a.g_x) {
     L.w = packed(a.weight, a.ldw, a.fan_out, a.fan_in, a.dtype, take);
     L.hx = dtc::shape_for(a.rows, a.fan_in, a.fan_out, a.dtype, 1);
@@ -313,11 +314,11 @@ int mp_dense_grad(const emp_dense_grad* a, void* ws, size_t ws_bytes, cudaStream
   if (st != EMP_OK) return st;
   if (L.prep || a->g_bias) {
     const dense::GzArgs z{a->rows, a->fan_out, a->activation, a->g, a->z, a->ldg, a->ldz, L.ldgz,
-                          L.prep ? at<char>(ws, L.gz) : nullptr, a->g_bias ? at<float>(ws, L.colsum) : nullptr};
+                          L.prep ? at<char>(ws, L.gz) : nullptr, L.gz_blocks > 1 ? at<float>(ws, L.colsum) : nullptr, a->g_bias};
     if (a->dtype == EMP_F32) dense_gz<float>(z, L.gz_blocks, L.gz_v, stream);
     else if (a->dtype == EMP_BF16) dense_gz<__nv_bfloat16>(z, L.gz_blocks, L.gz_v, stream);
     else dense_gz<__half>(z, L.gz_blocks, L.gz_v, stream);
-    if (a->g_bias) {
+    if (a->g_bias && L.gz_blocks > 1) {
       Scope sc_("col_join", stream);
       k_col_join<<<(a->fan_out + 31) / 32, 32 * JOIN_WARPS, 0, stream>>>(L.gz_blocks, a->fan_out, z.part, a->g_bias, a->dtype);
     }

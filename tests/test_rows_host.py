@@ -73,7 +73,7 @@ def test_dense_gradient(kw):
 def test_workspace():
     """Too small a workspace is refused before its pointer is looked at; then a null or misaligned one."""
     assert norm_grad(g_weight=P) == -6
-    a = emp.DenseGradC(rows=4, fan_in=64, fan_out=32, dtype=0, g=P, ldg=32, x=P, ldx=64, weight=P, ldw=64, g_x=P, ldgx=64,
+    a = emp.DenseGradC(rows=400, fan_in=64, fan_out=32, dtype=0, g=P, ldg=32, x=P, ldx=64, weight=P, ldw=64, g_x=P, ldgx=64,
                        g_bias=P)
     L = emp.lib()
     need = L.mp_dense_grad_workspace_bytes(ctypes.byref(a))
