@@ -179,36 +179,80 @@ __device__ __forceinline__ void copy_rows(void* dst, const void* src, int bytes)
     reinterpret_cast<unsigned char*>(dst)[i] = reinterpret_cast<const unsigned char*>(src)[i];
 }
 
-template <typename T, bool QUANT, int RW>                         // RW rows of a warp, side by side
+// In shared memory a warp reads a row by 32-bit words, two elements each of a 16-bit type: a row that begins inside a
+// word leaves out its first element, one that ends inside a word its last, and lane 0 takes that one by itself (for an
+// odd number of columns there is exactly one, for an even number none): 80896 x 515 in bf16 takes 46 us, 3.6 TB/s,
+// where it took 56 by elements; the time between a block's load and its store and instruction issue bound it.  Rows behind the last one are computed from whatever the shared memory
+// holds and not written.
+template <typename T> struct Word {                               // fp32: an element is a word
+  static constexpr int N = 1;
+  static __device__ __forceinline__ void get(uint32_t u, float (&v)[1]) { v[0] = __uint_as_float(u); }
+  static __device__ __forceinline__ uint32_t put(const float (&v)[1]) { return __float_as_uint(v[0]); }
+};
+template <typename T> struct Word16 {
+  static constexpr int N = 2;
+  static __device__ __forceinline__ void get(uint32_t u, float (&v)[2]) { unpack2<T>(u, v[0], v[1]); }
+  static __device__ __forceinline__ uint32_t put(const float (&v)[2]) { return pack2<T>(v[0], v[1]); }
+};
+template <> struct Word<__nv_bfloat16> : Word16<__nv_bfloat16> {};
+template <> struct Word<__half> : Word16<__half> {};
+
+inline __host__ __device__ int round16(int bytes) { return (bytes + 15) & ~15; }
+
+template <typename T, bool QUANT, bool RES, int RW>               // RW rows of a warp, side by side
 __global__ void __launch_bounds__(ODD_THREADS) k_rms_norm_odd(const Args p) {
   extern __shared__ __align__(16) unsigned char odd_sm[];
-  constexpr int WARPS = ODD_THREADS / 32, R = RW * WARPS;
+  using Wd = Word<T>;
+  constexpr int WARPS = ODD_THREADS / 32, R = RW * WARPS, N = Wd::N;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, C = p.cols / NCOMP;
   const long long row0 = (long long)blockIdx.x * R;
   const int rows = (int)min((long long)R, p.rows - row0), bytes = rows * p.cols * (int)sizeof(T);
-  const int area = (R * p.cols * (int)sizeof(T) + 15) / 16 * 16;
-  T* xs = reinterpret_cast<T*>(odd_sm);
-  T* rs = p.residual ? reinterpret_cast<T*>(odd_sm + area) : xs;
-  __nv_fp8_storage_t* qs = reinterpret_cast<__nv_fp8_storage_t*>(odd_sm + (p.residual ? 2 : 1) * area);
+  const int area = round16(R * p.cols * (int)sizeof(T));
+  float* wf = reinterpret_cast<float*>(odd_sm);                   // the weights, one per column
+  T* xs = reinterpret_cast<T*>(odd_sm + round16(4 * p.cols));
+  T* rs = RES ? reinterpret_cast<T*>(reinterpret_cast<unsigned char*>(xs) + area) : xs;
+  __nv_fp8_storage_t* qs = reinterpret_cast<__nv_fp8_storage_t*>(reinterpret_cast<unsigned char*>(rs) + area);
   const T* w = static_cast<const T*>(p.w);
   copy_rows(xs, static_cast<const T*>(p.x) + row0 * p.cols, bytes);
-  if (p.residual) copy_rows(rs, static_cast<const T*>(p.residual) + row0 * p.cols, bytes);
+  if (RES) copy_rows(rs, static_cast<const T*>(p.residual) + row0 * p.cols, bytes);
+  for (int c = threadIdx.x; c < p.cols; c += ODD_THREADS) wf[c] = w ? to_f(w[weight_at(c, C, p.degrees)]) : 1.f;
   __syncthreads();
-  const bool two = p.residual != nullptr;
-  const int first = warp * RW;
+  const int first = warp * RW, n = p.cols / N;
+  const uint32_t *xw[RW], *rw[RW];                                // the row's first whole word
+  int head[RW];                                                   // and its column
+#pragma unroll
+  for (int j = 0; j < RW; ++j) {
+    const int start = (first + j) * p.cols;
+    head[j] = N == 2 ? start & 1 : 0;
+    xw[j] = reinterpret_cast<const uint32_t*>(xs + start + head[j]);
+    rw[j] = reinterpret_cast<const uint32_t*>(rs + start + head[j]);
+  }
+  const bool loose = N == 2 && (p.cols & 1) && lane == 0;         // this lane takes the row's loose element
   float ss[RW], top[RW];
 #pragma unroll
-  for (int j = 0; j < RW; ++j) ss[j] = top[j] = 0.f;
+  for (int j = 0; j < RW; ++j) {
+    ss[j] = top[j] = 0.f;
+    if (loose) {
+      const int c = head[j] ? 0 : p.cols - 1, i = (first + j) * p.cols + c;
+      float v = to_f(xs[i]);
+      if (RES) v += to_f(rs[i]);
+      ss[j] = v * v;
+      if (QUANT) top[j] = max_abs(0.f, v * wf[c]);
+    }
+  }
 #pragma unroll 4
-  for (int c = lane; c < p.cols; c += 32) {
-    const float wv = QUANT && w ? to_f(w[weight_at(c, C, p.degrees)]) : 1.f;
+  for (int k = lane; k < n; k += 32) {
 #pragma unroll
     for (int j = 0; j < RW; ++j) {
-      const int i = (first + j) * p.cols + c;
-      float v = first + j < rows ? to_f(xs[i]) : 0.f;
-      if (two && first + j < rows) v += to_f(rs[i]);
-      ss[j] += v * v;
-      if (QUANT) top[j] = max_abs(top[j], v * wv);
+      float v[N], r[N];
+      Wd::get(xw[j][k], v);
+      if (RES) Wd::get(rw[j][k], r);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        if (RES) v[e] += r[e];
+        ss[j] = fmaf(v[e], v[e], ss[j]);
+        if (QUANT) top[j] = max_abs(top[j], v[e] * wf[head[j] + k * N + e]);
+      }
     }
   }
   float rstd[RW], inv[RW];
@@ -229,26 +273,45 @@ __global__ void __launch_bounds__(ODD_THREADS) k_rms_norm_odd(const Args p) {
     }
   }
 #pragma unroll 4
-  for (int c = lane; c < p.cols; c += 32) {
-    const float wv = w ? to_f(w[weight_at(c, C, p.degrees)]) : 1.f;
+  for (int k = lane; k < n; k += 32) {
 #pragma unroll
     for (int j = 0; j < RW; ++j) {
-      if (first + j >= rows) continue;
-      const int i = (first + j) * p.cols + c;
-      float v = to_f(xs[i]);
-      if (two) {
-        v += to_f(rs[i]);
-        rs[i] = from_f<T>(v);                                     // s
+      float v[N], r[N];
+      Wd::get(xw[j][k], v);
+      if (RES) {
+        Wd::get(rw[j][k], r);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] += r[e];
+        const_cast<uint32_t*>(rw[j])[k] = Wd::put(v);             // s
       }
-      const float y = v * rstd[j] * wv;
-      if (QUANT) store_e4m3<1>(qs + i, {y * inv[j]});
-      else xs[i] = from_f<T>(y);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        v[e] = v[e] * rstd[j] * wf[head[j] + k * N + e];
+        if (QUANT) v[e] *= inv[j];
+      }
+      if (!QUANT) const_cast<uint32_t*>(xw[j])[k] = Wd::put(v);
+      else
+#pragma unroll
+        for (int e = 0; e < N; ++e) store_e4m3<1>(qs + (first + j) * p.cols + head[j] + k * N + e, {v[e]});
     }
+  }
+#pragma unroll
+  for (int j = 0; j < RW; ++j) {
+    if (!loose) continue;
+    const int c = head[j] ? 0 : p.cols - 1, i = (first + j) * p.cols + c;
+    float v = to_f(xs[i]);
+    if (RES) {
+      v += to_f(rs[i]);
+      rs[i] = from_f<T>(v);
+    }
+    v = v * rstd[j] * wf[c];
+    if (QUANT) store_e4m3<1>(qs + i, {v * inv[j]});
+    else xs[i] = from_f<T>(v);
   }
   __syncthreads();
   if (QUANT) copy_rows(static_cast<__nv_fp8_storage_t*>(p.y) + row0 * p.cols, qs, rows * p.cols);
   else copy_rows(static_cast<T*>(p.y) + row0 * p.cols, xs, bytes);
-  if (p.s && two) copy_rows(static_cast<T*>(p.s) + row0 * p.cols, rs, bytes);
+  if (RES && p.s) copy_rows(static_cast<T*>(p.s) + row0 * p.cols, rs, bytes);
 }
 
 // The gradient of the same rows: persistent, a row per warp at a time; a lane's columns are the same in every
@@ -787,12 +850,16 @@ cudaError_t launch_fwd_staged(const Args& a, cudaStream_t st) {
   if (h.NA == 16) return launch_staged<k_rms_norm_staged<T, QUANT, 16>>(a, h, blocks, st);
   return launch_staged<k_rms_norm_staged<T, QUANT, 32>>(a, h, blocks, st);
 }
+template <typename T, bool QUANT, bool RES, int RW>
+bool launch_odd4(const Args& a, int smem, cudaStream_t st) {
+  if (allow_smem<k_rms_norm_odd<T, QUANT, RES, RW>>(ODD_SMEM) != cudaSuccess) return false;
+  const int R = RW * ODD_THREADS / 32;
+  k_rms_norm_odd<T, QUANT, RES, RW><<<(unsigned)((a.rows + R - 1) / R), ODD_THREADS, smem, st>>>(a);
+  return true;
+}
 template <typename T, bool QUANT, int RW>
 bool launch_odd3(const Args& a, int smem, cudaStream_t st) {
-  if (allow_smem<k_rms_norm_odd<T, QUANT, RW>>(ODD_SMEM) != cudaSuccess) return false;
-  const int R = RW * ODD_THREADS / 32;
-  k_rms_norm_odd<T, QUANT, RW><<<(unsigned)((a.rows + R - 1) / R), ODD_THREADS, smem, st>>>(a);
-  return true;
+  return a.residual ? launch_odd4<T, QUANT, true, RW>(a, smem, st) : launch_odd4<T, QUANT, false, RW>(a, smem, st);
 }
 inline bool packed_rows(const void* p, long long ld, const Args& a) {       // contiguous, on a 16-byte boundary
   return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld == a.cols || a.rows == 1));
@@ -804,7 +871,7 @@ bool launch_odd(const Args& a, bool quant, cudaStream_t st) {
     return false;
   const int row = a.cols * (int)sizeof(T) * (a.residual ? 2 : 1) + (quant ? a.cols : 0);
   const int per = ODD_THREADS / 32;                                // 8 rows, or 16 (which 8-bit rows need for 16 bytes)
-  const int s16 = 2 * per * row + 64, s8 = per * row + 64;
+  const int s16 = 2 * per * row + 4 * a.cols + 64, s8 = per * row + 4 * a.cols + 64;
   // two rows a warp where that leaves four blocks on an SM
   if (s16 <= (quant ? ODD_SMEM : 56 * 1024) && (quant || a.rows > 2 * per * 148)) return quant ? launch_odd3<T, true, 2>(a, s16, st) : launch_odd3<T, false, 2>(a, s16, st);
   if (!quant && s8 <= ODD_SMEM) return launch_odd3<T, false, 1>(a, s8, st);
