@@ -237,19 +237,11 @@ __global__ void __launch_bounds__(32 * GZ_WARPS, GZ_PER_SM) k_dense_gz(const GzA
         if (m >= p.rows) break;
         // a rounded product (no contraction into the sum), so that g_bias has the same bits with and without gz
         if (p.act == EMP_ACT_SILU) {
-          if constexpr (V == 1) {
-            a[k][0] = __fmul_rn(a[k][0], dsilu_fast(b[k][0]));
-          } else {
 #pragma unroll
-            for (int i = 0; i < V; i += 2) {
-              dsilu2(b[k][i], b[k][i + 1]);
-              a[k][i] = __fmul_rn(a[k][i], b[k][i]);
-              a[k][i + 1] = __fmul_rn(a[k][i + 1], b[k][i + 1]);
-            }
-          }
+          for (int i = 0; i < V; ++i) a[k][i] = __fmul_rn(a[k][i], dact<EMP_ACT_SILU>(b[k][i]));
         } else if (p.act == EMP_ACT_GELU) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) a[k][i] = __fmul_rn(a[k][i], dact_f(EMP_ACT_GELU, b[k][i]));
+          for (int i = 0; i < V; ++i) a[k][i] = __fmul_rn(a[k][i], dact<EMP_ACT_GELU>(b[k][i]));
         }
         if (p.gz) store_v<T, V>(o + m * p.ldo, a[k]);
 #pragma unroll

@@ -206,10 +206,10 @@ __device__ __forceinline__ void finish_column(float (&v)[R], const float (&res)[
   }
   if (e.act == EMP_ACT_SILU) {
 #pragma unroll
-    for (int k = 0; k < R; k += 2) silu2(v[k], v[k + 1]);
+    for (int k = 0; k < R; ++k) v[k] = act<EMP_ACT_SILU>(v[k]);
   } else if (e.act == EMP_ACT_GELU) {
 #pragma unroll
-    for (int k = 0; k < R; ++k) v[k] = act_f(EMP_ACT_GELU, v[k]);
+    for (int k = 0; k < R; ++k) v[k] = act<EMP_ACT_GELU>(v[k]);
   }
   if (e.residual) {
 #pragma unroll
@@ -576,10 +576,10 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
         // each step for the whole piece: a branch per element would jump over the other activations' code every time
         if (e.act == EMP_ACT_SILU) {
 #pragma unroll
-          for (int i = 0; i < W; i += 2) silu2(v[h * W + i], v[h * W + i + 1]);
+          for (int i = 0; i < W; ++i) v[h * W + i] = act<EMP_ACT_SILU>(v[h * W + i]);
         } else if (e.act == EMP_ACT_GELU) {
 #pragma unroll
-          for (int i = 0; i < W; ++i) v[h * W + i] = act_f(EMP_ACT_GELU, v[h * W + i]);
+          for (int i = 0; i < W; ++i) v[h * W + i] = act<EMP_ACT_GELU>(v[h * W + i]);
         }
         if (e.residual) {
           if (!__all_sync(0xffffffffu, wait(&rbar[pl], (uint32_t)((done / PLACES) & 1)))) { ok = false; return; }

@@ -118,59 +118,56 @@ __device__ __forceinline__ void store_any(void* p, size_t i, int t, float v) {
 __device__ __forceinline__ int degree_of(int lm) { return (lm > 0) + (lm > 3) + (lm > 8); }
 
 // ------------------------------------------------------------- activations
-// SiLU z / (1 + exp(-z)) and GELU z Phi(z), and their derivatives.  Phi, the normal distribution function, is
-// 1/2 erfc(-z / sqrt 2) with the rational approximation 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical
-// Functions (1964): erfc(x) = t (a1 + t (a2 + ...)) exp(-x^2), t = 1 / (1 + p x), within 1.5e-7 for x >= 0; erff costs
-// twice as much and bounds a short-k epilogue.  With the FP32 arithmetic the error of GELU is about 2e-7 |z|.
-__device__ __forceinline__ float phi_from(float z, float t, float e) {      // t = 1 / (1 + p x), e = exp(-x^2), x = |z| / sqrt 2
-  float q = fmaf(t, 1.061405429f, -1.453152027f);
-  q = fmaf(t, q, 1.421413741f);
-  q = fmaf(t, q, -0.284496736f);
-  q = fmaf(t, q, 0.254829592f);
-  const float h = 0.5f * t * q * e;                       // Phi(-|z|)
+// SiLU z / (1 + exp(-z)) and GELU z Phi(z), and their derivatives, with e^x = 2^(x log2 e) by the special-function
+// unit's 2^x and 1/x, both with results below 2^-126 as zero: __expf and __fdividef, which keep those, take 14
+// instructions an element of SiLU instead of 5, and instructions bound a short-k epilogue (647168 x 64 -> 512 in FP32:
+// 401 us so, AFTER).  -inf and NaN give NaN.  Phi, the normal distribution function, is 1/2 erfc(-z / sqrt 2) with the rational
+// approximation 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical Functions (1964): erfc(x) = t (a1 + t (a2 + ...))
+// exp(-x^2), t = 1 / (1 + p x), within 1.5e-7 for x >= 0; erff costs more than twice as much.  With the FP32 arithmetic
+// the error of GELU is about 2e-7 |z|.
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float GELU_P = 0.3275911f * 0.70710678f;        // p / sqrt 2
+
+__device__ __forceinline__ float sigmoid_ftz(float z) { return rcp_ftz(1.0f + ex2_ftz(-LOG2E * z)); }
+__device__ __forceinline__ float phi_ftz(float z, float gauss) {            // Phi(z); gauss = exp(-z^2 / 2)
+  const float t = rcp_ftz(fmaf(GELU_P, fabsf(z), 1.f));
+  float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+  q = fmaf(t, q, 0.5f * 1.421413741f);
+  q = fmaf(t, q, 0.5f * -0.284496736f);
+  q = fmaf(t, q, 0.5f * 0.254829592f);
+  const float h = t * q * gauss;                          // Phi(-|z|)
   return z < 0.f ? h : 1.f - h;
 }
-constexpr float GELU_P = 0.3275911f * 0.70710678f;        // p / sqrt 2
-__device__ __forceinline__ float phi_f(float z, float* gauss) {             // Phi(z); *gauss = exp(-z^2 / 2)
-  *gauss = __expf(-0.5f * z * z);
-  return phi_from(z, __fdividef(1.f, fmaf(GELU_P, fabsf(z), 1.f)), *gauss);
+__device__ __forceinline__ float gauss_ftz(float z) { return ex2_ftz(-0.5f * LOG2E * z * z); }
+
+template <int ACT> __device__ __forceinline__ float act(float z) {
+  if constexpr (ACT == EMP_ACT_SILU) return z * sigmoid_ftz(z);
+  else if constexpr (ACT == EMP_ACT_GELU) return z * phi_ftz(z, gauss_ftz(z));
+  else return z;
 }
-__device__ __forceinline__ float act_f(int act, float z) {
-  if (act == EMP_ACT_SILU) return silu_f(z);
-  float g;
-  if (act == EMP_ACT_GELU) return z * phi_f(z, &g);
-  return z;
-}
-__device__ __forceinline__ float dact_f(int act, float z) {
-  if (act == EMP_ACT_SILU) return dsilu_f(z);
-  if (act == EMP_ACT_GELU) {
-    float g;
-    const float phi = phi_f(z, &g);
-    return phi + z * 0.39894228040143268f * g;
+template <int ACT> __device__ __forceinline__ float dact(float z) {
+  if constexpr (ACT == EMP_ACT_SILU) {
+    const float s = sigmoid_ftz(z);
+    return s * (1.0f + z * (1.0f - s));
+  } else if constexpr (ACT == EMP_ACT_GELU) {
+    const float g = gauss_ftz(z);
+    return phi_ftz(z, g) + z * 0.39894228040143268f * g;
+  } else {
+    return 1.0f;
   }
-  return 1.0f;
 }
-// The sigmoids of two values with one reciprocal: 1 / (p q) gives 1 / p and 1 / q (three special-function
-// instructions instead of four: they bound a short-k epilogue).  The exponentials are capped at e^43 so that the
-// product stays finite, which also keeps a NaN from the other value; below -43 the sigmoid (2e-19) is zero.
-__device__ __forceinline__ void sigmoid2(float a, float b, float& sa, float& sb) {
-  const float p = 1.0f + __expf(-fmaxf(a, -43.0f)), q = 1.0f + __expf(-fmaxf(b, -43.0f));
-  const float r = __fdividef(1.0f, p * q);
-  sa = a < -43.0f ? 0.0f : r * q;
-  sb = b < -43.0f ? 0.0f : r * p;
-}
-__device__ __forceinline__ void silu2(float& a, float& b) {
-  float sa, sb;
-  sigmoid2(a, b, sa, sb);
-  a *= sa;
-  b *= sb;
-}
-// the derivatives, s (1 + z (1 - s)) each
-__device__ __forceinline__ void dsilu2(float& a, float& b) {
-  float sa, sb;
-  sigmoid2(a, b, sa, sb);
-  a = sa * (1.0f + a * (1.0f - sa));
-  b = sb * (1.0f + b * (1.0f - sb));
+__device__ __forceinline__ float act_f(int a, float z) {
+  return a == EMP_ACT_SILU ? act<EMP_ACT_SILU>(z) : a == EMP_ACT_GELU ? act<EMP_ACT_GELU>(z) : z;
 }
 
 // ------------------------------------------------------------- join of column sums
