@@ -53,6 +53,7 @@ template <Path PATH, typename T, bool ROWS, bool SCALED>
 struct Cfg {
   static constexpr bool FP32 = PATH != DIRECT;
   static constexpr int EPI = PATH == SHORT || (ROWS && !SCALED) ? 16 : 8;
+  static constexpr int SETS = PATH == SHORT ? 2 : 1;
   static constexpr int W = PATH == SPLIT && ROWS ? 16 : 32;                   // columns put out at once (staging)
   static constexpr int LAND = 3, SLOTS = 3;             // FP32: stages as they land (A and B; A alone in SHORT) and split
   static constexpr int LAND_BYTES = PATH == SHORT ? A_BYTES : 2 * A_BYTES;
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&acc_full[b], 1);
-      tc::mbar_init(&acc_empty[b], EPI_WARPS);
+      tc::mbar_init(&acc_empty[b], EPI_WARPS / C::SETS);
     }
     tc::mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -449,7 +450,9 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
     // ---------------------------------------------------------------- epilogue
     constexpr int V = 16 / sizeof(T), W = C::W, ROW_BYTES = W * sizeof(T), PLACE_BYTES = C::PLACE_BYTES, PLACES = C::PLACES;
     using B = std::conditional_t<SCALED, float, T>;          // the bias's type
-    const int q = warp & 3, sub = (warp - 2) >> 2;           // TMEM lanes q * 32 ..; chunks sub, sub + PER_QUARTER, ...
+    constexpr int SETS = C::SETS, per = PER_QUARTER / SETS;
+    const int set = ((warp - 2) >> 2) / per;
+    const int q = warp & 3, sub = ((warp - 2) >> 2) % per;   // TMEM lanes q * 32 ..; chunks sub, sub + per, ...
     unsigned char* place = sm + C::RING_BYTES + (warp - 2) * PLACES * PLACE_BYTES;
     B* bsm = reinterpret_cast<B*>(sm + C::RING_BYTES + C::STAGING) + (warp - 2) * W;
     uint64_t* rbar = res_full + (warp - 2) * 2;
@@ -605,13 +608,17 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
         ask(tn, next);
       }
     };
-    uint32_t ch = 0;
+    uint32_t ch = set;                                       // accumulators before the warp's next one
+    const long long step = (long long)SETS * gridDim.x;
     Item t = first_item(p);
-    if (!p.part && sub < nch && here(t, sub)) ask(t, sub);
+    if (set) t = t.next(p);
+    const long long w0 = blockIdx.x + (long long)set * gridDim.x;
+    if (!p.part && w0 < p.items && sub < nch && here(t, sub)) ask(t, sub);
     Item tn;
-    for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x, t = tn) {
-      const bool more = w + gridDim.x < p.items;
+    for (long long w = w0; w < p.items && ok; w += step, t = tn) {
+      const bool more = w + step < p.items;
       tn = t.next(p);
+      if (SETS == 2) tn = tn.next(p);
       if constexpr (PATH == SPLIT) {
         constexpr int HELD = 4 / PER_QUARTER;                // chunks of a warp (bn is 128 at most)
         float acc[HELD][32];
@@ -653,19 +660,19 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
         if (!__all_sync(0xffffffffu, wait(&acc_full[buf], (uint32_t)((ch >> 1) & 1)))) break;
         tc::fence_after();
 #pragma unroll 1
-        for (int c = sub; c < nch; c += PER_QUARTER) {
+        for (int c = sub; c < nch; c += per) {
           float v[32];
           tc::tmem_ld32(lanes + (uint32_t)(buf * (FP32 ? 128 : 256) + c * 32), v);
-          const bool last = c + PER_QUARTER >= nch;
+          const bool last = c + per >= nch;
           if (last) {                                        // the last read of this accumulator
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&acc_empty[buf]);
           }
-          put(t, c, v, last ? tn : t, last ? (more ? sub : -1) : c + PER_QUARTER);
+          put(t, c, v, last ? tn : t, last ? (more ? sub : -1) : c + per);
         }
         if (sub >= nch && lane == 0) tc::mbar_arrive(&acc_empty[buf]);   // a narrow tile has no chunk for this warp
-        ++ch;
+        ch += SETS;
       }
     }
     if (ROWS) {
