@@ -199,6 +199,16 @@ template <> struct Word<__half> : Word16<__half> {};
 
 inline __host__ __device__ int round16(int bytes) { return (bytes + 15) & ~15; }
 
+// the same into shared memory without waiting (up to cp.async.wait_all)
+__device__ __forceinline__ void copy_rows_async(void* dst, const void* src, int bytes) {
+  const int n = bytes >> 4;
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  for (int i = threadIdx.x; i < n; i += ODD_THREADS)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + i * 16), "l"(reinterpret_cast<const uint4*>(src) + i) : "memory");
+  for (int i = (n << 4) + threadIdx.x; i < bytes; i += ODD_THREADS)
+    reinterpret_cast<unsigned char*>(dst)[i] = reinterpret_cast<const unsigned char*>(src)[i];
+}
+
 template <typename T, bool QUANT, bool RES, int RW>               // RW rows of a warp, side by side
 __global__ void __launch_bounds__(ODD_THREADS) k_rms_norm_odd(const Args p) {
   extern __shared__ __align__(16) unsigned char odd_sm[];
@@ -314,43 +324,74 @@ __global__ void __launch_bounds__(ODD_THREADS) k_rms_norm_odd(const Args p) {
   if (RES && p.s) copy_rows(static_cast<T*>(p.s) + row0 * p.cols, rs, bytes);
 }
 
-// The gradient of the same rows: persistent, a row per warp at a time; a lane's columns are the same in every
-// row, so its part of g_w stays in registers (NA of them: up to 32 NA columns).
+// The gradient of the same rows: persistent, a row per warp at a time, read by words in the same way.  Whether a row begins
+// inside a word depends on the warp alone, so a lane's columns are the same in every row of its, and its part of g_w
+// stays in registers (NS words, and the loose column of lane 0).  The next rows are on their way (cp.async) into the
+// other half of the shared memory meanwhile.
 constexpr int ODD_GRAD_COLS = 1024;
-template <typename T, int NA>
+template <typename T, int NS>
 __global__ void __launch_bounds__(ODD_THREADS) k_rms_norm_grad_odd(const GradArgs p) {
   extern __shared__ __align__(16) unsigned char odd_sm[];
-  constexpr int R = ODD_THREADS / 32;
+  using Wd = Word<T>;
+  constexpr int R = ODD_THREADS / 32, N = Wd::N;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, C = p.cols / NCOMP;
   const int area = R * p.cols * (int)sizeof(T);                   // a multiple of 16: R = 8
-  T* gs = reinterpret_cast<T*>(odd_sm);
-  T* ss_ = reinterpret_cast<T*>(odd_sm + area);
-  T* ts = reinterpret_cast<T*>(odd_sm + 2 * area);
+  const int half = area * (p.g_s ? 3 : 2);                        // g, s and g_s of R rows
   const T* w = static_cast<const T*>(p.w);
-  float acc[NA], wv[NA];
+  const int start = warp * p.cols, head = N == 2 ? start & 1 : 0, n = p.cols / N;
+  const bool loose = N == 2 && (p.cols & 1) && lane == 0;
+  const int lc = head ? 0 : p.cols - 1;                           // the loose column
+  auto weight = [&](int c) { return w ? to_f(w[weight_at(c, C, p.degrees)]) : 1.f; };
+  float acc[NS][N], wv[NS][N], accl = 0.f, wl = loose ? weight(lc) : 0.f;
 #pragma unroll
-  for (int k = 0; k < NA; ++k) {
-    const int c = lane + 32 * k;
-    acc[k] = 0.f;
-    wv[k] = w && c < p.cols ? to_f(w[weight_at(c, C, p.degrees)]) : 1.f;
-  }
+  for (int k = 0; k < NS; ++k)
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      acc[k][e] = 0.f;
+      wv[k][e] = lane + 32 * k < n ? weight(head + (lane + 32 * k) * N + e) : 0.f;
+    }
   const long long groups = (p.rows + R - 1) / R;
+  auto rows_of = [&](long long b) { return (int)min((long long)R, p.rows - b * R); };
+  auto fetch = [&](long long b, unsigned char* to) {
+    const long long at = b * R * p.cols;
+    const int bytes = rows_of(b) * p.cols * (int)sizeof(T);
+    copy_rows_async(to, static_cast<const T*>(p.g) + at, bytes);
+    copy_rows_async(to + area, static_cast<const T*>(p.s) + at, bytes);
+    if (p.g_s) copy_rows_async(to + 2 * area, static_cast<const T*>(p.g_s) + at, bytes);
+  };
+  unsigned char* cur = odd_sm;
+  unsigned char* other = odd_sm + half;
+  if (blockIdx.x < groups) fetch(blockIdx.x, cur);
   for (long long b = blockIdx.x; b < groups; b += gridDim.x) {
-    const long long row0 = b * R;
-    const int rows = (int)min((long long)R, p.rows - row0), bytes = rows * p.cols * (int)sizeof(T);
-    copy_rows(gs, static_cast<const T*>(p.g) + row0 * p.cols, bytes);
-    copy_rows(ss_, static_cast<const T*>(p.s) + row0 * p.cols, bytes);
-    if (p.g_s) copy_rows(ts, static_cast<const T*>(p.g_s) + row0 * p.cols, bytes);
-    __syncthreads();
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();                                              // cur has landed, other's rows have been copied out
+    if (b + gridDim.x < groups) fetch(b + gridDim.x, other);
+    const int rows = rows_of(b);
+    T* gs = reinterpret_cast<T*>(cur);
+    const T* ss_ = reinterpret_cast<const T*>(cur + area);
+    const T* ts = reinterpret_cast<const T*>(cur + 2 * area);
+    uint32_t* gw = reinterpret_cast<uint32_t*>(gs + start + head) + lane;
+    const uint32_t* sw = reinterpret_cast<const uint32_t*>(ss_ + start + head) + lane;
+    const uint32_t* tw = reinterpret_cast<const uint32_t*>(ts + start + head) + lane;
     if (warp < rows) {
-      const int base = warp * p.cols + lane;
+      const int li = start + lc;
       float s2 = 0.f, hs = 0.f;
+      if (loose) {
+        const float s = to_f(ss_[li]);
+        s2 = s * s;
+        hs = to_f(gs[li]) * wl * s;
+      }
 #pragma unroll
-      for (int k = 0; k < NA; ++k)
-        if (lane + 32 * k < p.cols) {
-          const float s = to_f(ss_[base + 32 * k]);
-          s2 += s * s;
-          hs += to_f(gs[base + 32 * k]) * wv[k] * s;
+      for (int k = 0; k < NS; ++k)
+        if (lane + 32 * k < n) {
+          float s[N], g[N];
+          Wd::get(sw[32 * k], s);
+          Wd::get(gw[32 * k], g);
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            s2 += s[e] * s[e];
+            hs += g[e] * wv[k][e] * s[e];
+          }
         }
 #pragma unroll
       for (int o = 16; o; o >>= 1) {
@@ -359,28 +400,51 @@ __global__ void __launch_bounds__(ODD_THREADS) k_rms_norm_grad_odd(const GradArg
       }
       const float rstd = rsqrtf(s2 / (float)p.cols + p.eps), q = hs * rstd * rstd / (float)p.cols;
 #pragma unroll
-      for (int k = 0; k < NA; ++k)
-        if (lane + 32 * k < p.cols) {
-          const int i = base + 32 * k;
-          const float s = to_f(ss_[i]), g = to_f(gs[i]);
-          float o = rstd * (g * wv[k] - s * q);
-          if (p.g_s) o += to_f(ts[i]);
-          acc[k] += g * (s * rstd);
-          gs[i] = from_f<T>(o);
+      for (int k = 0; k < NS; ++k)
+        if (lane + 32 * k < n) {
+          float s[N], g[N], o[N];
+          Wd::get(sw[32 * k], s);
+          Wd::get(gw[32 * k], g);
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            o[e] = rstd * (g[e] * wv[k][e] - s[e] * q);
+            acc[k][e] += g[e] * (s[e] * rstd);
+          }
+          if (p.g_s) {
+            float t[N];
+            Wd::get(tw[32 * k], t);
+#pragma unroll
+            for (int e = 0; e < N; ++e) o[e] += t[e];
+          }
+          gw[32 * k] = Wd::put(o);
         }
+      if (loose) {
+        const float s = to_f(ss_[li]), g = to_f(gs[li]);
+        float o = rstd * (g * wl - s * q);
+        if (p.g_s) o += to_f(ts[li]);
+        accl += g * (s * rstd);
+        gs[li] = from_f<T>(o);
+      }
     }
     __syncthreads();
-    copy_rows(static_cast<T*>(p.g_x) + row0 * p.cols, gs, bytes);
-    __syncthreads();
+    copy_rows(static_cast<T*>(p.g_x) + b * R * p.cols, gs, rows * p.cols * (int)sizeof(T));
+    unsigned char* t = cur;
+    cur = other;
+    other = t;
   }
   if (!p.part) return;
+  __syncthreads();
   float* sum = reinterpret_cast<float*>(odd_sm);                  // [cols]; the warps in order
   for (int q = 0; q < R; ++q) {
     if (q) __syncthreads();
-    if (warp == q)
+    if (warp != q) continue;
+    auto add = [&](int c, float a) { sum[c] = q ? sum[c] + a : a; };
 #pragma unroll
-      for (int k = 0; k < NA; ++k)
-        if (lane + 32 * k < p.cols) sum[lane + 32 * k] = q ? sum[lane + 32 * k] + acc[k] : acc[k];
+    for (int k = 0; k < NS; ++k)
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (lane + 32 * k < n) add(head + (lane + 32 * k) * N + e, acc[k][e]);
+    if (loose) add(lc, accl);
   }
   __syncthreads();
   const int nout = p.degrees ? 4 * C : p.cols;
@@ -900,11 +964,11 @@ void launch_grad2(const GradArgs& a, const Shape& h, int blocks, cudaStream_t st
   if (h.G * h.R <= 256) k_rms_norm_grad<T, V, SL, 256><<<blocks, dim3(h.G, h.R), smem, st>>>(a);
   else k_rms_norm_grad<T, V, SL, MAX_THREADS><<<blocks, dim3(h.G, h.R), smem, st>>>(a);
 }
-template <typename T, int NA>
+template <typename T, int NS>
 int launch_grad_odd3(const GradArgs& a, int smem, cudaStream_t st) {
-  if (allow_smem<k_rms_norm_grad_odd<T, NA>>(ODD_SMEM) != cudaSuccess) return 0;
+  if (allow_smem<k_rms_norm_grad_odd<T, NS>>(ODD_SMEM) != cudaSuccess) return 0;
   const int blocks = grad_blocks(a.rows, ODD_THREADS / 32);
-  k_rms_norm_grad_odd<T, NA><<<blocks, ODD_THREADS, smem, st>>>(a);
+  k_rms_norm_grad_odd<T, NS><<<blocks, ODD_THREADS, smem, st>>>(a);
   return blocks;
 }
 template <typename T>
@@ -912,13 +976,18 @@ int launch_grad_odd(const GradArgs& a, cudaStream_t st) {      // 0: not for the
   auto packed = [&](const void* p, long long ld) {
     return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld == a.cols || a.rows == 1));
   };
-  const int smem = std::max(ODD_THREADS / 32 * a.cols * (int)sizeof(T) * (a.g_s ? 3 : 2), a.cols * 4);
+  const int smem = 2 * ODD_THREADS / 32 * a.cols * (int)sizeof(T) * (a.g_s ? 3 : 2);      // (the final sums, 4 cols, fit too)
   if (a.cols > ODD_GRAD_COLS || smem > ODD_SMEM || !packed(a.g, a.ldg) || !packed(a.s, a.lds) || !packed(a.g_s, a.ldgs) ||
       !packed(a.g_x, a.ldgx))
     return 0;
-  if (a.cols <= 128) return launch_grad_odd3<T, 4>(a, smem, st);
-  if (a.cols <= 512) return launch_grad_odd3<T, 16>(a, smem, st);
-  return launch_grad_odd3<T, 32>(a, smem, st);
+  const int words = (a.cols / Word<T>::N + 31) / 32;                // of a lane
+  if (words <= 2) return launch_grad_odd3<T, 2>(a, smem, st);
+  if (words <= 4) return launch_grad_odd3<T, 4>(a, smem, st);
+  if (words <= 8) return launch_grad_odd3<T, 8>(a, smem, st);
+  if (words <= 12) return launch_grad_odd3<T, 12>(a, smem, st);
+  if (words <= 16) return launch_grad_odd3<T, 16>(a, smem, st);
+  if constexpr (Word<T>::N == 1) return launch_grad_odd3<T, 32>(a, smem, st);
+  return 0;
 }
 template <typename T>
 cudaError_t launch_grad(const GradArgs& a, int* blocks, cudaStream_t st) {          // *blocks: the rows of a.part
