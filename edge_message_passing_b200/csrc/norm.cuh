@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm(const Args p) {
 // (R cols sizeof(T) is), so a block moves R rows at once between memory and shared memory in 16-byte
 // vectors, and a warp takes whole rows there, a lane every 32nd element.  (Element-wise loads from memory
 // instead took 350 us for 80896 x 515 in bf16.)
-constexpr int ODD_THREADS = 256, ODD_SMEM = 110 * 1024;          // two blocks per SM at least
+constexpr int ODD_THREADS = 256, ODD_SMEM = 110 * 1024, SM_SMEM = 227 * 1024;   // two blocks per SM at least
 
 // `bytes` from src to dst, one of them in shared memory; both 16-byte aligned
 __device__ __forceinline__ void copy_rows(void* dst, const void* src, int bytes) {
@@ -181,9 +181,10 @@ __device__ __forceinline__ void copy_rows(void* dst, const void* src, int bytes)
 
 // In shared memory a warp reads a row by 32-bit words, two elements each of a 16-bit type: a row that begins inside a
 // word leaves out its first element, one that ends inside a word its last, and lane 0 takes that one by itself (for an
-// odd number of columns there is exactly one, for an even number none): 80896 x 515 in bf16 takes 46 us, 3.6 TB/s,
-// where it took 56 by elements; the time between a block's load and its store and instruction issue bound it.  Rows behind the last one are computed from whatever the shared memory
-// holds and not written.
+// odd number of columns there is exactly one, for an even number none): 80896 x 515 in bf16 took 56 us by elements
+// and takes 46, 3.6 TB/s, bound by instructions.  Persistent where shared memory has room for a second buffer, into which the
+// next rows are on their way (cp.async) meanwhile: with a residual 82 us without that, 74 (4.5 TB/s) with it.  Rows behind
+// the last one are computed from whatever the shared memory holds and not written.
 template <typename T> struct Word {                               // fp32: an element is a word
   static constexpr int N = 1;
   static __device__ __forceinline__ void get(uint32_t u, float (&v)[1]) { v[0] = __uint_as_float(u); }
@@ -210,124 +211,141 @@ __device__ __forceinline__ void copy_rows_async(void* dst, const void* src, int 
 }
 
 template <typename T, bool QUANT, bool RES, int RW>               // RW rows of a warp, side by side
-__global__ void __launch_bounds__(ODD_THREADS) k_rms_norm_odd(const Args p) {
+__global__ void __launch_bounds__(ODD_THREADS) k_rms_norm_odd(const Args p, int bufs) {
   extern __shared__ __align__(16) unsigned char odd_sm[];
   using Wd = Word<T>;
   constexpr int WARPS = ODD_THREADS / 32, R = RW * WARPS, N = Wd::N;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, C = p.cols / NCOMP;
-  const long long row0 = (long long)blockIdx.x * R;
-  const int rows = (int)min((long long)R, p.rows - row0), bytes = rows * p.cols * (int)sizeof(T);
-  const int area = round16(R * p.cols * (int)sizeof(T));
+  const int area = round16(R * p.cols * (int)sizeof(T)), half = RES ? 2 * area : area;
   float* wf = reinterpret_cast<float*>(odd_sm);                   // the weights, one per column
-  T* xs = reinterpret_cast<T*>(odd_sm + round16(4 * p.cols));
-  T* rs = RES ? reinterpret_cast<T*>(reinterpret_cast<unsigned char*>(xs) + area) : xs;
-  __nv_fp8_storage_t* qs = reinterpret_cast<__nv_fp8_storage_t*>(reinterpret_cast<unsigned char*>(rs) + area);
+  unsigned char* cur = odd_sm + round16(4 * p.cols);
+  unsigned char* other = cur + (bufs - 1) * half;
+  __nv_fp8_storage_t* qs = reinterpret_cast<__nv_fp8_storage_t*>(cur + bufs * half);
   const T* w = static_cast<const T*>(p.w);
-  copy_rows(xs, static_cast<const T*>(p.x) + row0 * p.cols, bytes);
-  if (RES) copy_rows(rs, static_cast<const T*>(p.residual) + row0 * p.cols, bytes);
+  const long long groups = (p.rows + R - 1) / R;
+  auto rows_of = [&](long long b) { return (int)min((long long)R, p.rows - b * R); };
+  auto fetch = [&](long long b, unsigned char* to) {
+    const long long at = b * R * p.cols;
+    const int bytes = rows_of(b) * p.cols * (int)sizeof(T);
+    copy_rows_async(to, static_cast<const T*>(p.x) + at, bytes);
+    if (RES) copy_rows_async(to + area, static_cast<const T*>(p.residual) + at, bytes);
+  };
+  fetch(blockIdx.x, cur);
   for (int c = threadIdx.x; c < p.cols; c += ODD_THREADS) wf[c] = w ? to_f(w[weight_at(c, C, p.degrees)]) : 1.f;
-  __syncthreads();
   const int first = warp * RW, n = p.cols / N;
-  const uint32_t *xw[RW], *rw[RW];                                // the row's first whole word
-  int head[RW];                                                   // and its column
-#pragma unroll
-  for (int j = 0; j < RW; ++j) {
-    const int start = (first + j) * p.cols;
-    head[j] = N == 2 ? start & 1 : 0;
-    xw[j] = reinterpret_cast<const uint32_t*>(xs + start + head[j]);
-    rw[j] = reinterpret_cast<const uint32_t*>(rs + start + head[j]);
-  }
   const bool loose = N == 2 && (p.cols & 1) && lane == 0;         // this lane takes the row's loose element
-  float ss[RW], top[RW];
+  for (long long b = blockIdx.x; b < groups; b += gridDim.x) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();                                                // cur has landed, other's rows have been copied out
+    if (b + gridDim.x < groups) fetch(b + gridDim.x, other);        // (with one buffer there is no second turn)
+    const long long row0 = b * R;
+    const int rows = rows_of(b), bytes = rows * p.cols * (int)sizeof(T);
+    T* xs = reinterpret_cast<T*>(cur);
+    T* rs = reinterpret_cast<T*>(RES ? cur + area : cur);
+    const uint32_t *xw[RW], *rw[RW];                                // the row's first whole word
+    int head[RW];                                                   // and its column
 #pragma unroll
-  for (int j = 0; j < RW; ++j) {
-    ss[j] = top[j] = 0.f;
-    if (loose) {
+    for (int j = 0; j < RW; ++j) {
+      const int start = (first + j) * p.cols;
+      head[j] = N == 2 ? start & 1 : 0;
+      xw[j] = reinterpret_cast<const uint32_t*>(xs + start + head[j]);
+      rw[j] = reinterpret_cast<const uint32_t*>(rs + start + head[j]);
+    }
+    float ss[RW], top[RW];
+#pragma unroll
+    for (int j = 0; j < RW; ++j) {
+      ss[j] = top[j] = 0.f;
+      if (loose) {
+        const int c = head[j] ? 0 : p.cols - 1, i = (first + j) * p.cols + c;
+        float v = to_f(xs[i]);
+        if (RES) v += to_f(rs[i]);
+        ss[j] = v * v;
+        if (QUANT) top[j] = max_abs(0.f, v * wf[c]);
+      }
+    }
+#pragma unroll 4
+    for (int k = lane; k < n; k += 32) {
+#pragma unroll
+      for (int j = 0; j < RW; ++j) {
+        float v[N], r[N];
+        Wd::get(xw[j][k], v);
+        if (RES) Wd::get(rw[j][k], r);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          if (RES) v[e] += r[e];
+          ss[j] = fmaf(v[e], v[e], ss[j]);
+          if (QUANT) top[j] = max_abs(top[j], v[e] * wf[head[j] + k * N + e]);
+        }
+      }
+    }
+    float rstd[RW], inv[RW];
+#pragma unroll
+    for (int j = 0; j < RW; ++j) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        ss[j] += __shfl_xor_sync(0xffffffffu, ss[j], o);
+        if (QUANT) top[j] = max_abs(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+      }
+      rstd[j] = rsqrtf(ss[j] / (float)p.cols + p.eps);
+      inv[j] = 1.f;
+      if (QUANT) {
+        const float m = top[j] * rstd[j];
+        const float scale = m < TINY ? 1.f : m / 448.f;
+        inv[j] = 1.f / scale;
+        if (lane == 0 && first + j < rows) p.scale[row0 + first + j] = scale;
+      }
+    }
+#pragma unroll 4
+    for (int k = lane; k < n; k += 32) {
+#pragma unroll
+      for (int j = 0; j < RW; ++j) {
+        float v[N], r[N];
+        Wd::get(xw[j][k], v);
+        if (RES) {
+          Wd::get(rw[j][k], r);
+#pragma unroll
+          for (int e = 0; e < N; ++e) v[e] += r[e];
+          const_cast<uint32_t*>(rw[j])[k] = Wd::put(v);             // s
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          v[e] = v[e] * rstd[j] * wf[head[j] + k * N + e];
+          if (QUANT) v[e] *= inv[j];
+        }
+        if (!QUANT) const_cast<uint32_t*>(xw[j])[k] = Wd::put(v);
+        else
+#pragma unroll
+          for (int e = 0; e < N; ++e) store_e4m3<1>(qs + (first + j) * p.cols + head[j] + k * N + e, {v[e]});
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < RW; ++j) {
+      if (!loose) continue;
       const int c = head[j] ? 0 : p.cols - 1, i = (first + j) * p.cols + c;
       float v = to_f(xs[i]);
-      if (RES) v += to_f(rs[i]);
-      ss[j] = v * v;
-      if (QUANT) top[j] = max_abs(0.f, v * wf[c]);
-    }
-  }
-#pragma unroll 4
-  for (int k = lane; k < n; k += 32) {
-#pragma unroll
-    for (int j = 0; j < RW; ++j) {
-      float v[N], r[N];
-      Wd::get(xw[j][k], v);
-      if (RES) Wd::get(rw[j][k], r);
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        if (RES) v[e] += r[e];
-        ss[j] = fmaf(v[e], v[e], ss[j]);
-        if (QUANT) top[j] = max_abs(top[j], v[e] * wf[head[j] + k * N + e]);
-      }
-    }
-  }
-  float rstd[RW], inv[RW];
-#pragma unroll
-  for (int j = 0; j < RW; ++j) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      ss[j] += __shfl_xor_sync(0xffffffffu, ss[j], o);
-      if (QUANT) top[j] = max_abs(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
-    }
-    rstd[j] = rsqrtf(ss[j] / (float)p.cols + p.eps);
-    inv[j] = 1.f;
-    if (QUANT) {
-      const float m = top[j] * rstd[j];
-      const float scale = m < TINY ? 1.f : m / 448.f;
-      inv[j] = 1.f / scale;
-      if (lane == 0 && first + j < rows) p.scale[row0 + first + j] = scale;
-    }
-  }
-#pragma unroll 4
-  for (int k = lane; k < n; k += 32) {
-#pragma unroll
-    for (int j = 0; j < RW; ++j) {
-      float v[N], r[N];
-      Wd::get(xw[j][k], v);
       if (RES) {
-        Wd::get(rw[j][k], r);
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[e] += r[e];
-        const_cast<uint32_t*>(rw[j])[k] = Wd::put(v);             // s
+        v += to_f(rs[i]);
+        rs[i] = from_f<T>(v);
       }
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        v[e] = v[e] * rstd[j] * wf[head[j] + k * N + e];
-        if (QUANT) v[e] *= inv[j];
-      }
-      if (!QUANT) const_cast<uint32_t*>(xw[j])[k] = Wd::put(v);
-      else
-#pragma unroll
-        for (int e = 0; e < N; ++e) store_e4m3<1>(qs + (first + j) * p.cols + head[j] + k * N + e, {v[e]});
+      v = v * rstd[j] * wf[c];
+      if (QUANT) store_e4m3<1>(qs + i, {v * inv[j]});
+      else xs[i] = from_f<T>(v);
     }
+    __syncthreads();
+    if (QUANT) copy_rows(static_cast<__nv_fp8_storage_t*>(p.y) + row0 * p.cols, qs, rows * p.cols);
+    else copy_rows(static_cast<T*>(p.y) + row0 * p.cols, xs, bytes);
+    if (RES && p.s) copy_rows(static_cast<T*>(p.s) + row0 * p.cols, rs, bytes);
+    unsigned char* t = cur;
+    cur = other;
+    other = t;
   }
-#pragma unroll
-  for (int j = 0; j < RW; ++j) {
-    if (!loose) continue;
-    const int c = head[j] ? 0 : p.cols - 1, i = (first + j) * p.cols + c;
-    float v = to_f(xs[i]);
-    if (RES) {
-      v += to_f(rs[i]);
-      rs[i] = from_f<T>(v);
-    }
-    v = v * rstd[j] * wf[c];
-    if (QUANT) store_e4m3<1>(qs + i, {v * inv[j]});
-    else xs[i] = from_f<T>(v);
-  }
-  __syncthreads();
-  if (QUANT) copy_rows(static_cast<__nv_fp8_storage_t*>(p.y) + row0 * p.cols, qs, rows * p.cols);
-  else copy_rows(static_cast<T*>(p.y) + row0 * p.cols, xs, bytes);
-  if (RES && p.s) copy_rows(static_cast<T*>(p.s) + row0 * p.cols, rs, bytes);
 }
 
 // The gradient of the same rows: persistent, a row per warp at a time, read by words in the same way.  Whether a row begins
 // inside a word depends on the warp alone, so a lane's columns are the same in every row of its, and its part of g_w
 // stays in registers (NS words, and the loose column of lane 0).  The next rows are on their way (cp.async) into the
-// other half of the shared memory meanwhile.
+// other half of the shared memory meanwhile: 80896 x 515 in bf16 104 us, 2.4 TB/s, bound by instructions (198 by elements and
+// without it).
 constexpr int ODD_GRAD_COLS = 1024;
 template <typename T, int NS>
 __global__ void __launch_bounds__(ODD_THREADS) k_rms_norm_grad_odd(const GradArgs p) {
@@ -915,15 +933,22 @@ cudaError_t launch_fwd_staged(const Args& a, cudaStream_t st) {
   return launch_staged<k_rms_norm_staged<T, QUANT, 32>>(a, h, blocks, st);
 }
 template <typename T, bool QUANT, bool RES, int RW>
-bool launch_odd4(const Args& a, int smem, cudaStream_t st) {
+bool launch_odd4(const Args& a, int rows_smem, int smem, cudaStream_t st) {
   if (allow_smem<k_rms_norm_odd<T, QUANT, RES, RW>>(ODD_SMEM) != cudaSuccess) return false;
-  const int R = RW * ODD_THREADS / 32;
-  k_rms_norm_odd<T, QUANT, RES, RW><<<(unsigned)((a.rows + R - 1) / R), ODD_THREADS, smem, st>>>(a);
+  const long long groups = (a.rows + RW * ODD_THREADS / 32 - 1) / (RW * ODD_THREADS / 32);
+  // persistent where two buffers of rows fit, else a block per group of rows
+  const int bufs = smem + rows_smem <= ODD_SMEM ? 2 : 1;
+  if (bufs == 2) smem += rows_smem;
+  const long long grid = bufs == 2 ? std::min<long long>(groups, (long long)tc::num_sms() * std::min(8, SM_SMEM / (smem + 1024))) : groups;
+  k_rms_norm_odd<T, QUANT, RES, RW><<<(unsigned)grid, ODD_THREADS, smem, st>>>(a, bufs);
   return true;
 }
 template <typename T, bool QUANT, int RW>
-bool launch_odd3(const Args& a, int smem, cudaStream_t st) {
-  return a.residual ? launch_odd4<T, QUANT, true, RW>(a, smem, st) : launch_odd4<T, QUANT, false, RW>(a, smem, st);
+bool launch_odd3(const Args& a, cudaStream_t st) {
+  const int rows_smem = round16(RW * ODD_THREADS / 32 * a.cols * (int)sizeof(T)) * (a.residual ? 2 : 1);
+  const int smem = round16(4 * a.cols) + rows_smem + (QUANT ? RW * ODD_THREADS / 32 * a.cols : 0);
+  if (smem > ODD_SMEM) return false;
+  return a.residual ? launch_odd4<T, QUANT, true, RW>(a, rows_smem, smem, st) : launch_odd4<T, QUANT, false, RW>(a, rows_smem, smem, st);
 }
 inline bool packed_rows(const void* p, long long ld, const Args& a) {       // contiguous, on a 16-byte boundary
   return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld == a.cols || a.rows == 1));
@@ -933,13 +958,10 @@ bool launch_odd(const Args& a, bool quant, cudaStream_t st) {
   if (!packed_rows(a.x, a.ldx, a) || !packed_rows(a.residual, a.ldr, a) || !packed_rows(a.y, a.ldy, a) ||
       !packed_rows(a.s, a.lds, a) || (a.s && !a.residual))
     return false;
-  const int row = a.cols * (int)sizeof(T) * (a.residual ? 2 : 1) + (quant ? a.cols : 0);
-  const int per = ODD_THREADS / 32;                                // 8 rows, or 16 (which 8-bit rows need for 16 bytes)
-  const int s16 = 2 * per * row + 4 * a.cols + 64, s8 = per * row + 4 * a.cols + 64;
-  // two rows a warp where that leaves four blocks on an SM
-  if (s16 <= (quant ? ODD_SMEM : 56 * 1024) && (quant || a.rows > 2 * per * 148)) return quant ? launch_odd3<T, true, 2>(a, s16, st) : launch_odd3<T, false, 2>(a, s16, st);
-  if (!quant && s8 <= ODD_SMEM) return launch_odd3<T, false, 1>(a, s8, st);
-  return false;
+  if (quant) return launch_odd3<T, true, 2>(a, st);                 // 16 rows of 8 bits are whole 16 bytes
+  // two rows a warp where there are enough of them for every SM, else (or where they do not fit) one
+  const bool many = a.rows > 2 * ODD_THREADS / 32 * tc::num_sms();
+  return (many && launch_odd3<T, false, 2>(a, st)) || launch_odd3<T, false, 1>(a, st);
 }
 
 template <typename T>

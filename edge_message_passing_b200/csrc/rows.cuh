@@ -121,7 +121,7 @@ __device__ __forceinline__ int degree_of(int lm) { return (lm > 0) + (lm > 3) + 
 // SiLU z / (1 + exp(-z)) and GELU z Phi(z), and their derivatives, with e^x = 2^(x log2 e) by the special-function
 // unit's 2^x and 1/x, both with results below 2^-126 as zero: __expf and __fdividef, which keep those, take 14
 // instructions an element of SiLU instead of 5, and instructions bound a short-k epilogue (647168 x 64 -> 512 in FP32:
-// 401 us so, AFTER).  -inf and NaN give NaN.  Phi, the normal distribution function, is 1/2 erfc(-z / sqrt 2) with the rational
+// 401 us so, 340 thus).  -inf and NaN give NaN.  Phi, the normal distribution function, is 1/2 erfc(-z / sqrt 2) with the rational
 // approximation 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical Functions (1964): erfc(x) = t (a1 + t (a2 + ...))
 // exp(-x^2), t = 1 / (1 + p x), within 1.5e-7 for x >= 0; erff costs more than twice as much.  With the FP32 arithmetic
 // the error of GELU is about 2e-7 |z|.

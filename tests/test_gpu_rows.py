@@ -665,3 +665,44 @@ def test_a_weight_gradient_over_many_rows(type):
     ref = g.double().t() @ x.double()
     assert ((g_w.double() - ref).norm() / ref.norm()).item() <= (2.0 ** -17 if t == torch.float32 else half_step(t))
     assert ((g_b.double() - g.double().sum(0)).norm() / g.double().sum(0).norm()).item() <= (2.0 ** -17 if t == torch.float32 else half_step(t))
+
+
+@pytest.mark.parametrize("type", list(TYPES))
+@pytest.mark.parametrize("rows,cols", [(1, 3), (2, 1023), (15, 66), (33, 515), (2401, 65), (20003, 34), (9999, 129), (700, 2047)])
+def test_norm_of_contiguous_rows_off_16_bytes(rows, cols, type):
+    """Rows that begin and end inside a 16-byte vector or a 32-bit word, with and without a residual, weights and 8-bit
+    values, forward and back; what lies behind the last row stays.  Tolerances as in the tests above."""
+    t, rng = TYPES[type], np.random.default_rng(rows * 31 + cols)
+    x, r, g = (dev(normal(rng, rows, cols), t) for _ in range(3))
+    w = dev(1 + 0.3 * normal(rng, cols), t)
+    for res in (None, r):
+        for weight in (None, w):
+            ry, rs = orow.rms_norm(host(x), host(weight), host(res), EPS)
+            y, s = emp.mp_rms_norm(x, weight, residual=res, eps=EPS)
+            near(y, ry, (half_step(t) + 32 * U) * np.abs(ry) + floor_of(t), "y")
+            near(s, rs, (half_step(t) + U) * np.abs(rs) + floor_of(t), "s")
+            q, scale, s2 = emp.mp_rms_norm(x, weight, residual=res, eps=EPS, quantize=True)
+            rscale = orow.scale_of(ry)
+            near(scale, rscale, 40 * U * rscale, "scale")
+            value = host(q) * host(scale)[:, None]
+            assert torch.equal(s, s2)
+            assert np.all(np.abs(value - ry) <= np.maximum(2.0 ** -4 * np.abs(ry), 2.0 ** -10 * rscale[:, None]) + 64 * U * np.abs(ry))
+    S, G, W = host(x), host(g), host(w)
+    rstd = 1 / np.sqrt((S * S).mean(1, keepdims=True) + EPS)
+    n, h = S * rstd, G * W
+    for through in (None, r):
+        g_x, g_w = emp.mp_rms_norm_grad(g, x, w, g_s=through, eps=EPS)
+        rx, rw = orow.rms_norm_grad(G, S, W, host(through), EPS)
+        size = rstd * (np.abs(h) + np.abs(n) * np.abs(h * n).mean(1, keepdims=True)) + (0 if through is None else np.abs(host(through)))
+        near(g_x, rx, half_step(t) * np.abs(rx) + 64 * U * size + floor_of(t), "g_x")
+        near(g_w, rw, half_step(t) * np.abs(rw) + (rows / 592 + 400) * U * np.abs(G * n).sum(0) + floor_of(t), "g_w")
+    # the library writes rows it was given and nothing behind them
+    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}[t]
+    for y_code, y_type in ((code, t), (3, torch.uint8)):
+        y = torch.full(((rows + 2) * cols,), 7, dtype=y_type, device="cuda")
+        sums = torch.full(((rows + 2) * cols,), 7, dtype=t, device="cuda")
+        scale = torch.full((rows + 1,), 7.0, device="cuda")
+        a = emp.RmsNormC(rows, cols, code, y_code, 0, EPS, x.data_ptr(), cols, r.data_ptr(), cols, w.data_ptr(), y.data_ptr(), cols,
+                         scale.data_ptr() if y_code == 3 else None, sums.data_ptr(), cols)
+        assert emp.lib().mp_rms_norm(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.all(y[rows * cols:].float() == 7) and torch.all(sums[rows * cols:].float() == 7) and scale[rows] == 7
