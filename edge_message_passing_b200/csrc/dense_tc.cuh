@@ -8,12 +8,13 @@
 // Persistent kernel, one CTA per SM, 128 x bn tiles (bn a multiple of 32, up to 256 or in FP32 128) taken round-robin with n
 // fastest, so that neighbouring CTAs share an A tile in L2.  A long k axis with few tiles is split:
 // each split leaves a partial product, and k_join adds them in order.  Warps: one issues TMA loads, one
-// the MMAs, eight drain the accumulators (two per TMEM lane quarter, every other 32 columns each) and
-// write the rows.
+// the MMAs, 8 or 16 drain the accumulators (two or four per TMEM lane quarter) and write the rows.
 //
 // bf16, fp16 and e4m3 operands go from TMA straight to the MMA: a ring of stages of 128 bytes of k
 // (128-byte swizzle), two accumulators of bn columns, so the epilogue of a tile overlaps the next
-// tile's products.
+// tile's products.  Bound by shared memory, which takes every operand byte in and gives it out once: 16384 x 2048 -> 2048 in bf16
+// 98 us, 1400 TFLOP/s (85 % of the measured rate; the tensor pipe is active 70 % of the time); 65536 x 2048 -> 512 in e4m3 with SiLU
+// and residual 77 us, 1790 TFLOP/s, with half of its time per tile in the epilogue's exchange with memory.
 //
 // FP32 operands are split a = hi + lo (hi = RN_tf32(a), lo = RN_tf32(a - hi)) inside the kernel, by two
 // groups of four warps that take the 32-wide k stages in turn, so neither operand needs a pass of its
@@ -22,7 +23,15 @@
 // FP32 accumulator by truncation, which shrinks a sum by about 2e-8 of itself per MMA (measured on the
 // SO(2) products: 7e-9 K).  So an accumulator takes K_CHUNK = 96 of k only and is then added, rounded
 // to nearest, to sums in the epilogue warps' registers, and within each stage the small products
-// lo.hi and hi.lo come before hi.hi.
+// lo.hi and hi.lo come before hi.hi.  Bound by the split (16 instructions per 4 elements and lane) and the epilogue's
+// additions: 161792 x 512 -> 512 takes 408 us, 208 TFLOP/s of products (two thirds of what three TF32 products
+// allow).
+//
+// FP32 with k of one chunk (SHORT) needs no sums in registers.  A CTA stays on one column of tiles, so that B is split
+// once and kept, and the two halves of the epilogue's warps take every other tile each: a warp's way through a
+// tile is latency (TMEM, staging, the store's read) as much as instructions (647168 x 64 -> 512 with SiLU 340 us
+// with all warps on each tile, 322 us, 4.6 TB/s, thus; 16-bit operands, whose epilogue overlaps more stages, gain nothing
+// and 8-bit ones lose: 77 and 87 us at 65536 x 2048 -> 512).  Bound by the instructions of split and epilogue together.
 //
 // Every mbarrier wait is bounded; the producer waits out its own copies before exit.
 #pragma once
@@ -53,7 +62,7 @@ template <Path PATH, typename T, bool ROWS, bool SCALED>
 struct Cfg {
   static constexpr bool FP32 = PATH != DIRECT;
   static constexpr int EPI = PATH == SHORT || (ROWS && !SCALED) ? 16 : 8;
-  static constexpr int SETS = PATH == SHORT ? 2 : 1;
+  static constexpr int SETS = PATH == SHORT ? 2 : 1;    // of epilogue warps, which take the tiles in turn
   static constexpr int W = PATH == SPLIT && ROWS ? 16 : 32;                   // columns put out at once (staging)
   static constexpr int LAND = 3, SLOTS = 3;             // FP32: stages as they land (A and B; A alone in SHORT) and split
   static constexpr int LAND_BYTES = PATH == SHORT ? A_BYTES : 2 * A_BYTES;

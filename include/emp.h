@@ -277,7 +277,11 @@ int mp_radial_chain(const void* chain, int64_t E, const float* x, float* kc, flo
  * channels of node features [N][16][C] are rows of C with pitch 16 C.  A row's elements are
  * contiguous.  Pointers need the alignment of their element; 16-byte aligned pointers and
  * pitches that are multiples of 16 bytes run faster.  Nothing behind the last row or the last
- * column is read or written.  Zero rows are allowed (no launch; row pointers may then be NULL). */
+ * column is written, and what lies there has no effect.  Outputs overlap no input and no other output.
+ * Zero rows are allowed (no launch; row pointers may then be NULL).  A workspace is 256-byte aligned (else
+ * EMP_ERR_ARG; too small a one, or none where one is needed, is EMP_ERR_WORKSPACE and launches nothing) and belongs to the
+ * call until its work is done: calls that may overlap, captured graphs among them, need one each.  The first call of a kind on
+ * a device loads its kernel; make it before a stream capture. */
 typedef enum {
   EMP_F32 = 0,
   EMP_BF16 = 1,
@@ -362,9 +366,11 @@ typedef struct {
 } emp_dense;
 
 /* Dense layer on rows:  z = x W^T + bias,  y = activation(z) + residual.
- * FP32 inputs keep FP32 accuracy; 16-bit and 8-bit inputs are multiplied as they are and summed in FP32; y and
- * z are rounded once, at the end.  An infinite or NaN input makes outputs of its row (of x) or
- * column (of weight) NaN or infinite, and no others.  Errors: EMP_ERR_ARG, EMP_ERR_UNSUPPORTED,
+ * FP32 inputs keep FP32 accuracy (above 16 rows an input of magnitude over 3.4e38 counts as infinite, and an infinite one
+ * gives NaN); 16-bit and 8-bit inputs are multiplied as they are and summed in FP32, where the tensor cores' truncation may
+ * shrink a sum by 8e-5 of itself over the longest k and by 2e-8 over the shortest; y and z are rounded once, at the end.
+ * An infinite or NaN input makes outputs of its row (of x) or column (of weight) NaN or infinite, and no others; through
+ * an activation z = -inf gives NaN.  Errors: EMP_ERR_ARG, EMP_ERR_UNSUPPORTED,
  * EMP_ERR_WORKSPACE (ws_bytes below mp_dense_workspace_bytes(a); 0 for many shapes). */
 size_t mp_dense_workspace_bytes(const emp_dense* a);
 int mp_dense(const emp_dense* a, void* ws, size_t ws_bytes, cudaStream_t stream);
