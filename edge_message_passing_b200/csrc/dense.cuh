@@ -36,7 +36,7 @@ __device__ __forceinline__ void put_one(const Epi& e, long long m, int n, float 
 // ------------------------------------------------------------------ few rows
 // Up to 16 rows of a short k and a small W: the product reads W once per 8 rows and little else, so it runs on SIMT with
 // a warp on FEW_COLS columns of the output and up to 8 rows at a time (x in shared memory as floats, K_PART of
-// k at once; a lane takes V elements of k, 32 V apart), in FP32 throughout.  Against the tensor-core kernel, whose
+// k at once; a lane takes V elements of k, 32 V apart, and where V is 1 eight of those at a time, for as many loads in flight), in FP32 throughout.  Against the tensor-core kernel, whose
 // set-up costs more: 8 rows, 256 -> 1024, FP32: 9.4 and 15.8 us; 2048 -> 2048: 20.6 and 25.0 (bf16 16.8 and 17.0); beyond,
 // W's reads and a warp's long k lose: 16 rows, 2048 -> 2048 bf16 20.9 and 17.0, 8 rows, 8192 -> 128 51.7 and 20.2.
 constexpr int FEW_COLS = 2, FEW_WARPS = 4, FEW_M = 8, K_PART = 1024;
@@ -60,40 +60,76 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) k_dense_few(const Few p, const
   const bool mine = lane < FEW_COLS * FEW_M && m < p.M && n < p.N;
   EpiIn in{};
   if (mine) in = epi_in(e, m, n);
-  float w[FEW_COLS][V];
+  constexpr int B = V == 1 ? 8 : 1, STEP = 32 * V * B;            // B groups of V elements, 32 V apart
+  using U = typename Bits<T>::U;
+  U wu[FEW_COLS][B];                                              // V = 1
+  float w[FEW_COLS][B][V];
   auto load_w = [&](int k) {
 #pragma unroll
-    for (int c = 0; c < FEW_COLS; ++c) {
+    for (int c = 0; c < FEW_COLS; ++c)
 #pragma unroll
-      for (int j = 0; j < V; ++j) w[c][j] = 0.f;
-      if (n0 + c < p.N && k < p.K) load_v<T, V>(static_cast<const T*>(p.w) + (n0 + c) * p.ldw + k, w[c]);
-    }
+      for (int b = 0; b < B; ++b) {
+        const T* at = static_cast<const T*>(p.w) + (n0 + c) * p.ldw + k + 32 * V * b;
+        const bool in = n0 + c < p.N && k + 32 * V * b < p.K;
+        if constexpr (V == 1) {
+          wu[c][b] = U(0);
+          if (in) wu[c][b] = *reinterpret_cast<const U*>(at);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) w[c][b][j] = 0.f;
+          if (in) load_v<T, V>(at, w[c][b]);
+        }
+      }
   };
   load_w(lane * V);
   float acc[FEW_COLS][FEW_M] = {};
   for (int k0 = 0; k0 < p.K; k0 += K_PART) {
-    const int kn = min(K_PART, p.K - k0), kq = kn / V;          // V divides K (or is 1)
+    const int kn = min(K_PART, p.K - k0), kz = (kn + STEP - 1) / STEP * STEP;     // V divides K (or is 1)
     if (k0) __syncthreads();
-    for (int i = threadIdx.x; i < FEW_M * kq; i += 32 * FEW_WARPS) {
-      const int r = i / kq, k = (i - r * kq) * V;
-      float v[V];
+    for (int r = warp; r < FEW_M; r += FEW_WARPS) {
+      const T* x = static_cast<const T*>(p.x) + (m0 + r) * p.ldx + k0;
+      if constexpr (V == 1) {
+        for (int k1 = lane; k1 < kz; k1 += STEP) {                // zeros behind the last of k
+          U u[B];
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[j] = 0.f;
-      if (m0 + r < p.M) load_v<T, V>(static_cast<const T*>(p.x) + (m0 + r) * p.ldx + k0 + k, v);
+          for (int b = 0; b < B; ++b) {
+            u[b] = U(0);
+            if (m0 + r < p.M && k1 + 32 * b < kn) u[b] = reinterpret_cast<const U*>(x)[k1 + 32 * b];
+          }
 #pragma unroll
-      for (int j = 0; j < V; ++j) xs[r][k + j] = v[j];
+          for (int b = 0; b < B; ++b) xs[r][k1 + 32 * b] = bits_to_f(u[b], T());
+        }
+      } else {
+#pragma unroll 8
+        for (int k = lane * V; k < kn; k += 32 * V) {
+          float v[V];
+#pragma unroll
+          for (int j = 0; j < V; ++j) v[j] = 0.f;
+          if (m0 + r < p.M) load_v<T, V>(x + k, v);
+#pragma unroll
+          for (int j = 0; j < V; ++j) xs[r][k + j] = v[j];
+        }
+      }
     }
     __syncthreads();
-    for (int k = lane * V; k < kn; k += 32 * V) {
+    for (int k = lane * V; k < kn; k += STEP) {
+      if constexpr (V == 1) {
+#pragma unroll
+        for (int c = 0; c < FEW_COLS; ++c)
+#pragma unroll
+          for (int b = 0; b < B; ++b) w[c][b][0] = bits_to_f(wu[c][b], T());
+      }
 #pragma unroll
       for (int r = 0; r < FEW_M; ++r)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float x = xs[r][k + j];
+        for (int b = 0; b < B; ++b)
 #pragma unroll
-          for (int c = 0; c < FEW_COLS; ++c) acc[c][r] += w[c][j] * x;
-        }
-      load_w(k0 + k + 32 * V < k0 + kn ? k0 + k + 32 * V : k0 + K_PART + lane * V);       // the next of this part, or of the next part
+          for (int j = 0; j < V; ++j) {
+            const float x = xs[r][k + 32 * V * b + j];
+#pragma unroll
+            for (int c = 0; c < FEW_COLS; ++c) acc[c][r] += w[c][b][j] * x;
+          }
+      load_w(k0 + k + STEP < k0 + kn ? k0 + k + STEP : k0 + K_PART + lane * V);           // the next of this part, or of the next part
     }
   }
   float sum = 0.f;

@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+#include <type_traits>
 #include "emp_common.cuh"
 
 namespace emp {
@@ -38,6 +39,16 @@ template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, fl
 template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// an element as it is in memory, so that many loads can be on their way before the first conversion
+template <typename T> struct Bits { using U = std::conditional_t<sizeof(T) == 4, float, std::conditional_t<sizeof(T) == 2, unsigned short, unsigned char>>; };
+__device__ __forceinline__ float bits_to_f(float u, float) { return u; }
+__device__ __forceinline__ float bits_to_f(unsigned short u, __nv_bfloat16) { return __uint_as_float((uint32_t)u << 16); }
+__device__ __forceinline__ float bits_to_f(unsigned short u, __half) { return __half2float(__ushort_as_half(u)); }
+__device__ __forceinline__ float bits_to_f(unsigned char u, __nv_fp8_e4m3) {
+  __nv_fp8_e4m3 e;
+  e.__x = u;
+  return (float)e;
 }
 // 16 bytes as floats: four of fp32 or eight of a 16-bit type
 template <typename T, int V>
