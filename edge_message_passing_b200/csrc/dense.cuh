@@ -61,8 +61,7 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) k_dense_few(const Few p, const
   EpiIn in{};
   if (mine) in = epi_in(e, m, n);
   constexpr int B = V == 1 ? 8 : 1, STEP = 32 * V * B;            // B groups of V elements, 32 V apart
-  using U = typename Bits<T>::U;
-  U wu[FEW_COLS][B];                                              // V = 1
+  Raw<T, 1> wu[FEW_COLS][B];                                      // V = 1
   float w[FEW_COLS][B][V];
   auto load_w = [&](int k) {
 #pragma unroll
@@ -72,8 +71,7 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) k_dense_few(const Few p, const
         const T* at = static_cast<const T*>(p.w) + (n0 + c) * p.ldw + k + 32 * V * b;
         const bool in = n0 + c < p.N && k + 32 * V * b < p.K;
         if constexpr (V == 1) {
-          wu[c][b] = U(0);
-          if (in) wu[c][b] = *reinterpret_cast<const U*>(at);
+          wu[c][b].load(at, in);
         } else {
 #pragma unroll
           for (int j = 0; j < V; ++j) w[c][b][j] = 0.f;
@@ -90,14 +88,11 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) k_dense_few(const Few p, const
       const T* x = static_cast<const T*>(p.x) + (m0 + r) * p.ldx + k0;
       if constexpr (V == 1) {
         for (int k1 = lane; k1 < kz; k1 += STEP) {                // zeros behind the last of k
-          U u[B];
+          Raw<T, 1> u[B];
 #pragma unroll
-          for (int b = 0; b < B; ++b) {
-            u[b] = U(0);
-            if (m0 + r < p.M && k1 + 32 * b < kn) u[b] = reinterpret_cast<const U*>(x)[k1 + 32 * b];
-          }
+          for (int b = 0; b < B; ++b) u[b].load(x + k1 + 32 * b, m0 + r < p.M && k1 + 32 * b < kn);
 #pragma unroll
-          for (int b = 0; b < B; ++b) xs[r][k1 + 32 * b] = bits_to_f(u[b], T());
+          for (int b = 0; b < B; ++b) xs[r][k1 + 32 * b] = u[b].one(T());
         }
       } else {
 #pragma unroll 8
@@ -117,7 +112,7 @@ __global__ void __launch_bounds__(32 * FEW_WARPS) k_dense_few(const Few p, const
 #pragma unroll
         for (int c = 0; c < FEW_COLS; ++c)
 #pragma unroll
-          for (int b = 0; b < B; ++b) w[c][b][0] = bits_to_f(wu[c][b], T());
+          for (int b = 0; b < B; ++b) w[c][b][0] = wu[c][b].one(T());
       }
 #pragma unroll
       for (int r = 0; r < FEW_M; ++r)
@@ -230,9 +225,11 @@ __global__ void __launch_bounds__(256) k_join(long long M, int N, int splits, co
 // gz = g act'(z), rounded to the operands' type (it is an operand of both products, which take that
 // type), and part[block][n] = the block's column sums of the unrounded values (bias gradient).
 // A warp takes 32 V neighbouring columns of every 8 gridDim.x-th row, a few rows' loads at a time.
-// Bound by HBM: g and z in, gz out (80896 x 512 in FP32: 80 us, 6.2 TB/s).
-// Four blocks per SM: with 16-bit vectors one row at a time (34 us at 16384 x 1024 with two rows and three blocks, 29 so),
-// else two (102 us at 80896 x 512 in FP32 with four rows and two blocks, 86 so).
+// Bound by HBM: g and z in, gz out (80896 x 512: FP32 80 us, 6.2 TB/s; bf16 43 us, 5.8 TB/s), at widths off 16 bytes by the
+// instructions of its narrow loads (80896 x 515: FP32 90 us, bf16 104 us; 514 in bf16, by words, 59).
+// Four blocks per SM, and as many rows in flight as their registers hold: two of 16-byte vectors (bf16 one 52 us, two 47,
+// four 47), four of 32-bit words, eight single floats (four 107 us at 80896 x 515, eight 94) or four single 16-bit
+// elements (two 134 us, four 108, eight 122).
 constexpr int GZ_WARPS = 8, GZ_PER_SM = 4;
 struct GzArgs {
   long long rows;
@@ -245,7 +242,7 @@ struct GzArgs {
 };
 template <typename T, int V>
 __global__ void __launch_bounds__(32 * GZ_WARPS, GZ_PER_SM) k_dense_gz(const GzArgs p) {
-  constexpr int GZ_BATCH = V == 8 ? 1 : V == 4 ? 2 : V == 2 ? 4 : 8;
+  constexpr int GZ_BATCH = V >= 4 ? 2 : V == 2 || sizeof(T) == 2 ? 4 : 8;
   __shared__ float sm[GZ_WARPS][32 * V];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c = (blockIdx.y * 32 + lane) * V;
@@ -253,37 +250,39 @@ __global__ void __launch_bounds__(32 * GZ_WARPS, GZ_PER_SM) k_dense_gz(const GzA
 #pragma unroll
   for (int i = 0; i < V; ++i) s[i] = 0.f;
   if (c < p.cols) {
-    const T* g = static_cast<const T*>(p.g) + c;
-    const T* z = static_cast<const T*>(p.z) + c;
-    T* o = static_cast<T*>(p.gz) + c;
-    const long long step = (long long)gridDim.x * GZ_WARPS;
-    for (long long m0 = (long long)blockIdx.x * GZ_WARPS + w; m0 < p.rows; m0 += GZ_BATCH * step) {
-      float a[GZ_BATCH][V], b[GZ_BATCH][V];
+    const int step = gridDim.x * GZ_WARPS, first = blockIdx.x * GZ_WARPS + w;
+    const T* g = static_cast<const T*>(p.g) + first * p.ldg + c;
+    const T* z = static_cast<const T*>(p.z) + first * p.ldz + c;
+    T* o = static_cast<T*>(p.gz) + first * p.ldo + c;
+    const long long sg = step * p.ldg, sz = step * p.ldz, so = step * p.ldo;
+    // the lane's rows; the pointers go along (a 64-bit product per load would cost as much as the rest)
+    for (int left = first < p.rows ? ((int)p.rows - first - 1) / step + 1 : 0; left > 0; left -= GZ_BATCH) {
+      Raw<T, V> rg[GZ_BATCH], rz[GZ_BATCH];
 #pragma unroll
       for (int k = 0; k < GZ_BATCH; ++k) {
-        const long long m = m0 + k * step;
-#pragma unroll
-        for (int i = 0; i < V; ++i) a[k][i] = b[k][i] = 0.f;
-        if (m < p.rows) {
-          load_v<T, V>(g + m * p.ldg, a[k]);
-          if (p.z) load_v<T, V>(z + m * p.ldz, b[k]);
-        }
+        rg[k].load(g, k < left);
+        rz[k].load(z, k < left && p.z);
+        g += sg;
+        z += sz;
       }
 #pragma unroll
       for (int k = 0; k < GZ_BATCH; ++k) {
-        const long long m = m0 + k * step;
-        if (m >= p.rows) break;
+        if (k >= left) break;
+        float a[V], b[V];
+        rg[k].get(a);
+        rz[k].get(b);
         // a rounded product (no contraction into the sum), so that g_bias has the same bits with and without gz
         if (p.act == EMP_ACT_SILU) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) a[k][i] = __fmul_rn(a[k][i], dact<EMP_ACT_SILU>(b[k][i]));
+          for (int i = 0; i < V; ++i) a[i] = __fmul_rn(a[i], dact<EMP_ACT_SILU>(b[i]));
         } else if (p.act == EMP_ACT_GELU) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) a[k][i] = __fmul_rn(a[k][i], dact<EMP_ACT_GELU>(b[k][i]));
+          for (int i = 0; i < V; ++i) a[i] = __fmul_rn(a[i], dact<EMP_ACT_GELU>(b[i]));
         }
-        if (p.gz) store_v<T, V>(o + m * p.ldo, a[k]);
+        if (p.gz) store_v<T, V>(o, a);
+        o += so;
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[i] += a[k][i];
+        for (int i = 0; i < V; ++i) s[i] += a[i];
       }
     }
   }

@@ -738,13 +738,6 @@ __global__ void __launch_bounds__(ST_THREADS, NA > 16 ? 2 : 3) k_rms_norm_grad_s
 // Two blocks of 256 threads per SM and two vectors a thread: 4096 x 2048 FP32 takes 28 us, 4.8 TB/s, and 80896 x 512 bf16
 // 67 us, 4.9 TB/s; three blocks spill (33 us), one vector with four blocks 40 us (both at 4096 x 2048).
 constexpr int GRAD_PER_SM = 2;
-template <typename T, int V>
-struct Raw {                     // V elements as they are in memory
-  uint4 u;
-  __device__ __forceinline__ void load(const T* p, bool in) { u = in ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void get(float (&v)[V]) const { unpack16<T, V>(u, v); }
-};
-
 template <typename T, int V, int SL, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? GRAD_PER_SM : 1) k_rms_norm_grad(const GradArgs p) {
   extern __shared__ float acc_sm[];              // [cols] when the block has several rows or there are degrees
@@ -938,10 +931,12 @@ template <typename T, bool QUANT, bool RES, int RW>
 bool launch_odd4(const Args& a, int rows_smem, int smem, cudaStream_t st) {
   if (allow_smem<k_rms_norm_odd<T, QUANT, RES, RW>>(ODD_SMEM) != cudaSuccess) return false;
   const long long groups = (a.rows + RW * ODD_THREADS / 32 - 1) / (RW * ODD_THREADS / 32);
-  // persistent where two buffers of rows fit, else a block per group of rows
-  const int bufs = smem + rows_smem <= ODD_SMEM ? 2 : 1;
+  // a block per group of rows where they are all at work at once (5374 x 794 bf16 with a residual: 12.3 us, 14.3 with two
+  // buffers) or two buffers do not fit, else persistent
+  auto at_once = [](int bytes) { return (long long)tc::num_sms() * std::min(8, SM_SMEM / (bytes + 1024)); };
+  const int bufs = groups > at_once(smem) && smem + rows_smem <= ODD_SMEM ? 2 : 1;
   if (bufs == 2) smem += rows_smem;
-  const long long grid = bufs == 2 ? std::min<long long>(groups, (long long)tc::num_sms() * std::min(8, SM_SMEM / (smem + 1024))) : groups;
+  const long long grid = bufs == 2 ? at_once(smem) : groups;
   k_rms_norm_odd<T, QUANT, RES, RW><<<(unsigned)grid, ODD_THREADS, smem, st>>>(a, bufs);
   return true;
 }

@@ -40,16 +40,6 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) 
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// an element as it is in memory, so that many loads can be on their way before the first conversion
-template <typename T> struct Bits { using U = std::conditional_t<sizeof(T) == 4, float, std::conditional_t<sizeof(T) == 2, unsigned short, unsigned char>>; };
-__device__ __forceinline__ float bits_to_f(float u, float) { return u; }
-__device__ __forceinline__ float bits_to_f(unsigned short u, __nv_bfloat16) { return __uint_as_float((uint32_t)u << 16); }
-__device__ __forceinline__ float bits_to_f(unsigned short u, __half) { return __half2float(__ushort_as_half(u)); }
-__device__ __forceinline__ float bits_to_f(unsigned char u, __nv_fp8_e4m3) {
-  __nv_fp8_e4m3 e;
-  e.__x = u;
-  return (float)e;
-}
 // 16 bytes as floats: four of fp32 or eight of a 16-bit type
 template <typename T, int V>
 __device__ __forceinline__ void unpack16(const uint4& u, float (&v)[V]) {
@@ -92,6 +82,31 @@ __device__ __forceinline__ void store_v(T* p, const float (&v)[V]) {
     *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
   }
 }
+// V elements as they are in memory (zeros where `in` is false): a load with its conversion in one branch would be
+// waited for before the next one.  One element of 8 or 16 bits has a register to itself.
+template <typename T, int V> struct Raw {
+  using U = std::conditional_t<V * sizeof(T) == 16, uint4, uint32_t>;
+  U u;
+  __device__ __forceinline__ void load(const T* p, bool in) {
+    u = U();
+    if (!in) return;
+    if constexpr (V > 1 || sizeof(T) == 4) u = *reinterpret_cast<const U*>(p);
+    else if constexpr (sizeof(T) == 2) u = *reinterpret_cast<const unsigned short*>(p);
+    else u = *reinterpret_cast<const unsigned char*>(p);
+  }
+  __device__ __forceinline__ void get(float (&v)[V]) const {
+    if constexpr (V == 1) v[0] = one(T());
+    else if constexpr (V == 2) unpack2<T>(u, v[0], v[1]);
+    else unpack16<T, V>(u, v);
+  }
+  __device__ __forceinline__ float one(float) const { return __uint_as_float(u); }
+  __device__ __forceinline__ float one(__nv_bfloat16) const { return __uint_as_float(u << 16); }
+  __device__ __forceinline__ float one(__half) const { return __half2float(__ushort_as_half((unsigned short)u)); }
+  __device__ __forceinline__ float one(__nv_fp8_e4m3 e) const {
+    e.__x = (unsigned char)u;
+    return (float)e;
+  }
+};
 // V values rounded to e4m3 (to nearest even; beyond +-448 to +-448; NaN kept)
 template <int V>
 __device__ __forceinline__ void store_e4m3(__nv_fp8_storage_t* p, const float (&v)[V]) {
