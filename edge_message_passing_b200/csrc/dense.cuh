@@ -37,8 +37,8 @@ __device__ __forceinline__ void put_one(const Epi& e, long long m, int n, float 
 // Up to 16 rows of a short k and a small W: the product reads W once per 8 rows and little else, so it runs on SIMT with
 // a warp on FEW_COLS columns of the output and up to 8 rows at a time (x in shared memory as floats, K_PART of
 // k at once; a lane takes V elements of k, 32 V apart, and where V is 1 eight of those at a time, for as many loads in flight), in FP32 throughout.  Against the tensor-core kernel, whose
-// set-up costs more: 8 rows, 256 -> 1024, FP32: 9.4 and 15.8 us; 2048 -> 2048: 20.6 and 25.0 (bf16 16.8 and 17.0); beyond,
-// W's reads and a warp's long k lose: 16 rows, 2048 -> 2048 bf16 20.9 and 17.0, 8 rows, 8192 -> 128 51.7 and 20.2.
+// set-up costs more: 8 rows, 256 -> 1024, FP32: 9.2 and 15.1 us; 2048 -> 2048: 14.9 and 24.4 (bf16 15.1 and 17.1); beyond,
+// W's reads and a warp's long k lose: 16 rows, 2048 -> 2048 bf16 20.9 and 17.0, 8 rows, 8192 -> 128 51.7 and 17.4.
 constexpr int FEW_COLS = 2, FEW_WARPS = 4, FEW_M = 8, K_PART = 1024;
 inline bool few_rows(long long rows, long long N, long long K) {
   return rows <= 2 * FEW_M && K <= 2048 && (rows + FEW_M - 1) / FEW_M * N * K <= (1 << 22);

@@ -706,3 +706,41 @@ def test_norm_of_contiguous_rows_off_16_bytes(rows, cols, type):
                          scale.data_ptr() if y_code == 3 else None, sums.data_ptr(), cols)
         assert emp.lib().mp_rms_norm(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0
         assert torch.all(y[rows * cols:].float() == 7) and torch.all(sums[rows * cols:].float() == 7) and scale[rows] == 7
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16"])
+@pytest.mark.parametrize("K,N", [(64, 128), (96, 72), (40, 260), (33, 45)])
+@pytest.mark.parametrize("residual,keep", [(False, False), (True, False), (True, True)])
+def test_dense_of_many_tiles_per_block(K, N, residual, keep, type):
+    """More than two tiles of 128 rows for every SM, the last one ragged: what the epilogue asks for ahead of a tile belongs to it."""
+    t, rows = TYPES[type], 2 * 148 * 128 + 19000 + 77
+    rng = np.random.default_rng(K + N)
+    x, w, b = dev(normal(rng, rows, K), t), dev(normal(rng, N, K) / np.sqrt(K), t), dev(normal(rng, N), t)
+    r = dev(normal(rng, rows, N), t) if residual else None
+    out = emp.mp_dense(x, w, b, activation="silu", residual=r, keep_z=keep)
+    y, z = out if keep else (out, None)
+    ry, rz, ty, tz = dense_tol(host(x), host(w), host(b), host(r), "silu", t, K)
+    near(y, ry, ty, "y")
+    if keep:
+        near(z, rz, tz, "z")
+
+
+@pytest.mark.parametrize("type", [*TYPES, "e4m3"])
+@pytest.mark.parametrize("rows,K,N", [(12, 2001, 99), (16, 1025, 33), (1, 1153, 130), (9, 2047, 7)])
+def test_dense_of_few_rows_off_16_bytes(rows, K, N, type):
+    """Rows of a k that is odd and longer than what is staged at once."""
+    rng = np.random.default_rng(rows * K + N)
+    x, w, r = normal(rng, rows, K), normal(rng, N, K) / np.sqrt(K), normal(rng, rows, N)
+    if type == "e4m3":
+        t = torch.float16
+        (x, xs), (w, ws) = to_e4m3(x), to_e4m3(w)
+        r = dev(r, t)
+        y = emp.mp_dense(x, w, activation="silu", residual=r, x_scale=xs, w_scale=ws, out_dtype=t)
+        X, W = host(x) * host(xs)[:, None], host(w) * host(ws)[:, None]
+    else:
+        t = TYPES[type]
+        x, w, r = dev(x, t), dev(w, t), dev(r, t)
+        y = emp.mp_dense(x, w, activation="silu", residual=r)
+        X, W = host(x), host(w)
+    ry, _, ty, _ = dense_tol(X, W, None, host(r), "silu", t, K)
+    near(y, ry, ty, "y")
