@@ -796,7 +796,7 @@ inline bool tma_ok(const void* p, long long ld, int t) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * dtype_size(t) % 16 == 0;
 }
 
-// Tile width and splits of the k axis of an M x N product with K summed: those of the least estimated time (a width
+// Tile width and splits of the k axis of an M x N product with K summed (each at least 1): those of the least estimated time (a width
 // that divides N well against one that uses each operand byte more often).  A CTA's
 // tile takes the longer of its k stages and its epilogue (which runs beside the next tile's stages), the CTAs work in
 // waves, and splits pay for their partial products.  Microseconds as measured for the 16-bit and the FP32 kernel: a

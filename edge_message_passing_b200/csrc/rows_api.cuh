@@ -78,6 +78,7 @@ struct DenseLayout {
 };
 DenseLayout dense_layout(const emp_dense& a) {
   DenseLayout L;
+  if (a.rows == 0) return L;                             // nothing to launch; shape_for wants a tile at least
   L.few = dense::few_rows(a.rows, a.fan_out, a.fan_in);
   if (L.few) return L;
   auto take = [&](size_t bytes) { size_t r = L.total; L.total = align_up(L.total + bytes); return r; };

@@ -371,7 +371,7 @@ typedef struct {
  * shrink a sum by 8e-5 of itself over the longest k and by 2e-8 over the shortest; y and z are rounded once, at the end.
  * An infinite or NaN input makes outputs of its row (of x) or column (of weight) NaN or infinite, and no others; through
  * an activation z = -inf gives NaN.  Errors: EMP_ERR_ARG, EMP_ERR_UNSUPPORTED,
- * EMP_ERR_WORKSPACE (ws_bytes below mp_dense_workspace_bytes(a); 0 for many shapes). */
+ * EMP_ERR_WORKSPACE (ws_bytes below mp_dense_workspace_bytes(a); 0 for many shapes and for zero rows). */
 size_t mp_dense_workspace_bytes(const emp_dense* a);
 int mp_dense(const emp_dense* a, void* ws, size_t ws_bytes, cudaStream_t stream);
 
