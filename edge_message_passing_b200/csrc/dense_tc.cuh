@@ -39,6 +39,7 @@
 #include <type_traits>
 #include "so2_tc.cuh"
 #include "dense.cuh"
+#include "steps.cuh"
 
 namespace emp {
 namespace dtc {
@@ -710,18 +711,17 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
       }
     };
     if constexpr (PATH == SHORT) {
-      for (int k = g; k < p.nk; k += SPLIT_GROUPS) {        // B, in place: the whole stage is read before hi is written over it
-        const bool landed = __all_sync(0xffffffffu, wait(&b_full[k], 0));
-        unsigned char* bhi = hl + k * HL_BYTES;
-        float x[32];
-        if (r < p.bn) read_row(bhi, r, p.b_mn, p.bn, x);
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");       // reached by all four warps, landed or not
-        if (!landed) { ok = false; break; }
-        if (r < p.bn) split_b(bhi, x);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&b_split[k]);
-      }
+      float x[32];                                          // B, in place: the whole stage is read before hi is written over it
+      ok = in_place_stages(g, SPLIT_GROUPS, p.nk,
+          [&](int k) { return __all_sync(0xffffffffu, wait(&b_full[k], 0)) != 0; },
+          [&](int k) { if (r < p.bn) read_row(hl + k * HL_BYTES, r, p.b_mn, p.bn, x); },
+          [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory"); },
+          [&](int k) {
+            if (r < p.bn) split_b(hl + k * HL_BYTES, x);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&b_split[k]);
+          });
     }
     for (long long w = blockIdx.x; w < p.items && ok; w += gridDim.x, t = t.next(p)) {
       for (int k = 0; k < t.k_n; ++k, ++it) {
