@@ -469,7 +469,8 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     const int nch = p.bn / 32;
     uint32_t done = 0;                                       // pieces of W columns put through the places
-    bool ok = true, asked = false;                           // asked: the next chunk's residual is on its way
+    bool ok = true, asked = false;                           // asked: what the next chunk reads is on its way
+    bool coming = false;                                     // a residual's TMA load, into place done % PLACES
     B bias_l = from_f<B>(0.f);
     float ws_l = 0.f, xs_l = 0.f;                            // of the next chunk: column lane's bias and scale, row lane's scale
     auto here = [&](const Item& t, int c) { return t.m0 + q * 32 < p.M && t.n0 + c * 32 < p.N; };
@@ -478,10 +479,13 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
     auto ask_residual = [&](const Item& t, int c, int h) {   // of piece h of the chunk; its place must be free
       if constexpr (!ROWS) {
         if (R == 32) load_column<T, R>(res, e, (int)min((long long)32, p.M - t.m0 - q * 32), t.m0 + q * 32, t.n0 + c * 32 + lane, p.N, 0);
-      } else if (lane == 0) {
-        const int pl = done % PLACES;
-        tc::mbar_expect_tx(&rbar[pl], PLACE_BYTES);
-        tc::tma_load(place + pl * PLACE_BYTES, &maps.res, &rbar[pl], t.n0 + c * 32 + h * W, (int)(t.m0 + q * 32));
+      } else {
+        coming = true;
+        if (lane == 0) {
+          const int pl = done % PLACES;
+          tc::mbar_expect_tx(&rbar[pl], PLACE_BYTES);
+          tc::tma_load(place + pl * PLACE_BYTES, &maps.res, &rbar[pl], t.n0 + c * 32 + h * W, (int)(t.m0 + q * 32));
+        }
       }
     };
     // ask for what chunk c of an item needs
@@ -596,6 +600,7 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
         }
         if (e.residual) {
           if (!__all_sync(0xffffffffu, wait(&rbar[pl], (uint32_t)((done / PLACES) & 1)))) { ok = false; return; }
+          coming = false;
 #pragma unroll
           for (int j = 0; j < W / V; ++j) {
             float a[V];
@@ -686,7 +691,7 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
       }
     }
     if (ROWS) {
-      if (asked && e.residual && !e.z) wait(&rbar[done % PLACES], (uint32_t)((done / PLACES) & 1));   // a load in flight (after a timeout)
+      if (coming) wait(&rbar[done % PLACES], (uint32_t)((done / PLACES) & 1));   // a load in flight (after a timeout)
       if (lane == 0) stores_read<0>();                       // the places outlive the stores' reads
     }
   } else if (FP32 && warp >= 2 + EPI_WARPS) {
