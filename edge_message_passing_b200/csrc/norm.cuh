@@ -12,6 +12,11 @@
 // y in 8 bits: scale = max_j |y_j| / 448 per row, q = RN_e4m3(y / scale).  max |y| = rstd max |s w|
 // (rstd is one positive factor of the row), so the maximum is taken together with the sum of squares
 // and the row still needs one block-wide reduction.  The maximum keeps a NaN, so a row with one comes out as NaN.
+//
+// The squares of a whole row would leave FP32 at |s| of 1.8e19 / sqrt(cols), and 1 / sqrt of infinity would turn the row into
+// zeros.  So a thread's sum (of 176 elements at the most) is multiplied by `unit`, a power of two of 1 / cols at most, before it
+// is added to the others: |s| up to 1.3e18 then stays in range at any width, and the factor changes no bit.  (On every square
+// it would allow 1.8e19 and cost up to 5 %: 80896 x 515 bf16 43 us instead of 41.)
 #pragma once
 #include <atomic>
 #include <type_traits>
@@ -32,6 +37,7 @@ struct Args {
   void *y, *s;
   float* scale;
   long long ldx, ldr, ldy, lds;
+  float unit, count;           // set by the launch: a power of two of 1 / cols at most, and cols unit
 };
 struct GradArgs {
   long long rows;
@@ -41,6 +47,7 @@ struct GradArgs {
   void* g_x;
   float* part;                 // [gridDim.x][weights] sums of g n (null: no weight gradient)
   long long ldg, lds, ldgs, ldgx;
+  float unit, count;           // as in Args
 };
 
 __device__ __forceinline__ int weight_at(int col, int C, int degrees) {
@@ -86,8 +93,9 @@ __device__ __forceinline__ float degree_sum(const float* sums, int o, int C) {
 
 // Rows of 16-byte vectors.  Bound by HBM (from L2's side: the loads of many small blocks in flight): 4096 x 2048 FP32 with
 // a residual 26.5 us, 5.1 TB/s; 16384 x 2048 bf16 with a residual to 8 bits 46 us, 5.1 TB/s.
+// (FP32 with 16 elements a thread: 42 registers at most; the compiler would take 50 and 27.2 us.)
 template <typename T, int V, int SL, bool QUANT>
-__global__ void __launch_bounds__(MAX_THREADS) k_rms_norm(const Args p) {
+__global__ void __launch_bounds__(MAX_THREADS, V == 4 && SL == 4 && !QUANT ? 3 : 0) k_rms_norm(const Args p) {
   __shared__ float red_a[32], red_b[32];
   const int G = blockDim.x, t = threadIdx.x, r = threadIdx.y;
   const long long row = (long long)blockIdx.x * blockDim.y + r;
@@ -138,9 +146,10 @@ __global__ void __launch_bounds__(MAX_THREADS) k_rms_norm(const Args p) {
     }
   }
   const int slot = r * (G >> 5);
+  ss *= p.unit;
   row_reduce<QUANT>(ss, top, G, t, red_a + slot, red_b + slot);
   if (!live) return;
-  const float rstd = rsqrtf(ss / (float)p.cols + p.eps);
+  const float rstd = rsqrtf(ss / p.count + p.eps);
   float inv = 1.f;
   if (QUANT) {
     const float m = top * rstd;
@@ -283,12 +292,13 @@ __global__ void __launch_bounds__(ODD_THREADS) k_rms_norm_odd(const Args p, int 
     float rstd[RW], inv[RW];
 #pragma unroll
     for (int j = 0; j < RW; ++j) {
+      ss[j] *= p.unit;
 #pragma unroll
       for (int o = 16; o; o >>= 1) {
         ss[j] += __shfl_xor_sync(0xffffffffu, ss[j], o);
         if (QUANT) top[j] = max_abs(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
       }
-      rstd[j] = rsqrtf(ss[j] / (float)p.cols + p.eps);
+      rstd[j] = rsqrtf(ss[j] / p.count + p.eps);
       inv[j] = 1.f;
       if (QUANT) {
         const float m = top[j] * rstd[j];
@@ -413,12 +423,14 @@ __global__ void __launch_bounds__(ODD_THREADS) k_rms_norm_grad_odd(const GradArg
             hs += g[e] * wv[k][e] * s[e];
           }
         }
+      s2 *= p.unit;
+      hs *= p.unit;
 #pragma unroll
       for (int o = 16; o; o >>= 1) {
         s2 += __shfl_xor_sync(0xffffffffu, s2, o);
         hs += __shfl_xor_sync(0xffffffffu, hs, o);
       }
-      const float rstd = rsqrtf(s2 / (float)p.cols + p.eps), q = hs * rstd * rstd / (float)p.cols;
+      const float rstd = rsqrtf(s2 / p.count + p.eps), q = hs * rstd * rstd / p.count;
 #pragma unroll
       for (int k = 0; k < NS; ++k)
         if (lane + 32 * k < n) {
@@ -614,8 +626,9 @@ __global__ void __launch_bounds__(ST_THREADS, NA > 16 ? 2 : 4) k_rms_norm_staged
       v[k] *= wv[k];
       if (QUANT) top = max_abs(top, v[k]);
     }
+    ss *= p.unit;
     team_reduce<true>(ss, top, m, red);
-    const float rstd = rsqrtf(ss / (float)p.cols + p.eps);
+    const float rstd = rsqrtf(ss / p.count + p.eps);
     float inv = 1.f;
     if (QUANT) {
       const float big = top * rstd;
@@ -694,8 +707,10 @@ __global__ void __launch_bounds__(ST_THREADS, NA > 16 ? 2 : 3) k_rms_norm_grad_s
       s2 += v * v;
       hs += to_f(gv[c]) * wv[k] * v;
     }
+    s2 *= p.unit;
+    hs *= p.unit;
     team_reduce<false>(s2, hs, m, red);
-    const float rstd = rsqrtf(s2 / (float)p.cols + p.eps), q = hs * rstd * rstd / (float)p.cols;
+    const float rstd = rsqrtf(s2 / p.count + p.eps), q = hs * rstd * rstd / p.count;
     T* out = static_cast<T*>(p.g_x) + row * p.ldgx;
     T* ov = reinterpret_cast<T*>(os + phase_of(out));
 #pragma unroll
@@ -794,6 +809,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? GRAD_PER_SM : 1) k_rms_nor
         hs += g[k][i] * wv[i] * s[k][i];
       }
     }
+    ss *= p.unit;
+    hs *= p.unit;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
       ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -808,8 +825,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? GRAD_PER_SM : 1) k_rms_nor
       for (int i = 0; i < nw; ++i) { ss += red[par][0][w0 + i]; hs += red[par][1][w0 + i]; }
     }
     if (!live) continue;
-    const float rstd = rsqrtf(ss / (float)p.cols + p.eps);
-    const float q = hs * rstd * rstd / (float)p.cols;      // mean(h n) rstd: n mean(h n) = s q
+    const float rstd = rsqrtf(ss / p.count + p.eps);
+    const float q = hs * rstd * rstd / p.count;      // mean(h n) rstd: n mean(h n) = s q
 #pragma unroll
     for (int k = 0; k < SL; ++k) {
       const int c = (k * G + t) * V;
@@ -961,8 +978,17 @@ bool launch_odd(const Args& a, bool quant, cudaStream_t st) {
   return (many && launch_odd3<T, false, 2>(a, st)) || launch_odd3<T, false, 1>(a, st);
 }
 
+template <typename A>
+A with_unit(A a) {
+  a.unit = 1.f;
+  while (a.unit * a.cols > 1.f) a.unit *= 0.5f;
+  a.count = a.unit * a.cols;
+  return a;
+}
+
 template <typename T>
-cudaError_t launch_fwd(const Args& a, bool quant, cudaStream_t st) {
+cudaError_t launch_fwd(const Args& args, bool quant, cudaStream_t st) {
+  const Args a = with_unit(args);
   constexpr int ES = sizeof(T), V = 16 / ES;
   const bool yv = quant ? reinterpret_cast<uintptr_t>(a.y) % V == 0 && (a.rows == 1 || a.ldy % V == 0) : vec_ok(a.y, a.ldy, a.rows, ES);
   const bool vec = a.cols % V == 0 && yv && vec_ok(a.x, a.ldx, a.rows, ES) && vec_ok(a.residual, a.ldr, a.rows, ES) &&
@@ -1009,7 +1035,8 @@ int launch_grad_odd(const GradArgs& a, cudaStream_t st) {      // 0: not for the
   return 0;
 }
 template <typename T>
-cudaError_t launch_grad(const GradArgs& a, int* blocks, cudaStream_t st) {          // *blocks: the rows of a.part
+cudaError_t launch_grad(const GradArgs& args, int* blocks, cudaStream_t st) {       // *blocks: the rows of part
+  const GradArgs a = with_unit(args);
   constexpr int ES = sizeof(T), V = 16 / ES;
   const bool vec = a.cols % V == 0 && vec_ok(a.g, a.ldg, a.rows, ES) && vec_ok(a.s, a.lds, a.rows, ES) &&
                    vec_ok(a.g_s, a.ldgs, a.rows, ES) && vec_ok(a.g_x, a.ldgx, a.rows, ES) && vec_ok(a.w, 0, 1, ES) &&

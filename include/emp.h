@@ -316,7 +316,8 @@ typedef struct {
 
 /* Root-mean-square norm of rows with the residual's addition:
  *   s = x + residual,  y_j = s_j weight_j / sqrt(mean_j s_j^2 + eps)
- * (y from the unrounded s; sums in FP32, so |s| up to 1e18).  With degrees, a row is an atom's
+ * (y from the unrounded s; sums in FP32, so |s| up to 1e18 at any width and |s weight| up to
+ * 3e38; beyond, a row's sum may be infinite and the row zeros).  With degrees, a row is an atom's
  * [16][C] features and the weight depends on degree and channel alone: the norm then commutes
  * with rotations.  y_dtype EMP_E4M3: scale = max_j |y_j| / 448 and y / scale rounded to e4m3
  * (ties to even); a row with max |y| < 2^-110 has scale 1; a row with a NaN or an infinity in s has
@@ -339,8 +340,8 @@ typedef struct {
   void* g_weight;           /* [cols] or [4][C], contiguous, or NULL */
 } emp_rms_norm_grad;
 
-/* Gradient of mp_rms_norm (y not in 8 bits).  Types are dtype throughout; sums over rows in FP32
- * in a fixed order.  Workspace only with g_weight.  Zero rows: g_weight is zeroed. */
+/* Gradient of mp_rms_norm (y not in 8 bits).  Types are dtype throughout; |s| up to 1e18 and
+ * |g weight s| up to 1e36; sums over rows in FP32 in a fixed order.  Workspace only with g_weight.  Zero rows: g_weight is zeroed. */
 size_t mp_rms_norm_grad_workspace_bytes(const emp_rms_norm_grad* a);
 int mp_rms_norm_grad(const emp_rms_norm_grad* a, void* ws, size_t ws_bytes, cudaStream_t stream);
 
