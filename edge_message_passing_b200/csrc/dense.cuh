@@ -274,10 +274,10 @@ __global__ void __launch_bounds__(32 * GZ_WARPS, GZ_PER_SM) k_dense_gz(const GzA
         // a rounded product (no contraction into the sum), so that g_bias has the same bits with and without gz
         if (p.act == EMP_ACT_SILU) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) a[i] = __fmul_rn(a[i], dact<EMP_ACT_SILU>(b[i]));
+          for (int i = 0; i < V; ++i) a[i] = __fmul_rn(a[i], dact<EMP_ACT_SILU, T>(b[i]));
         } else if (p.act == EMP_ACT_GELU) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) a[i] = __fmul_rn(a[i], dact<EMP_ACT_GELU>(b[i]));
+          for (int i = 0; i < V; ++i) a[i] = __fmul_rn(a[i], dact<EMP_ACT_GELU, T>(b[i]));
         }
         if (p.gz) store_v<T, V>(o, a);
         o += so;

@@ -217,10 +217,10 @@ __device__ __forceinline__ void finish_column(float (&v)[R], const float (&res)[
   }
   if (e.act == EMP_ACT_SILU) {
 #pragma unroll
-    for (int k = 0; k < R; ++k) v[k] = act<EMP_ACT_SILU>(v[k]);
+    for (int k = 0; k < R; ++k) v[k] = act<EMP_ACT_SILU, T>(v[k]);
   } else if (e.act == EMP_ACT_GELU) {
 #pragma unroll
-    for (int k = 0; k < R; ++k) v[k] = act<EMP_ACT_GELU>(v[k]);
+    for (int k = 0; k < R; ++k) v[k] = act<EMP_ACT_GELU, T>(v[k]);
   }
   if (e.residual) {
 #pragma unroll
@@ -593,10 +593,10 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
         // each step for the whole piece: a branch per element would jump over the other activations' code every time
         if (e.act == EMP_ACT_SILU) {
 #pragma unroll
-          for (int i = 0; i < W; ++i) v[h * W + i] = act<EMP_ACT_SILU>(v[h * W + i]);
+          for (int i = 0; i < W; ++i) v[h * W + i] = act<EMP_ACT_SILU, T>(v[h * W + i]);
         } else if (e.act == EMP_ACT_GELU) {
 #pragma unroll
-          for (int i = 0; i < W; ++i) v[h * W + i] = act<EMP_ACT_GELU>(v[h * W + i]);
+          for (int i = 0; i < W; ++i) v[h * W + i] = act<EMP_ACT_GELU, T>(v[h * W + i]);
         }
         if (e.residual) {
           if (!__all_sync(0xffffffffu, wait(&rbar[pl], (uint32_t)((done / PLACES) & 1)))) { ok = false; return; }

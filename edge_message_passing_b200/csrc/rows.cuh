@@ -147,10 +147,14 @@ __device__ __forceinline__ int degree_of(int lm) { return (lm > 0) + (lm > 3) + 
 // SiLU z / (1 + exp(-z)) and GELU z Phi(z), and their derivatives, with e^x = 2^(x log2 e) by the special-function
 // unit's 2^x and 1/x, both with results below 2^-126 as zero: __expf and __fdividef, which keep those, take 14
 // instructions an element of SiLU instead of 5, and instructions bound a short-k epilogue (647168 x 64 -> 512 in FP32:
-// 401 us so, 340 thus).  -inf and NaN give NaN.  Phi, the normal distribution function, is 1/2 erfc(-z / sqrt 2) with the rational
-// approximation 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical Functions (1964): erfc(x) = t (a1 + t (a2 + ...))
-// exp(-x^2), t = 1 / (1 + p x), within 1.5e-7 for x >= 0; erff costs more than twice as much.  With the FP32 arithmetic
-// the error of GELU is about 2e-7 |z|.
+// 401 us so, 340 thus).  -inf and NaN give NaN.  Phi, the normal distribution function, is for z < 0
+//   Phi(z) = exp(-z^2 / 2) t q(t),  t = 1 / (1 + p |z|),
+// with q a polynomial fitted to exp(z^2 / 2) Phi(z) / t over -13.3 <= z <= 0 for the least largest RELATIVE error (least squares with
+// Lawson's weights), so that GELU keeps its digits where it is small: 1/2 (1 + erf) has none there beyond z = -5, and erff costs
+// more than twice as much.  For FP32 degree 7, within 1.2e-7: with the FP32 arithmetic Phi is within (32 + 1.5 z^2) 2^-24 of itself,
+// the second term from the rounding of z^2 / 2 (SiLU's exponential has the same, |z| 2^-23).  For 16-bit types degree 5,
+// within 1.2e-6 up to |z| = 1 and 5e-5 from 3 on, a tenth of half a step of fp16 (161792 x 64 -> 512 with GELU: bf16 90 us with
+// degree 7, 85 with 5; FP32 106).  Below z = -13.2 (SiLU: -87) the results are zero.
 __device__ __forceinline__ float ex2_ftz(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -162,38 +166,51 @@ __device__ __forceinline__ float rcp_ftz(float x) {
   return y;
 }
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr float GELU_P = 0.3275911f * 0.70710678f;        // p / sqrt 2
 
 __device__ __forceinline__ float sigmoid_ftz(float z) { return rcp_ftz(1.0f + ex2_ftz(-LOG2E * z)); }
-__device__ __forceinline__ float phi_ftz(float z, float gauss) {            // Phi(z); gauss = exp(-z^2 / 2)
-  const float t = rcp_ftz(fmaf(GELU_P, fabsf(z), 1.f));
-  float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
-  q = fmaf(t, q, 0.5f * 1.421413741f);
-  q = fmaf(t, q, 0.5f * -0.284496736f);
-  q = fmaf(t, q, 0.5f * 0.254829592f);
+template <typename T> __device__ __forceinline__ float phi_ftz(float z, float gauss) {            // Phi(z); gauss = exp(-z^2 / 2)
+  float t, q;
+  if constexpr (sizeof(T) == 4) {
+    t = rcp_ftz(fmaf(0.3f, fabsf(z), 1.f));
+    q = fmaf(t, 0.0360362099f, -0.158713255f);
+    q = fmaf(t, q, 0.208964023f);
+    q = fmaf(t, q, -0.0560953968f);
+    q = fmaf(t, q, 0.129843179f);
+    q = fmaf(t, q, 0.0995231307f);
+    q = fmaf(t, q, 0.120816882f);
+    q = fmaf(t, q, 0.119625166f);
+  } else {
+    t = rcp_ftz(fmaf(0.29f, fabsf(z), 1.f));
+    q = fmaf(t, -0.0867664392f, 0.278030956f);
+    q = fmaf(t, q, -0.0844277764f);
+    q = fmaf(t, q, 0.174245341f);
+    q = fmaf(t, q, 0.102189743f);
+    q = fmaf(t, q, 0.116728611f);
+  }
   const float h = t * q * gauss;                          // Phi(-|z|)
   return z < 0.f ? h : 1.f - h;
 }
 __device__ __forceinline__ float gauss_ftz(float z) { return ex2_ftz(-0.5f * LOG2E * z * z); }
 
-template <int ACT> __device__ __forceinline__ float act(float z) {
+// T: the type that the result is rounded to
+template <int ACT, typename T> __device__ __forceinline__ float act(float z) {
   if constexpr (ACT == EMP_ACT_SILU) return z * sigmoid_ftz(z);
-  else if constexpr (ACT == EMP_ACT_GELU) return z * phi_ftz(z, gauss_ftz(z));
+  else if constexpr (ACT == EMP_ACT_GELU) return z * phi_ftz<T>(z, gauss_ftz(z));
   else return z;
 }
-template <int ACT> __device__ __forceinline__ float dact(float z) {
+template <int ACT, typename T> __device__ __forceinline__ float dact(float z) {
   if constexpr (ACT == EMP_ACT_SILU) {
     const float s = sigmoid_ftz(z);
     return s * (1.0f + z * (1.0f - s));
   } else if constexpr (ACT == EMP_ACT_GELU) {
     const float g = gauss_ftz(z);
-    return phi_ftz(z, g) + z * 0.39894228040143268f * g;
+    return phi_ftz<T>(z, g) + z * 0.39894228040143268f * g;
   } else {
     return 1.0f;
   }
 }
 __device__ __forceinline__ float act_f(int a, float z) {
-  return a == EMP_ACT_SILU ? act<EMP_ACT_SILU>(z) : a == EMP_ACT_GELU ? act<EMP_ACT_GELU>(z) : z;
+  return a == EMP_ACT_SILU ? act<EMP_ACT_SILU, float>(z) : a == EMP_ACT_GELU ? act<EMP_ACT_GELU, float>(z) : z;
 }
 
 // ------------------------------------------------------------- join of column sums

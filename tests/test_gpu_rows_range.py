@@ -3,7 +3,8 @@ block, values at the ends of the types, long sums.  Tolerances as derived in tes
 import numpy as np
 import pytest
 
-from test_gpu_rows import TYPES, dense_tol, dev, host, near, normal, to_e4m3
+from oracle import rows as orow
+from test_gpu_rows import TYPES, U, dense_tol, dev, floor_of, half_step, host, near, normal, to_e4m3
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -60,3 +61,38 @@ def test_gelu_of_8_bits(rows, K, N):
         ry, rz, ty, tz = dense_tol(host(x) * host(xs)[:, None], host(w) * host(ws)[:, None], None, None, "gelu", t, K)
         near(z, rz, tz, "z")
         near(y, ry, ty, "y")
+
+
+# ------------------------------------------------------------------ activations, relative to their own size
+def activation_tol(z, act, t):
+    """Relative: GELU (32 + 1.5 z^2) u (2^x and 1/x 4 u each with what their arguments' errors do, the polynomial's fit 2 u and eight
+    steps, three products; z^2 / 2 is rounded three times); SiLU 8 u (2^x 4 u, 1/x 2 u, the sum and the product) and
+    |z| log 2 times two roundings of the exponent.  GELU of 16-bit types: a fit within 5e-5."""
+    if act == "gelu":
+        return (32 + 1.5 * z * z) * U + (5e-5 if t != torch.float32 else 0)
+    return (8 + 2 * np.abs(z)) * U
+
+
+@pytest.mark.parametrize("type", list(TYPES))
+@pytest.mark.parametrize("rows", [8, 16, 200, 1620])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activations_keep_their_digits(act, rows, type):
+    """z = x 1 with at most 8 bits of x, so z has no error; down to where the results leave the normal range."""
+    t = TYPES[type]
+    low = -12.5 if act == "gelu" else -80.0
+    x = torch.linspace(low, -low, rows).to(torch.bfloat16).unsqueeze(1)
+    z = x.double().numpy()
+    w = torch.ones((12, 1), device="cuda", dtype=t)
+    y = host(emp.mp_dense(x.cuda().to(t), w, activation=act))
+    ref = orow.activation(z, act)
+    near(torch.from_numpy(y), np.broadcast_to(ref, y.shape), (half_step(t) + activation_tol(z, act, t)) * np.abs(ref) + floor_of(t), act)
+    # the slope, where its two terms do not cancel: through g_x = g act'(z) W with one column
+    g = torch.ones((len(z), 1), device="cuda", dtype=t)
+    g_x = host(emp.mp_dense_grad(g, x.cuda().to(t), w[:1], z=x.cuda().to(t), activation=act, need_weight=False)[0])
+    if act == "gelu":
+        size = orow.phi(z) + np.abs(z) * np.exp(-0.5 * z * z) / np.sqrt(2 * np.pi)
+    else:
+        p = 1 / (1 + np.exp(-z))
+        size = p + np.abs(z) * p * (1 - p)
+    tol = (2 * half_step(t) + 2.0 ** -20) * np.abs(orow.slope(z, act)) + (activation_tol(z, act, t) + 8 * U) * size + 2 * floor_of(t)
+    near(torch.from_numpy(g_x), orow.slope(z, act), tol, act + "'")
