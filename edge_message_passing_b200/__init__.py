@@ -627,13 +627,13 @@ _CODES: Dict[object, int] = {}
 
 
 def _row_torch():
-    global _T
+    global _T, _stream_of
     if _T is None:
-        _T = _torch()
-        _CODES.update({_T.float32: 0, _T.bfloat16: 1, _T.float16: 2, _T.float8_e4m3fn: 3})
+        torch = _torch()
+        _CODES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.float8_e4m3fn: 3})
         # the stream's handle without a Stream object, where this torch has it
-        global _stream_of
-        _stream_of = getattr(_T._C, "_cuda_getCurrentRawStream", _stream_of)
+        _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
+        _T = torch             # last: another thread that finds it finds the rest too
     return _T
 
 
