@@ -18,7 +18,9 @@ def test_first_calls_of_two_threads(monkeypatch):
             go.wait(10)
             super().update(*a, **k)
 
+    monkeypatch.setattr(emp, "_torch", lambda: torch)          # (which wants a device)
     monkeypatch.setattr(emp, "_T", None)
+    monkeypatch.setattr(emp, "_stream_of", emp._stream_of)
     monkeypatch.setattr(emp, "_CODES", Slow())
     seen = []
 
