@@ -180,7 +180,7 @@ int dense_product(long long M, int N, long long K, int t, const dtc::Operand& a,
   { Scope sc_("dense", s); st = dtc::launch(M, N, K, t, a, b, e, h, h.splits > 1 ? part : nullptr, s); }
   if (st != EMP_OK || h.splits == 1) return st;
   Scope sc_("dense_join", s);
-  if (h.splits > JOIN_WARPS && M * N <= (1 << 14) && e.ldy == N && !e.z && !e.bias && !e.residual && e.act == EMP_ACT_NONE)
+  if (h.splits > JOIN_WARPS && M * N <= (1 << 14) && e.ldy == N && !e.x_scale && !e.z && !e.bias && !e.residual && e.act == EMP_ACT_NONE)
     // few outputs of many splits (a weight gradient): warps share an output's splits
     k_col_join<<<(unsigned)((M * N + 31) / 32), 32 * JOIN_WARPS, 0, s>>>(h.splits, (int)(M * N), part, e.y, e.y_dtype);
   else if (N % 4 == 0) dense::k_join<4><<<grid_for(M * N, 1024), 256, 0, s>>>(M, N, h.splits, part, e);

@@ -96,3 +96,69 @@ def test_activations_keep_their_digits(act, rows, type):
         size = p + np.abs(z) * p * (1 - p)
     tol = (2 * half_step(t) + 2.0 ** -20) * np.abs(orow.slope(z, act)) + (activation_tol(z, act, t) + 8 * U) * size + 2 * floor_of(t)
     near(torch.from_numpy(g_x), orow.slope(z, act), tol, act + "'")
+
+
+# ------------------------------------------------------------------ long sums of one sign
+# The tensor cores' adder truncates: each of the n MMAs of a chain takes half a unit in the last place off the running sum on
+# average, n / 4 of the last sum's units in all, a unit being 0.72 2^-23 on average: 2.15e-8 n, 8.8e-5 for the longest chain of 4096 MMAs.
+CHAIN = 1e-4
+
+
+def columns(rng, rows, cols, t, scale=1.0):
+    """Positive values, every column of another size (else all outputs would be rounded alike)."""
+    return dev(rng.uniform(0.5, 1.5, (rows, cols)) * rng.uniform(1, 2, (1, cols)) * scale, t)
+
+
+def short_of(got, ref, t):
+    """Every output within the chain's part and half a step; their mean within the chain's part and five deviations of the rounding."""
+    d = got.double() / ref - 1
+    e = half_step(t) if t != torch.float32 else U
+    assert d.abs().max().item() <= CHAIN + e, d.abs().max().item()
+    assert abs(d.mean().item()) <= CHAIN + 5 * e / np.sqrt(3 * d.numel()), d.mean().item()
+
+
+@pytest.mark.parametrize("type", ["bf16", "f16"])
+@pytest.mark.parametrize("rows", [65536, 300000])
+def test_a_weight_gradient_of_one_sign_over_many_rows(rows, type):
+    t, rng = TYPES[type], np.random.default_rng(rows)
+    x, g = columns(rng, rows, 64, t), columns(rng, rows, 48, t, 2.0 ** -6 if type == "f16" else 1.0)
+    _, g_w, g_b = emp.mp_dense_grad(g, x, torch.zeros((48, 64), device="cuda", dtype=t), need_x=False)
+    short_of(g_w, g.double().t() @ x.double(), t)
+    short_of(g_b, g.double().sum(0), t)
+
+
+@pytest.mark.parametrize("type", ["f32", "bf16", "f16", "e4m3"])
+@pytest.mark.parametrize("rows", [40, 300])
+def test_a_layer_of_one_sign_and_the_longest_k(rows, type):
+    """e4m3 inputs with FP32 outputs show the chain (2048 MMAs of 32) without the output's rounding; FP32 inputs leave the chain
+    every 96 of k and add 683 parts rounded to nearest (at most 683 u) to 36 MMAs' truncation."""
+    K, N, rng = 65536, 64, np.random.default_rng(rows)
+    if type == "e4m3":
+        x, w = (dev(np.exp(rng.uniform(-4, 0, (n, K))), torch.float32).to(torch.float8_e4m3fn) for n in (rows, N))
+        xs, ws = (dev(rng.uniform(1, 2, n), torch.float32) for n in (rows, N))
+        y = emp.mp_dense(x, w, x_scale=xs, w_scale=ws, out_dtype=torch.float32)
+        short_of(y, (x.double() * xs.double()[:, None]) @ (w.double() * ws.double()[:, None]).t(), torch.float32)
+        return
+    t = TYPES[type]
+    x, w = (columns(rng, K, n, t, 1 / 64).t().contiguous() for n in (rows, N))
+    y, ref = emp.mp_dense(x, w), x.double() @ w.double().t()
+    if type == "f32":
+        assert (y.double() / ref - 1).abs().max().item() <= (683 + 2 * 36) * U
+    else:
+        short_of(y, ref, t)
+
+
+@pytest.mark.parametrize("out", list(TYPES))
+@pytest.mark.parametrize("rows,K,N", [(17, 65536, 5), (40, 20000, 64), (128, 33000, 128), (33, 65536, 497), (1, 65536, 33)])
+def test_scales_of_many_splits(rows, K, N, out):
+    """A long k with few outputs is split, and the parts' sum still takes the scales."""
+    t, rng = TYPES[out], np.random.default_rng(rows + K + N)
+    (x, xs), (w, ws) = to_e4m3(normal(rng, rows, K) * np.exp(normal(rng, rows, 1))), to_e4m3(normal(rng, N, K) / np.sqrt(K))
+    X, W = x.double() * xs.double()[:, None], w.double() * ws.double()[:, None]
+    for act, bias in (("none", False), ("silu", True)):
+        b = dev(normal(rng, N), torch.float32) if bias else None
+        y = emp.mp_dense(x, w, b, activation=act, x_scale=xs, w_scale=ws, out_dtype=t)
+        z = host(X @ W.t()) + (0 if b is None else host(b))
+        ref = orow.activation(z, act)
+        dz = (2.0 ** -20 + 2 * (K / 32 + 200) * U) * host(X.abs() @ W.abs().t()) + 8 * U * np.abs(z)    # an MMA sums 32 of k
+        near(y, ref, half_step(t) * np.abs(ref) + 1.13 * dz + 16 * U * (np.abs(z) + np.abs(ref)) + floor_of(t), act)
