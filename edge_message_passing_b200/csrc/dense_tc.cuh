@@ -806,7 +806,7 @@ inline bool tma_ok(const void* p, long long ld, int t) {
 // tile takes the longer of its k stages and its epilogue (which runs beside the next tile's stages), the CTAs work in
 // waves, and splits pay for their partial products.  Microseconds as measured for the 16-bit and the FP32 kernel: a
 // stage with the operands in L2, the epilogue of a tile with one stage.
-constexpr int MAX_CHAIN = 1024;   // 4096 MMAs: a sum shrinks by 8e-5 of itself at most, a fiftieth of a bf16 step
+constexpr int MAX_CHAIN = 1024;   // 4096 MMAs: a sum shrinks by 9e-5 of itself at most, a fortieth of a bf16 step
 struct Shape {
   int bn, splits, per, nk, mtiles, ntiles;
 };

@@ -368,9 +368,10 @@ typedef struct {
 } emp_dense;
 
 /* Dense layer on rows:  z = x W^T + bias,  y = activation(z) + residual.
- * FP32 inputs keep FP32 accuracy (above 16 rows an input of magnitude over 3.4e38 counts as infinite, and an infinite one
- * gives NaN); 16-bit and 8-bit inputs are multiplied as they are and summed in FP32, where the tensor cores' truncation may
- * shrink a sum by 8e-5 of itself over the longest k and by 2e-8 over the shortest; y and z are rounded once, at the end.
+ * FP32 inputs keep FP32 accuracy down to magnitudes of 2^-116.  (Where the product runs on the tensor cores, which depends on
+ * the sizes, an input of magnitude over 3.4e38 counts as infinite, and an infinite one may give NaN.)  16-bit and 8-bit inputs
+ * are multiplied as they are and summed in FP32, where the tensor cores' truncation may shrink a sum by 9e-5 of itself over the
+ * longest k and by 2e-8 over the shortest.  y and z are rounded once, at the end.
  * An infinite or NaN input makes outputs of its row (of x) or column (of weight) NaN or infinite, and no others; through
  * an activation z = -inf gives NaN.  Errors: EMP_ERR_ARG, EMP_ERR_UNSUPPORTED,
  * EMP_ERR_WORKSPACE (ws_bytes below mp_dense_workspace_bytes(a); 0 for many shapes and for zero rows). */
@@ -398,7 +399,8 @@ typedef struct {
 
 /* Gradient of mp_dense:  gz = g activation'(z),  g_x = gz W,  g_weight = gz^T x,  g_bias = sum gz.
  * For 16-bit types gz is rounded to dtype as an operand of the two products (g_bias sums it
- * unrounded).  Sums over rows in FP32 in a fixed order.  Zero rows: g_weight and g_bias are zeroed. */
+ * unrounded).  Non-finite, very large and very small FP32 values are as in mp_dense's products on the
+ * tensor cores.  Sums over rows in FP32 in a fixed order.  Zero rows: g_weight and g_bias are zeroed. */
 size_t mp_dense_grad_workspace_bytes(const emp_dense_grad* a);
 int mp_dense_grad(const emp_dense_grad* a, void* ws, size_t ws_bytes, cudaStream_t stream);
 

@@ -162,3 +162,57 @@ def test_scales_of_many_splits(rows, K, N, out):
         ref = orow.activation(z, act)
         dz = (2.0 ** -20 + 2 * (K / 32 + 200) * U) * host(X.abs() @ W.abs().t()) + 8 * U * np.abs(z)    # an MMA sums 32 of k
         near(y, ref, half_step(t) * np.abs(ref) + 1.13 * dz + 16 * U * (np.abs(z) + np.abs(ref)) + floor_of(t), act)
+
+
+# ------------------------------------------------------------------ infinite inputs, and values that become infinite
+@pytest.mark.parametrize("rows,K,N", [(1, 64, 40), (8, 256, 100), (1, 4096, 40), (8, 2500, 100), (16, 2048, 2100), (40, 96, 33)])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan"), 3.4028e38])
+def test_fp32_non_finite_inputs_of_few_rows(rows, K, N, value):
+    """On SIMT and on the tensor cores: no other row or column changes, and a row of an infinite or NaN input has no
+    finite output.  (3.4028e38 counts as infinite on the tensor cores alone: its outputs are right where they are finite.)"""
+    rng = np.random.default_rng(rows + K)
+    t = torch.float32
+    x, w = dev(normal(rng, rows, K), t), dev(1 + 0.1 * normal(rng, N, K), t)
+    clean = emp.mp_dense(x, w)
+    xb = x.clone()
+    xb[rows - 1, K // 2] = value
+    bad = emp.mp_dense(xb, w)
+    assert torch.equal(bad[:-1], clean[:-1])
+    last = bad[-1].double()
+    if np.isfinite(value):
+        ref = xb[-1].double() @ w.double().t()
+        ok = torch.isfinite(last)
+        assert ((last - ref).abs() <= 1e-5 * ref.abs())[ok].all()
+    else:
+        assert not torch.isfinite(last).any()
+    wb = w.clone()
+    wb[N // 2, 1] = value
+    bad = emp.mp_dense(x, wb)
+    keep = torch.arange(N, device="cuda") != N // 2
+    assert torch.equal(bad[:, keep], clean[:, keep])
+    if not np.isfinite(value):
+        assert not torch.isfinite(bad[:, N // 2]).any()
+
+
+@pytest.mark.parametrize("rows,K,N", [(1, 64, 40), (8, 70, 33), (300, 64, 96)])
+def test_fp32_gradient_of_non_finite_inputs(rows, K, N):
+    rng = np.random.default_rng(rows + N)
+    t = torch.float32
+    x, w, g = dev(1 + 0.1 * normal(rng, rows, K), t), dev(1 + 0.1 * normal(rng, N, K), t), dev(normal(rng, rows, N), t)
+    g_x, g_w, g_b = emp.mp_dense_grad(g, x, w)
+    gb = g.clone()
+    gb[rows - 1, N - 1] = float("inf")
+    b_x, b_w, b_b = emp.mp_dense_grad(gb, x, w)
+    assert torch.equal(b_x[:-1], g_x[:-1]) and not torch.isfinite(b_x[-1]).any()
+    assert torch.equal(b_w[:-1], g_w[:-1]) and not torch.isfinite(b_w[-1]).any()
+    assert torch.equal(b_b[:-1], g_b[:-1]) and torch.isinf(b_b[-1])
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -60, 2.0 ** -110])
+@pytest.mark.parametrize("rows,K,N", [(8, 256, 100), (300, 64, 96), (300, 500, 96)])
+def test_fp32_of_small_magnitudes(rows, K, N, scale):
+    rng = np.random.default_rng(rows + K)
+    t = torch.float32
+    x, w = dev(normal(rng, rows, K) * scale, t), dev(normal(rng, N, K) * 2.0 ** 20, t)
+    y, _, ty, _ = dense_tol(host(x), host(w), None, None, "none", t, K)
+    near(emp.mp_dense(x, w), y, ty, "y")
