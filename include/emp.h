@@ -399,7 +399,8 @@ typedef struct {
 
 /* Gradient of mp_dense:  gz = g activation'(z),  g_x = gz W,  g_weight = gz^T x,  g_bias = sum gz.
  * For 16-bit types gz is rounded to dtype as an operand of the two products (g_bias sums it
- * unrounded).  Non-finite, very large and very small FP32 values are as in mp_dense's products on the
+ * unrounded): in EMP_F16 a |gz| above 65504 (with an activation, whose slope reaches 1.13, |g| from 57,900 on) is infinite
+ * there, and one below 2^-25 is zero.  Non-finite, very large and very small FP32 values are as in mp_dense's products on the
  * tensor cores.  Sums over rows in FP32 in a fixed order.  Zero rows: g_weight and g_bias are zeroed. */
 size_t mp_dense_grad_workspace_bytes(const emp_dense_grad* a);
 int mp_dense_grad(const emp_dense_grad* a, void* ws, size_t ws_bytes, cudaStream_t stream);

@@ -216,3 +216,25 @@ def test_fp32_of_small_magnitudes(rows, K, N, scale):
     x, w = dev(normal(rng, rows, K) * scale, t), dev(normal(rng, N, K) * 2.0 ** 20, t)
     y, _, ty, _ = dense_tol(host(x), host(w), None, None, "none", t, K)
     near(emp.mp_dense(x, w), y, ty, "y")
+
+
+@pytest.mark.parametrize("act,z0", [("silu", 2.4), ("gelu", 1.4142)])
+def test_fp16_gradient_whose_product_with_the_slope_leaves_the_type(act, z0):
+    """|g act'(z)| above 65504 is infinite as an operand in fp16: its row of g_x and its column's g_weight show it, no others do;
+    below that, and in bf16, they are finite."""
+    rng = np.random.default_rng(29)
+    rows, K, N = 150, 64, 48
+    for t, top, finite in ((torch.float16, 60000.0, False), (torch.float16, 57000.0, True), (torch.bfloat16, 60000.0, True)):
+        x, w = dev(normal(rng, rows, K) / 64, t), dev(normal(rng, N, K) / 64, t)
+        z, g = dev(normal(rng, rows, N), t), dev(normal(rng, rows, N), t)
+        clean = emp.mp_dense_grad(g, x, w, z=z, activation=act)
+        zb, gb = z.clone(), g.clone()
+        zb[7, 5], gb[7, 5] = z0, top
+        g_x, g_w, _ = emp.mp_dense_grad(gb, x, w, z=zb, activation=act)
+        rest = torch.arange(rows, device="cuda") != 7
+        cols = torch.arange(N, device="cuda") != 5
+        assert torch.equal(g_x[rest], clean[0][rest])
+        assert torch.isfinite(g_w[cols]).all()
+        assert torch.isfinite(g_x[7]).all() == finite and torch.isfinite(g_w[5]).all() == finite
+        if not finite:
+            assert not torch.isfinite(g_x[7]).any() and not torch.isfinite(g_w[5]).any()
