@@ -898,12 +898,13 @@ inline int launch(long long M, int N, long long K, int t, const Operand& a, cons
   const bool one_chunk = split && h.splits == 1 && h.nk <= CHUNK_STAGES && h.ntiles <= tc::num_sms();
   // rows of y, z and residual in boxes of 32 rows
   const int cols = split && !one_chunk ? Cfg<SPLIT, float, true, false>::W : 32;
-  const int ys = dtype_size(e.y_dtype), one = (N * ys + 15) / 16 * 16 / ys;       // a single row: any pitch will do
-  auto fits = [&](const void* q, long long ld) { return !q || tma_ok(q, M == 1 ? one : ld, e.y_dtype); };
-  const bool rows = !part && fits(e.y, e.ldy) && fits(e.z, e.ldz) && fits(e.residual, e.ldr);
+  // A TMA store fills its last 16 bytes of a row with zeros where the tensor ends inside them, so rows have to be whole 16 bytes.
+  const int ys = dtype_size(e.y_dtype);
+  auto fits = [&](const void* q, long long ld) { return !q || tma_ok(q, M == 1 ? N : ld, e.y_dtype); };      // (one row: any pitch)
+  const bool rows = !part && N * ys % 16 == 0 && fits(e.y, e.ldy) && fits(e.z, e.ldz) && fits(e.residual, e.ldr);
   if (rows) {
     auto map = [&](CUtensorMap* m, const void* q, long long ld) {
-      return !q || make_map(m, q, e.y_dtype, N, M, M == 1 ? one : ld, cols, 32, cols * ys);
+      return !q || make_map(m, q, e.y_dtype, N, M, M == 1 ? N : ld, cols, 32, cols * ys);
     };
     if (!map(&maps.y, e.y, e.ldy) || !map(&maps.z, e.z, e.ldz) || !map(&maps.res, e.residual, e.ldr)) return EMP_ERR_CUDA;
   }

@@ -1,5 +1,7 @@
 """The row-wise operators over the rest of their range, against the float64 oracle: forms that take several tiles per
 block, values at the ends of the types, long sums.  Tolerances as derived in test_gpu_rows.py where nothing else is said."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -238,3 +240,56 @@ def test_fp16_gradient_whose_product_with_the_slope_leaves_the_type(act, z0):
         assert torch.isfinite(g_x[7]).all() == finite and torch.isfinite(g_w[5]).all() == finite
         if not finite:
             assert not torch.isfinite(g_x[7]).any() and not torch.isfinite(g_w[5]).any()
+
+
+# ------------------------------------------------------------------ what lies beside an output
+def framed(rows, cols, pitch, t):
+    """A buffer of sentinels and the view of rows inside it, both of whose ends it goes beyond by 64 elements."""
+    full = torch.full((rows * pitch + 128,), -77.0, dtype=t, device="cuda")
+    return full, torch.as_strided(full, (rows, cols), (pitch, 1), 64)
+
+
+def only_inside(full, inner):
+    got = inner.clone()
+    inner.fill_(-77.0)
+    assert torch.all(full == -77.0)
+    return got
+
+
+@pytest.mark.parametrize("type", list(TYPES))
+@pytest.mark.parametrize("rows,K,N", [(1, 2500, 1), (1, 2500, 37), (40, 96, 1), (40, 96, 13), (40, 200, 37), (300, 64, 61), (300, 500, 7)])
+def test_aligned_pitches_of_odd_widths(rows, K, N, type):
+    """Rows of y, z and g_x that begin on 16 bytes and end inside them, single rows, and weight gradients of such a width: the
+    bytes behind a row's last element and behind the last row stay."""
+    t, rng = TYPES[type], np.random.default_rng(rows + K + N)
+    code, L, st = {"f32": 0, "bf16": 1, "f16": 2}[type], emp.lib(), torch.cuda.current_stream().cuda_stream
+    x, w, b = dev(normal(rng, rows, K), t), dev(normal(rng, N, K) / np.sqrt(K), t), dev(normal(rng, N), t)
+    pitch = -(-N // 16) * 16 + 16
+    r = framed(rows, N, pitch, t)[1]
+    r.copy_(dev(normal(rng, rows, N), t))
+    (yf, y), (zf, z) = framed(rows, N, pitch, t), framed(rows, N, pitch, t)
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    a = emp.DenseC(rows, K, N, code, code, 1, x.data_ptr(), K, None, w.data_ptr(), K, None, b.data_ptr(), r.data_ptr(), pitch, y.data_ptr(),
+                   pitch, z.data_ptr(), pitch)
+    assert L.mp_dense(ctypes.byref(a), ws.data_ptr(), ws.numel(), st) == 0
+    ry, rz, ty, tz = dense_tol(host(x), host(w), host(b), host(r), "silu", t, K)
+    near(only_inside(yf, y), ry, ty, "y")
+    near(only_inside(zf, z), rz, tz, "z")
+    # the other way about: g_x of width N from N columns of a weight, its gradient [K][N] and a bias gradient of K
+    g, v, xn = dev(normal(rng, rows, K), t), dev(normal(rng, K, N) / np.sqrt(K), t), dev(normal(rng, rows, N), t)
+    (xf, gx), (wf, gw), (bf, gb) = framed(rows, N, pitch, t), framed(K, N, N, t), framed(1, K, K, t)
+    d = emp.DenseGradC(rows, N, K, code, 0, g.data_ptr(), K, None, 0, xn.data_ptr(), N, v.data_ptr(), N, gx.data_ptr(), pitch, gw.data_ptr(),
+                       gb.data_ptr())
+    assert L.mp_dense_grad(ctypes.byref(d), ws.data_ptr(), ws.numel(), st) == 0
+    rx, rw, rb = orow.dense_grad(host(g), host(xn), host(v))
+    tol = lambda ref, S, n: half_step(t) * np.abs(ref) + (2.0 ** -20 + 2 * (n + 8) * U) * S + floor_of(t)  # noqa: E731
+    G = np.abs(host(g))
+    near(only_inside(xf, gx), rx, tol(rx, G @ np.abs(host(v)), K), "g_x")
+    near(only_inside(wf, gw), rw, tol(rw, G.T @ np.abs(host(xn)), rows), "g_w")
+    near(only_inside(bf, gb), rb[None], tol(rb, G.sum(0), rows)[None], "g_b")
+    # one output, whose weight gradient is a single row of K
+    g1, (of, o) = dev(normal(rng, rows, 1), t), framed(1, K - 3, K - 3, t)
+    d = emp.DenseGradC(rows, K - 3, 1, code, 0, g1.data_ptr(), 1, None, 0, x.data_ptr(), K, None, 0, None, 0, o.data_ptr(), None)
+    assert L.mp_dense_grad(ctypes.byref(d), ws.data_ptr(), ws.numel(), st) == 0
+    X = host(x)[:, :K - 3]
+    near(only_inside(of, o), host(g1).T @ X, tol(host(g1).T @ X, np.abs(host(g1)).T @ np.abs(X), rows), "g_w of one output")
