@@ -1006,8 +1006,13 @@ cudaError_t launch_fwd(const Args& args, bool quant, cudaStream_t st) {
 template <typename T, int V, int SL>
 void launch_grad2(const GradArgs& a, const Shape& h, int blocks, cudaStream_t st) {
   const int smem = h.R > 1 || a.degrees ? a.cols * 4 : 0;
-  if (h.G * h.R <= 256) k_rms_norm_grad<T, V, SL, 256><<<blocks, dim3(h.G, h.R), smem, st>>>(a);
-  else k_rms_norm_grad<T, V, SL, MAX_THREADS><<<blocks, dim3(h.G, h.R), smem, st>>>(a);
+  if constexpr (SL < 4) {                // rows of four vectors a thread are above 4096 columns, which takes 288 threads at least
+    if (h.G * h.R <= 256) {
+      k_rms_norm_grad<T, V, SL, 256><<<blocks, dim3(h.G, h.R), smem, st>>>(a);
+      return;
+    }
+  }
+  k_rms_norm_grad<T, V, SL, MAX_THREADS><<<blocks, dim3(h.G, h.R), smem, st>>>(a);
 }
 template <typename T, int NS>
 int launch_grad_odd3(const GradArgs& a, int smem, cudaStream_t st) {

@@ -14,7 +14,6 @@ __host__ __device__ constexpr int dtype_size(int t) { return t == EMP_F32 ? 4 : 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f(__nv_fp8_e4m3 v) { return (float)v; }
 template <typename T> __device__ __forceinline__ T from_f(float v);
 template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
@@ -123,13 +122,12 @@ __device__ __forceinline__ void store_e4m3(__nv_fp8_storage_t* p, const float (&
   }
 }
 
-// one element of a buffer whose type is known at run time only (edges, small operands)
+// one element of a buffer whose type, FP32, bf16 or fp16, is known at run time only (edges, small operands)
 __device__ __forceinline__ float load_any(const void* p, size_t i, int t) {
   switch (t) {
     case EMP_F32: return static_cast<const float*>(p)[i];
     case EMP_BF16: return to_f(static_cast<const __nv_bfloat16*>(p)[i]);
-    case EMP_F16: return to_f(static_cast<const __half*>(p)[i]);
-    default: return to_f(static_cast<const __nv_fp8_e4m3*>(p)[i]);
+    default: return to_f(static_cast<const __half*>(p)[i]);
   }
 }
 __device__ __forceinline__ void store_any(void* p, size_t i, int t, float v) {
