@@ -13,8 +13,9 @@
 // bf16, fp16 and e4m3 operands go from TMA straight to the MMA: a ring of stages of 128 bytes of k
 // (128-byte swizzle), two accumulators of bn columns, so the epilogue of a tile overlaps the next
 // tile's products.  Bound by shared memory, which takes every operand byte in and gives it out once: 16384 x 2048 -> 2048 in bf16
-// 98 us, 1400 TFLOP/s (85 % of the measured rate; the tensor pipe is active 70 % of the time); 65536 x 2048 -> 512 in e4m3 with SiLU
-// and residual 77 us, 1790 TFLOP/s, with half of its time per tile in the epilogue's exchange with memory.
+// 98 us, 1400 TFLOP/s (85 % of the measured rate; 106 us on rotating inputs; the tensor pipe is active 70 % of the time); 65536 x 2048
+// -> 512 in e4m3 with SiLU and residual 94 us among other calls, 1460 TFLOP/s (the kernel alone 75), with half of its time per tile
+// in the epilogue's exchange with memory.
 //
 // FP32 operands are split a = hi + lo (hi = RN_tf32(a), lo = RN_tf32(a - hi)) inside the kernel, by two
 // groups of four warps that take the 32-wide k stages in turn, so neither operand needs a pass of its
@@ -25,12 +26,12 @@
 // to nearest, to sums in the epilogue warps' registers, and within each stage the small products
 // lo.hi and hi.lo come before hi.hi.  Bound by the split (16 instructions per 4 elements and lane) and the epilogue's
 // additions: 161792 x 512 -> 512 takes 408 us, 208 TFLOP/s of products (two thirds of what three TF32 products
-// allow).
+// allow), 429 us on rotating inputs.  Spills 12 bytes with TMA rows, 112 without.
 //
 // FP32 with k of one chunk (SHORT) needs no sums in registers.  A CTA stays on one column of tiles, so that B is split
 // once and kept, and the two halves of the epilogue's warps take every other tile each: a warp's way through a
-// tile is latency (TMEM, staging, the store's read) as much as instructions (647168 x 64 -> 512 with SiLU 340 us
-// with all warps on each tile, 322 us, 4.6 TB/s, thus; 16-bit operands, whose epilogue overlaps more stages, gain nothing
+// tile is latency (TMEM, staging, the store's read) as much as instructions (647168 x 64 -> 512 with SiLU on one buffer 340 us
+// with all warps on each tile, 322 us thus; among other calls 389 us, 3.8 TB/s; 16-bit operands, whose epilogue overlaps more stages, gain nothing
 // and 8-bit ones lose: 77 and 87 us at 65536 x 2048 -> 512).  Bound by the instructions of split and epilogue together.
 //
 // Every mbarrier wait is bounded; the producer waits out its own copies before exit.
