@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(Cfg<PATH, T, ROWS, SCALED>::THREADS, 1)
     auto put = [&](const Item& t, int c, float (&v)[32], const Item& tn, int next) {
       const long long m0 = t.m0 + q * 32;
       const int n0 = t.n0 + c * 32;
-      if (!here(t, c)) return;
+      if (!ok || !here(t, c)) return;                        // (after a wait that ran out no further load is asked for)
       if constexpr (!ROWS) {
         float* stg = reinterpret_cast<float*>(place);
         stage_rows(v, stg, lane);
