@@ -293,3 +293,16 @@ def test_aligned_pitches_of_odd_widths(rows, K, N, type):
     assert L.mp_dense_grad(ctypes.byref(d), ws.data_ptr(), ws.numel(), st) == 0
     X = host(x)[:, :K - 3]
     near(only_inside(of, o), host(g1).T @ X, tol(host(g1).T @ X, np.abs(host(g1)).T @ np.abs(X), rows), "g_w of one output")
+
+
+@pytest.mark.parametrize("rows,K,N", [(5, 64, 40), (16, 2100, 33), (200, 128, 96), (300, 100, 61)])
+def test_nan_of_8_bits_stays_in_its_row_and_column(rows, K, N):
+    rng = np.random.default_rng(rows)
+    (x, xs), (w, ws) = to_e4m3(normal(rng, rows, K)), to_e4m3(normal(rng, N, K))
+    call = lambda a, b, c, d: emp.mp_dense(a, b, x_scale=c, w_scale=d, out_dtype=torch.float16)  # noqa: E731
+    clean = call(x, w, xs, ws)
+    xb, wb, sb = x.clone(), w.clone(), xs.clone()
+    xb.view(torch.uint8)[1, 3], wb.view(torch.uint8)[N - 1, 0], sb[0] = 0x7f, 0xff, float("nan")
+    bad = call(xb, wb, sb, ws)
+    assert torch.isnan(bad[:2]).all() and torch.isnan(bad[:, -1]).all()
+    assert torch.equal(bad[2:, :-1], clean[2:, :-1])
